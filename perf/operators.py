@@ -226,8 +226,8 @@ def _handles(s):
     h = dict(layer=lc, batch=batch)
     if c["op"] == "window":
         h["out"] = torch.empty((s["T"], c["hq"], c["dim"]), dtype=torch.bfloat16, device="cuda")
-        h["splits"] = pkv.pkv_window_splits(lc.desc, batch, c["window"], c["sinks"])
-        n = pkv.pkv_window_ws_bytes(lc.desc, batch, h["splits"])
+        h["split"] = pkv.pkv_window_split_tokens(lc.desc, batch, c["window"], c["sinks"])
+        n = pkv.pkv_window_ws_bytes(lc.desc, batch, c["window"], c["sinks"], h["split"])
         h["ws"] = torch.zeros(n, dtype=torch.uint8, device="cuda") if n else None
     if c["op"] == "rope":
         h["rope"] = pkv.make_rope(s["inv_freq"], interleaved=c["interleaved"], scale=s["factor"], positions=s["positions"])
@@ -249,7 +249,7 @@ def run(s):
         desc, batch = s["layer"].desc, s["batch"]
         if c["op"] == "window":
             pkv.pkv_window_attention(desc, batch, s["q"], s["out"], c["window"], c["sinks"], c["dim"] ** -0.5,
-                                     s["splits"], s["ws"])
+                                     s["split"], s["ws"])
             return s["out"]
         if c["op"] == "rope":
             pkv.pkv_rope_append(desc, batch, s["rope"], s["q"], s["k"], s["v"], s["out"])
