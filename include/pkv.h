@@ -61,6 +61,7 @@ extern "C" {
 #define PKV_DEVERR_CTX_LEN     4  /* context length < 0 or > max_blocks * block_size */
 #define PKV_DEVERR_OFFSET      8  /* in-block offset < 0 or >= block_size */
 #define PKV_DEVERR_TIMEOUT    16  /* a bounded wait on an asynchronous copy expired */
+#define PKV_DEVERR_BATCH      32  /* token_starts descend, pass num_tokens or give a sequence more than max_tokens */
 
 #define PKV_DTYPE_BF16 0
 #define PKV_DTYPE_INT8 1
@@ -317,6 +318,129 @@ int pkv_splitk_reduce(const float* ws_o, const float* ws_ml, const int32_t* ctx_
 
 size_t pkv_splitk_ws_o_bytes(int32_t B, int32_t Hq, int32_t head_dim, int32_t max_splits);
 size_t pkv_splitk_ws_ml_bytes(int32_t B, int32_t Hq, int32_t max_splits);
+
+/* ======================================================================== */
+/* Chunks: any number of new tokens a sequence                             */
+/* ======================================================================== */
+
+/* A batch of B sequences, sequence b bringing n_b = token_starts[b+1] -
+ * token_starts[b] >= 0 new tokens -- one in a decode step, a few drafted ones,
+ * a chunk of a prompt or a whole prompt. Row token_starts[b] + i of the token
+ * arrays (q, k, v, out) is token ctx_lens[b] - n_b + i of the sequence, whose
+ * context holds ctx_lens[b] tokens, the new ones included. The blocks for
+ * them must be in its table. One descriptor serves every layer and the three
+ * operators below.
+ *
+ * token_starts (ascending), block_tables, ctx_lens and slots (INT8; NULL in
+ * BF16 mode) are device arrays; num_tokens is the number of rows of the token
+ * arrays and max_tokens the most rows of one sequence. Rows at
+ * token_starts[B] and behind are left as they were. In the kernels, a
+ * sequence whose rows are not inside [0, num_tokens] or are more than
+ * max_tokens is left out (PKV_DEVERR_BATCH); one with ctx_lens[b] < n_b or
+ * > max_blocks * block_size writes nothing to the cache (PKV_DEVERR_CTX_LEN).
+ * A slot or a block that a call writes belongs to one sequence of its batch.
+ * B == 0 or num_tokens == 0 is a no-op. B <= 65535; max_blocks * block_size
+ * < 2^31 - 2^16. */
+typedef struct pkv_batch_desc {
+    const int32_t* token_starts;  /* [B + 1] */
+    const int32_t* block_tables;  /* [B][max_blocks] */
+    const int32_t* ctx_lens;      /* [B] */
+    const int32_t* slots;         /* [B] */
+    int32_t B;
+    int32_t max_blocks;
+    int32_t num_tokens;
+    int32_t max_tokens;
+} pkv_batch_desc;
+
+/* Rotary positions: the first rotary_dim elements of a head (a multiple of
+ * 16, 0 .. head_dim) turn in pairs, pair j by the angle position * inv_freq[j]
+ * -- (2j, 2j+1) if interleaved, else (j, j + rotary_dim/2):
+ *   x' = scale * (x cos a - y sin a),  y' = scale * (y cos a + x sin a).
+ * inv_freq is fp64 (radians a position, device, rotary_dim/2 entries): scaled
+ * frequencies for long contexts are other entries, their attention factor is
+ * `scale` (1 for none). The angle is reduced to a fraction of a turn in 64-bit
+ * integers, so it is as exact at any position as at the first ones.
+ * positions (nullable, device [num_tokens]) gives each row's rotary position;
+ * NULL: its token's index in the context. */
+typedef struct pkv_rope {
+    const double*  inv_freq;
+    const int32_t* positions;
+    int32_t rotary_dim;
+    int32_t interleaved;
+    float   scale;
+} pkv_rope;
+
+/* The rotary turn of the new tokens' q and k and the write of k and v into
+ * the cache, in one kernel. q [num_tokens][Hq][d] -> q_out; k, v
+ * [num_tokens][Hkv][d] bf16, whose token strides are q_stride, k_stride,
+ * v_stride and q_out_stride elements (multiples of 8, so that the parts of
+ * one projection's output can be passed as they lie; all pointers 16-byte
+ * aligned). q_out may be q itself with the same stride; otherwise they must
+ * not overlap. q NULL: no queries (q_out unused). rope NULL (or rotary_dim
+ * 0): nothing turns -- q is copied, k is written as given.
+ *
+ * The turned k is rounded to bf16 once. BF16 mode: rows into their blocks of
+ * the pool. INT8 mode: as appending the rows one by one and quantizing every
+ * block that fills (pkv_append_kv + pkv_quantize_full_blocks) would leave
+ * pool, scales and the slot's tail -- a block begun by earlier tokens takes
+ * their rows from the tail, the last, partly filled block ends up there --
+ * except that tail rows are written only for tokens of that last block.
+ *
+ * With programmatic launch on and max_tokens > 1, the call also launches an
+ * empty kernel behind itself, so that the early reads of a decode kernel
+ * launched next (see pkv_set_programmatic_launch) find the blocks written. */
+int pkv_rope_append(const pkv_cache_desc* c, const pkv_batch_desc* batch, const pkv_rope* rope,
+                    const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                    const void* v, int64_t v_stride, void* q_out, int64_t q_out_stride, void* stream);
+
+/* Attention of the new tokens over the cache that already holds them: query
+ * row i of sequence b, at position p = ctx_lens[b] - n_b + i, sees the tokens
+ *   t <= p  and  (p - t < window  or  t < sinks)
+ * -- causal, the last `window` tokens (itself included) and the first `sinks`
+ * ones, as models with attention sinks want them; window 0: every token up to
+ * p (sinks then means nothing). For each of them and query head h
+ *   out[row][h] = sum_t softmax_t(sm_scale * q[row][h] . k_t) v_t
+ * with K and V read as pkv_decode_attention reads them (INT8 dequantized, the
+ * partly filled last block from the slot's tail). q, out: [num_tokens][Hq][d]
+ * bf16 with token strides of q_stride, out_stride elements (multiples of 8;
+ * both 16-byte aligned). fp32 accumulation. Rows of a sequence with a bad
+ * context length are zero; a token whose block id or slot is bad counts as
+ * not visible, and a row that sees nothing is zero.
+ *
+ * Blocks before the window (and behind the sinks) are neither read nor looked
+ * up: their table entries may be -1 and their memory in use elsewhere. Rows
+ * of a block behind the context, and tokens no row of the call sees, may hold
+ * anything. A visible token's K and V must be finite: a NaN or infinity in V
+ * may reach every row of its sequence in the call.
+ *
+ * split_tokens > 0 (a multiple of 16; pkv_window_split_tokens gives one that
+ * fills the GPU, 0 where none is needed) cuts the visible tokens into splits
+ * of about that length, merged by the last of them to finish; ws is then
+ * pkv_window_ws_bytes(...) bytes of device memory, 256-byte aligned, zeroed
+ * before its first use and left ready for the next call (with any arguments
+ * that need no more bytes). Calls sharing a workspace must not overlap. The
+ * splits depend on the lengths alone: the same call gives the same bits. */
+int pkv_window_attention(const pkv_cache_desc* c, const pkv_batch_desc* batch, const void* q, int64_t q_stride,
+                         int32_t window, int32_t sinks, float sm_scale, int32_t split_tokens, void* ws,
+                         size_t ws_bytes, void* out, int64_t out_stride, void* stream);
+int pkv_window_split_tokens(const pkv_cache_desc* c, const pkv_batch_desc* batch, int32_t window, int32_t sinks);
+size_t pkv_window_ws_bytes(const pkv_cache_desc* c, const pkv_batch_desc* batch, int32_t window, int32_t sinks,
+                           int32_t split_tokens);
+
+/* Rows of the cache read back in token order, dequantized: row
+ * token_starts[b] + i of k_out, v_out ([num_tokens][Hkv][d], token stride
+ * out_stride elements, a multiple of 8 (BF16) or 4 (FP32)) is token
+ * first[b] + i of sequence b, or token ctx_lens[b] - n_b + i where first is
+ * NULL (with n_b = ctx_lens[b]: the whole context; with the batch of a chunk:
+ * the rows that it wrote). out_dtype PKV_OUT_BF16 (an INT8 value, code *
+ * scale in fp32, is rounded to bf16) or PKV_OUT_FP32 (not rounded again). In
+ * INT8 mode the last ctx_lens[b] % block_size tokens come from the tail. A
+ * range outside [0, ctx_lens[b]] leaves the sequence's rows as they were
+ * (PKV_DEVERR_CTX_LEN); a bad block id or slot its tokens' rows. */
+#define PKV_OUT_BF16 0
+#define PKV_OUT_FP32 1
+int pkv_gather_kv(const pkv_cache_desc* c, const pkv_batch_desc* batch, const int32_t* first,
+                  void* k_out, void* v_out, int64_t out_stride, int32_t out_dtype, void* stream);
 
 /* Reads, clears and reports the error words of n descriptors once the work
  * queued on `stream` has finished: synchronises the stream, copies each

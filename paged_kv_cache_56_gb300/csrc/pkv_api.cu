@@ -18,6 +18,7 @@
 
 #include "../../include/pkv.h"
 #include "decode_registry.h"
+#include "host.h"
 
 namespace pkv {
 
@@ -119,9 +120,7 @@ __global__ void __launch_bounds__(128) quantize_kernel(const uint16_t* __restric
 // ---------------------------------------------------------------------------
 // Host helpers
 // ---------------------------------------------------------------------------
-static inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-static int check_desc(const pkv_cache_desc* c) {
+int check_desc(const pkv_cache_desc* c) {
     if (!c || !c->k_pool || !c->v_pool) return PKV_ERR_INVALID;
     if (!aligned16(c->k_pool) || !aligned16(c->v_pool)) return PKV_ERR_INVALID;
     if (c->num_blocks <= 0 || c->num_q_heads <= 0 || c->num_kv_heads <= 0) return PKV_ERR_INVALID;
@@ -141,9 +140,7 @@ static int check_desc(const pkv_cache_desc* c) {
     return PKV_OK;
 }
 
-static inline int cuda_status(cudaError_t e) { return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA; }
-
-static std::atomic<int> g_pdl{0};
+std::atomic<int> g_pdl{0};
 static std::atomic<int> g_skip_copy{-1};
 
 // Copies whole slabs src[i] -> dst[i] for up to three arrays at once (slab
@@ -177,25 +174,6 @@ __global__ void __launch_bounds__(256) copy_slabs_kernel(const int32_t* __restri
         uint2* to = reinterpret_cast<uint2*>(a2 + size_t(d) * bytes2);
         for (size_t c = threadIdx.x; c < bytes2 / 8; c += blockDim.x) to[c] = from[c];
     }
-}
-
-// Launches with the programmatic-stream-serialization attribute when enabled
-// (pkv_set_programmatic_launch), plainly otherwise.
-template <typename... Params, typename... Args>
-static int launch(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, Args&&... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = block;
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    if (g_pdl.load(std::memory_order_relaxed)) {
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-    }
-    return cuda_status(cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...));
 }
 
 // The decode instantiation for a shape, and a small index for per-kernel state.
@@ -233,7 +211,7 @@ static int allow_smem(DecodeFn fn, int index, size_t smem) {
 
 // cuTensorMapEncodeTiled, looked up once through the runtime's driver entry
 // point (no link against the driver library); nullptr if unavailable.
-static PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
     static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
         void* f = nullptr;
         cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
@@ -250,7 +228,7 @@ static PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 // [num_blocks][rows = Hkv * bs][row_bytes], boxes of 16 rows x 128 bytes,
 // 128-byte swizzle. Encoding is host-only work; the last map of each pool is
 // kept per thread (a small direct-mapped cache keyed by the pool's shape).
-static int pool_tensor_map(const void* pool, int32_t num_blocks, int32_t rows, int32_t row_bytes, CUtensorMap* out) {
+int pool_tensor_map(const void* pool, int32_t num_blocks, int32_t rows, int32_t row_bytes, CUtensorMap* out) {
     struct Entry {
         CUtensorMap map;
         const void* pool;

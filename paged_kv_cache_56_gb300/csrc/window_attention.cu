@@ -1,0 +1,220 @@
+// Entry points of the windowed attention: argument checks, the choice of the
+// kernel and of the split, and the launch.
+#include <algorithm>
+#include <cstring>
+#include <mutex>
+
+#include "host.h"
+#include "window.cuh"
+
+namespace pkv {
+
+WindowFn window_rows_fn_d64_bf16(int nt);
+WindowFn window_rows_fn_d64_int8(int nt);
+WindowFn window_rows_fn_d128_bf16(int nt);
+WindowFn window_rows_fn_d128_int8(int nt);
+
+namespace {
+
+constexpr int kMaxSplits = 128;  // the merge holds 16 rows' weights of every split in a CTA's rings
+// Arrival counters at the front of every workspace, whatever the call, so
+// that calls of other shapes may share it: each leaves its counters at zero
+// and no call's partial results lie on another's counters. A batch of more
+// row tiles than this fills the GPU without splits and is not split.
+constexpr int kCounters = 16384;
+
+struct Plan {
+    WindowFn fn;
+    size_t smem;
+    int threads;
+    int row_tiles;    // row tiles of max_tokens tokens
+    int key_tiles;    // most 16-token tiles that one row tile sees
+    int ctas_per_sm;
+};
+
+// Raises a kernel's dynamic shared-memory limit once per kernel and device
+// and returns how many of its CTAs fit on an SM.
+int prepare_kernel(WindowFn fn, size_t smem, int threads, int* ctas) {
+    struct Entry {
+        WindowFn fn;
+        int dev;
+        int ctas;
+    };
+    static std::mutex mu;
+    static Entry seen[256];
+    static int n = 0;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return PKV_ERR_CUDA;
+    std::lock_guard<std::mutex> lock(mu);
+    for (int i = 0; i < n; ++i)
+        if (seen[i].fn == fn && seen[i].dev == dev) {
+            *ctas = seen[i].ctas;
+            return PKV_OK;
+        }
+    const void* f = reinterpret_cast<const void*>(fn);
+    if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) != cudaSuccess ||
+        cudaFuncSetAttribute(f, cudaFuncAttributePreferredSharedMemoryCarveout, int(cudaSharedmemCarveoutMaxShared)) !=
+            cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(ctas, fn, threads, smem) != cudaSuccess)
+        return PKV_ERR_CUDA;
+    if (n < 256) seen[n++] = Entry{fn, dev, *ctas};
+    return PKV_OK;
+}
+
+int sm_count(int* out) {
+    static std::atomic<int> known[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return PKV_ERR_CUDA;
+    int n = known[dev].load(std::memory_order_relaxed);
+    if (n == 0) {
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return PKV_ERR_CUDA;
+        known[dev].store(n, std::memory_order_relaxed);
+    }
+    *out = n;
+    return PKV_OK;
+}
+
+// Most 16-token tiles that `span` tokens in a row see.
+int most_key_tiles(const pkv_cache_desc* c, const pkv_batch_desc* bt, int window, int sinks, int span) {
+    const int64_t all = (int64_t(bt->max_blocks) * c->block_size + kTile - 1) / kTile;
+    if (window <= 0) return int(all);
+    const int64_t seen = (int64_t(window) + span + kTile - 2) / kTile + 1 + (int64_t(sinks) + kTile - 1) / kTile;
+    return int(std::min(all, seen));
+}
+
+int make_plan(const pkv_cache_desc* c, const pkv_batch_desc* bt, int window, int sinks, Plan* pl) {
+    const bool int8 = c->dtype == PKV_DTYPE_INT8;
+    const int g = c->num_q_heads / c->num_kv_heads;
+    const int64_t rows = int64_t(bt->max_tokens) * g;
+    const int nt = rows <= 8 ? 1 : 2;
+    if (c->head_dim == 128) pl->fn = int8 ? window_rows_fn_d128_int8(nt) : window_rows_fn_d128_bf16(nt);
+    else pl->fn = int8 ? window_rows_fn_d64_int8(nt) : window_rows_fn_d64_bf16(nt);
+    pl->smem = window_rows_smem(c->head_dim, int8);
+    pl->threads = kThreads;
+    pl->row_tiles = int((rows + 8 * nt - 1) / (8 * nt));
+    pl->key_tiles = most_key_tiles(c, bt, window, sinks, std::max(1, 8 * nt / g));
+    return prepare_kernel(pl->fn, pl->smem, pl->threads, &pl->ctas_per_sm);
+}
+
+int max_splits_of(const pkv_cache_desc* c, const pkv_batch_desc* bt, const Plan& pl, int split_tokens) {
+    if (split_tokens <= 0 || int64_t(bt->B) * c->num_kv_heads * pl.row_tiles > kCounters) return 1;
+    const int tiles = split_tokens / kTile;
+    return std::min(kMaxSplits, (pl.key_tiles + tiles - 1) / tiles);
+}
+
+struct Workspace {
+    size_t ml, o, total;
+};
+
+Workspace workspace_of(const pkv_cache_desc* c, const pkv_batch_desc* bt, const Plan& pl, int max_splits) {
+    const auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+    Workspace w;
+    w.ml = up(size_t(bt->num_tokens) * c->num_q_heads * max_splits * 8);
+    w.o = size_t(bt->num_tokens) * c->num_q_heads * max_splits * c->head_dim * 4;
+    w.total = max_splits > 1 ? size_t(kCounters) * 4 + w.ml + w.o : 0;
+    return w;
+}
+
+int check_window(const pkv_cache_desc* c, const pkv_batch_desc* batch, int window, int sinks, int split_tokens,
+                 BatchView* bt, CacheView* cv) {
+    const int st = check_batch(c, batch, bt, cv);
+    if (st != PKV_OK) return st;
+    if (window < 0 || sinks < 0 || split_tokens < 0 || split_tokens % kTile) return PKV_ERR_INVALID;
+    return PKV_OK;
+}
+
+bool is_empty(const pkv_batch_desc* b) { return b->B == 0 || b->num_tokens == 0 || b->max_tokens == 0; }
+
+}  // namespace
+
+size_t window_rows_smem(int d, bool int8) {
+    if (d == 64)
+        return int8 ? DecodeTraits<64, true>::kAlignSlack + size_t(kWarps) * DecodeTraits<64, true>::kStages * DecodeTraits<64, true>::kStageBytes
+                    : DecodeTraits<64, false>::kAlignSlack + size_t(kWarps) * DecodeTraits<64, false>::kStages * DecodeTraits<64, false>::kStageBytes;
+    return int8 ? DecodeTraits<128, true>::kAlignSlack + size_t(kWarps) * DecodeTraits<128, true>::kStages * DecodeTraits<128, true>::kStageBytes
+                : DecodeTraits<128, false>::kAlignSlack + size_t(kWarps) * DecodeTraits<128, false>::kStages * DecodeTraits<128, false>::kStageBytes;
+}
+
+}  // namespace pkv
+
+using namespace pkv;
+
+extern "C" {
+
+int pkv_window_split_tokens(const pkv_cache_desc* c, const pkv_batch_desc* batch, int32_t window, int32_t sinks) {
+    BatchView bt;
+    CacheView cv;
+    int st = check_window(c, batch, window, sinks, 0, &bt, &cv);
+    if (st != PKV_OK) return st;
+    if (is_empty(batch)) return 0;
+    Plan pl;
+    int sms = 0;
+    if ((st = make_plan(c, batch, window, sinks, &pl)) != PKV_OK || (st = sm_count(&sms)) != PKV_OK) return st;
+    const int64_t units = int64_t(batch->B) * c->num_kv_heads * pl.row_tiles;
+    const int64_t splits = int64_t(sms) * pl.ctas_per_sm / units;
+    if (splits <= 1) return 0;
+    // at least two tiles a warp: shorter splits spend their time on the start and the merge
+    const int64_t tiles = std::max<int64_t>((pl.key_tiles + splits - 1) / splits, 2 * kWarps);
+    return tiles >= pl.key_tiles ? 0 : int(tiles * kTile);
+}
+
+size_t pkv_window_ws_bytes(const pkv_cache_desc* c, const pkv_batch_desc* batch, int32_t window, int32_t sinks,
+                           int32_t split_tokens) {
+    BatchView bt;
+    CacheView cv;
+    Plan pl;
+    if (check_window(c, batch, window, sinks, split_tokens, &bt, &cv) != PKV_OK || is_empty(batch) ||
+        make_plan(c, batch, window, sinks, &pl) != PKV_OK)
+        return 0;
+    return workspace_of(c, batch, pl, max_splits_of(c, batch, pl, split_tokens)).total;
+}
+
+int pkv_window_attention(const pkv_cache_desc* c, const pkv_batch_desc* batch, const void* q, int64_t q_stride,
+                         int32_t window, int32_t sinks, float sm_scale, int32_t split_tokens, void* ws,
+                         size_t ws_bytes, void* out, int64_t out_stride, void* stream) {
+    WindowParams p;
+    int st = check_window(c, batch, window, sinks, split_tokens, &p.bt, &p.c);
+    if (st != PKV_OK) return st;
+    if (!(sm_scale == sm_scale)) return PKV_ERR_INVALID;
+    if (is_empty(batch)) return PKV_OK;
+    const int64_t row = int64_t(c->num_q_heads) * c->head_dim;
+    if (!q || !out || !aligned16(q) || !aligned16(out) || q_stride < row || out_stride < row ||
+        ((q_stride | out_stride) & 7))
+        return PKV_ERR_INVALID;
+    Plan pl;
+    if ((st = make_plan(c, batch, window, sinks, &pl)) != PKV_OK) return st;
+    const int splits = max_splits_of(c, batch, pl, split_tokens);
+    const Workspace w = workspace_of(c, batch, pl, splits);
+    if (w.total > 0 && (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < w.total)) return PKV_ERR_INVALID;
+
+    const bool int8 = c->dtype == PKV_DTYPE_INT8;
+    const int32_t row_bytes = c->head_dim * (int8 ? 1 : 2);
+    if (row_bytes >= 128) {
+        const int32_t rows = c->num_kv_heads * c->block_size;
+        if ((st = pool_tensor_map(c->k_pool, c->num_blocks, rows, row_bytes, &p.tm_k)) != PKV_OK) return st;
+        if ((st = pool_tensor_map(c->v_pool, c->num_blocks, rows, row_bytes, &p.tm_v)) != PKV_OK) return st;
+    } else {
+        std::memset(&p.tm_k, 0, sizeof(p.tm_k));
+        std::memset(&p.tm_v, 0, sizeof(p.tm_v));
+    }
+    p.q = static_cast<const uint16_t*>(q);
+    p.out = static_cast<uint16_t*>(out);
+    p.q_stride = q_stride;
+    p.out_stride = out_stride;
+    auto* bytes = static_cast<uint8_t*>(ws);
+    p.ws_count = splits > 1 ? reinterpret_cast<int32_t*>(bytes) : nullptr;
+    p.ws_ml = splits > 1 ? reinterpret_cast<float*>(bytes + kCounters * 4) : nullptr;
+    p.ws_o = splits > 1 ? reinterpret_cast<float*>(bytes + kCounters * 4 + w.ml) : nullptr;
+    p.window = window > 0 ? window : 0x7FFFFFFF;
+    p.sinks = window > 0 ? sinks : 0;
+    p.split_tiles = splits > 1 ? split_tokens / kTile : 0;
+    p.max_splits = splits;
+    p.row_tiles = pl.row_tiles;
+    p.qscale = sm_scale * 1.4426950408889634f;
+    const int64_t gx = int64_t(pl.row_tiles) * splits;
+    if (gx > 0x7FFFFFFF) return PKV_ERR_INVALID;
+    const dim3 grid(unsigned(gx), unsigned(c->num_kv_heads), unsigned(batch->B));
+    return launch(pl.fn, grid, dim3(unsigned(pl.threads)), pl.smem, static_cast<cudaStream_t>(stream), p);
+}
+
+}  // extern "C"

@@ -35,6 +35,10 @@ PKV_DEVERR_SLOT = 2
 PKV_DEVERR_CTX_LEN = 4
 PKV_DEVERR_OFFSET = 8
 PKV_DEVERR_TIMEOUT = 16
+PKV_DEVERR_BATCH = 32
+
+PKV_OUT_BF16 = 0
+PKV_OUT_FP32 = 1
 
 PKV_DTYPE_BF16 = 0
 PKV_DTYPE_INT8 = 1
@@ -52,7 +56,8 @@ EXPORTED = (
     "pkv_splitk_ws_o_bytes", "pkv_splitk_ws_ml_bytes", "pkv_decode_ctas_per_sm",
     "pkv_decode_attention_static_ws", "pkv_set_programmatic_launch", "pkv_decode_step", "pkv_decode_layers",
     "pkv_fork", "pkv_cow_block", "pkv_block_refs", "pkv_copy_blocks", "pkv_copy_slots",
-    "pkv_debug_skip_copy", "pkv_sync_status",
+    "pkv_debug_skip_copy", "pkv_sync_status", "pkv_rope_append", "pkv_window_attention",
+    "pkv_window_split_tokens", "pkv_window_ws_bytes", "pkv_gather_kv",
 )
 
 
@@ -71,6 +76,23 @@ class CacheDesc(ctypes.Structure):
         ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
         ("block_size", ctypes.c_int32), ("max_slots", ctypes.c_int32),
         ("dtype", ctypes.c_int32), ("err_word", ctypes.c_void_p),
+    ]
+
+
+class BatchDesc(ctypes.Structure):
+    """Mirror of ``pkv_batch_desc``; ``make_batch`` fills one from checked tensors."""
+    _fields_ = [
+        ("token_starts", ctypes.c_void_p), ("block_tables", ctypes.c_void_p), ("ctx_lens", ctypes.c_void_p),
+        ("slots", ctypes.c_void_p), ("B", ctypes.c_int32), ("max_blocks", ctypes.c_int32),
+        ("num_tokens", ctypes.c_int32), ("max_tokens", ctypes.c_int32),
+    ]
+
+
+class RopeDesc(ctypes.Structure):
+    """Mirror of ``pkv_rope``; ``make_rope`` fills one from checked tensors."""
+    _fields_ = [
+        ("inv_freq", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("rotary_dim", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32), ("scale", ctypes.c_float),
     ]
 
 
@@ -122,6 +144,12 @@ def lib() -> ctypes.CDLL:
             "pkv_decode_attention_static_ws": (ctypes.c_int, [ctypes.POINTER(CacheDesc), _VP, _VP, _I32, _VP, _VP,
                                                               _I32, ctypes.c_float, _I32, _I32, _VP, _VP]),
             "pkv_splitk_reduce": (ctypes.c_int, [_VP, _VP, _VP, _I32, _I32, _I32, _I32, _I32, _VP, _VP]),
+            "pkv_rope_append": (ctypes.c_int, [_VP, _VP, _VP, _VP, _I64, _VP, _I64, _VP, _I64, _VP, _I64, _VP]),
+            "pkv_window_attention": (ctypes.c_int, [_VP, _VP, _VP, _I64, _I32, _I32, ctypes.c_float, _I32, _VP,
+                                                    ctypes.c_size_t, _VP, _I64, _VP]),
+            "pkv_window_split_tokens": (ctypes.c_int, [_VP, _VP, _I32, _I32]),
+            "pkv_window_ws_bytes": (ctypes.c_size_t, [_VP, _VP, _I32, _I32, _I32]),
+            "pkv_gather_kv": (ctypes.c_int, [_VP, _VP, _VP, _VP, _VP, _I64, _I32, _VP]),
             "pkv_splitk_ws_o_bytes": (ctypes.c_size_t, [_I32, _I32, _I32, _I32]),
             "pkv_splitk_ws_ml_bytes": (ctypes.c_size_t, [_I32, _I32, _I32]),
         }
@@ -480,6 +508,121 @@ def pkv_decode_attention_static_ws(desc: CacheDesc, q: torch.Tensor, block_table
     _check("pkv_decode_attention_static_ws",
            lib().pkv_decode_attention_static_ws(_desc_ptr(desc), qp, tp, max_blocks, cp, sp, B, float(sm_scale),
                                                 split_tokens, max_splits, outp, _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# Chunks: any number of new tokens a sequence
+# ---------------------------------------------------------------------------
+
+def make_batch(token_starts: torch.Tensor, block_tables: torch.Tensor, ctx_lens: torch.Tensor, slots=None, *,
+               num_tokens: int, max_tokens: int) -> BatchDesc:
+    """Batch descriptor of the chunk operators (``pkv_batch_desc``): token_starts
+    [B+1], block_tables [B, max_blocks], ctx_lens [B] and slots [B] (INT8) are
+    int32 CUDA tensors, kept alive by the descriptor; their contents may change
+    between calls as long as num_tokens and max_tokens still bound them."""
+    B = ctx_lens.numel()
+    if block_tables.dim() != 2 or block_tables.shape[0] < B:
+        raise ValueError(f"block_tables must be [{B}, max_blocks], got {tuple(block_tables.shape)}")
+    keep = [token_starts, block_tables, ctx_lens, slots]
+    if len({t.device for t in keep if t is not None}) != 1:
+        raise ValueError("the batch's tensors must be on one device")
+    d = BatchDesc(_dev(token_starts, "token_starts", torch.int32, B + 1),
+                  _dev(block_tables, "block_tables", torch.int32, B * block_tables.shape[1]),
+                  _dev(ctx_lens, "ctx_lens", torch.int32, B), _opt_dev(slots, "slots", torch.int32, B),
+                  B, block_tables.shape[1], num_tokens, max_tokens)
+    d.keep, d.device = keep, ctx_lens.device
+    return d
+
+
+def make_rope(inv_freq: torch.Tensor, *, interleaved: bool = False, scale: float = 1.0, positions=None) -> RopeDesc:
+    """Rotary descriptor (``pkv_rope``): inv_freq fp64 CUDA tensor [rotary_dim / 2],
+    radians a position; positions: int32 CUDA tensor [num_tokens] or None (each
+    token's index in its context). The tensors are kept alive by the descriptor."""
+    d = RopeDesc(_dev(inv_freq, "inv_freq", torch.float64), _opt_dev(positions, "positions", torch.int32),
+                 2 * inv_freq.numel(), 1 if interleaved else 0, scale)
+    d.keep, d.num_positions = (inv_freq, positions), None if positions is None else positions.numel()
+    return d
+
+
+def _rows(t: torch.Tensor, name: str, batch: BatchDesc, heads: int, dim: int, dtype=torch.bfloat16) -> tuple:
+    """(pointer, token stride in elements) of a [>= num_tokens, heads, dim] tensor
+    whose rows are contiguous, on the batch's device."""
+    if not isinstance(t, torch.Tensor) or t.device != batch.device:
+        raise ValueError(f"{name} must be a tensor on {batch.device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[0] < batch.num_tokens or shape[1] != heads or shape[2] != dim:
+        raise ValueError(f"{name} must be [{batch.num_tokens}, {heads}, {dim}], got {tuple(shape)}")
+    if (stride[2] != 1 and dim > 1) or (stride[1] != dim and heads > 1):
+        raise ValueError(f"{name}: each token's row must be contiguous")
+    # a single row may carry any stride; the C entry wants one that holds a row
+    return t.data_ptr(), stride[0] if shape[0] > 1 else max(stride[0], heads * dim)
+
+
+def _batch_stream(batch: BatchDesc, stream) -> int:
+    if batch.device.index != torch.cuda.current_device():
+        raise ValueError(f"the batch is on {batch.device}, which is not the current device")
+    return _stream(stream)
+
+
+def pkv_rope_append(desc: CacheDesc, batch: BatchDesc, rope, q, k: torch.Tensor, v: torch.Tensor, q_out=None,
+                    stream=None) -> None:
+    """Turns the new tokens' q [T, Hq, d] into q_out and writes their k, v
+    [T, Hkv, d] into the cache (see ``pkv_rope_append`` in pkv.h). q may be None;
+    q_out None turns q in place. rope: from make_rope, or None (nothing turns)."""
+    hq, hkv, d = desc.num_q_heads, desc.num_kv_heads, desc.head_dim
+    qp, qs = (None, 0) if q is None else _rows(q, "q", batch, hq, d)
+    op, os_ = (qp, qs) if q is None or q_out is None else _rows(q_out, "q_out", batch, hq, d)
+    kp, ks = _rows(k, "k", batch, hkv, d)
+    vp, vs = _rows(v, "v", batch, hkv, d)
+    if rope is not None and rope.num_positions is not None and rope.num_positions < batch.num_tokens:
+        raise ValueError(f"positions hold {rope.num_positions} entries, need {batch.num_tokens}")
+    _check("pkv_rope_append",
+           lib().pkv_rope_append(ctypes.byref(desc), ctypes.byref(batch), None if rope is None else ctypes.byref(rope),
+                                 qp, qs, kp, ks, vp, vs, op, os_, _batch_stream(batch, stream)))
+
+
+def pkv_window_split_tokens(desc: CacheDesc, batch: BatchDesc, window: int, sinks: int) -> int:
+    n = lib().pkv_window_split_tokens(ctypes.byref(desc), ctypes.byref(batch), window, sinks)
+    if n < 0:
+        raise PkvError("pkv_window_split_tokens", n)
+    return n
+
+
+def pkv_window_ws_bytes(desc: CacheDesc, batch: BatchDesc, window: int, sinks: int, split_tokens: int) -> int:
+    return lib().pkv_window_ws_bytes(ctypes.byref(desc), ctypes.byref(batch), window, sinks, split_tokens)
+
+
+def pkv_window_attention(desc: CacheDesc, batch: BatchDesc, q: torch.Tensor, out: torch.Tensor, window: int, sinks: int,
+                         sm_scale: float, split_tokens: int = 0, ws=None, stream=None) -> None:
+    """Causal attention of the new tokens' q [T, Hq, d] over the cache into out,
+    each seeing the last `window` tokens (0: all) and the first `sinks`. ws: a
+    zeroed CUDA tensor of pkv_window_ws_bytes(...) bytes when split."""
+    hq, d = desc.num_q_heads, desc.head_dim
+    qp, qs = _rows(q, "q", batch, hq, d)
+    op, os_ = _rows(out, "out", batch, hq, d)
+    wp, wn = (None, 0) if ws is None else (_dev(ws, "ws", ws.dtype), ws.numel() * ws.element_size())
+    _check("pkv_window_attention",
+           lib().pkv_window_attention(ctypes.byref(desc), ctypes.byref(batch), qp, qs, window, sinks, sm_scale,
+                                      split_tokens, wp, wn, op, os_, _batch_stream(batch, stream)))
+
+
+def pkv_gather_kv(desc: CacheDesc, batch: BatchDesc, k_out: torch.Tensor, v_out: torch.Tensor, first=None,
+                  stream=None) -> None:
+    """Reads the batch's tokens back from the cache into k_out, v_out [T, Hkv, d]
+    (bf16 or fp32), or those from first[b] (int32 [B]) on."""
+    hkv, d = desc.num_kv_heads, desc.head_dim
+    if k_out.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"k_out must be bf16 or fp32, got {k_out.dtype}")
+    kp, ks = _rows(k_out, "k_out", batch, hkv, d, k_out.dtype)
+    vp, vs = _rows(v_out, "v_out", batch, hkv, d, k_out.dtype)
+    if ks != vs:
+        raise ValueError("k_out and v_out must have the same token stride")
+    kind = PKV_OUT_FP32 if k_out.dtype == torch.float32 else PKV_OUT_BF16
+    _check("pkv_gather_kv",
+           lib().pkv_gather_kv(ctypes.byref(desc), ctypes.byref(batch), _opt_dev(first, "first", torch.int32, batch.B),
+                               kp, vp, ks, kind, _batch_stream(batch, stream)))
 
 
 def pkv_sync_status(descs, stream=None, raise_on_error: bool = True) -> int:
