@@ -403,7 +403,7 @@ int pkv_rope_append(const pkv_cache_desc* c, const pkv_batch_desc* batch, const 
  * with K and V read as pkv_decode_attention reads them (INT8 dequantized, the
  * partly filled last block from the slot's tail). q, out: [num_tokens][Hq][d]
  * bf16 with token strides of q_stride, out_stride elements (multiples of 8;
- * both 16-byte aligned). fp32 accumulation. Rows of a sequence with a bad
+ * both 16-byte aligned); sm_scale is finite and not negative. fp32 accumulation. Rows of a sequence with a bad
  * context length are zero; a token whose block id or slot is bad counts as
  * not visible, and a row that sees nothing is zero.
  *

@@ -49,7 +49,8 @@ int check_batch(const pkv_cache_desc* c, const pkv_batch_desc* batch, BatchView*
 // cuTensorMapEncodeTiled, or nullptr if the driver does not offer it.
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 
-// Tensor map of a pool for 16-row x 128-byte boxes (kept per thread).
-int pool_tensor_map(const void* pool, int32_t num_blocks, int32_t rows, int32_t row_bytes, CUtensorMap* out);
+// Tensor map of a pool for box_rows x 128-byte boxes (kept per thread).
+int pool_tensor_map(const void* pool, int32_t num_blocks, int32_t rows, int32_t row_bytes, CUtensorMap* out,
+                    int32_t box_rows = 16);
 
 }  // namespace pkv

@@ -225,24 +225,26 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 }
 
 // The decode kernel's tensor map of a pool: the pool as bytes
-// [num_blocks][rows = Hkv * bs][row_bytes], boxes of 16 rows x 128 bytes,
+// [num_blocks][rows = Hkv * bs][row_bytes], boxes of box_rows rows x 128 bytes,
 // 128-byte swizzle. Encoding is host-only work; the last map of each pool is
 // kept per thread (a small direct-mapped cache keyed by the pool's shape).
-int pool_tensor_map(const void* pool, int32_t num_blocks, int32_t rows, int32_t row_bytes, CUtensorMap* out) {
+int pool_tensor_map(const void* pool, int32_t num_blocks, int32_t rows, int32_t row_bytes, CUtensorMap* out,
+                    int32_t box_rows) {
     struct Entry {
         CUtensorMap map;
         const void* pool;
-        int32_t num_blocks, rows, row_bytes;
+        int32_t num_blocks, rows, row_bytes, box_rows;
     };
     thread_local Entry cache[128] = {};
-    const uint64_t h = (uint64_t(reinterpret_cast<uintptr_t>(pool)) >> 8) * 0x9E3779B97F4A7C15ull;
+    const uint64_t h = ((uint64_t(reinterpret_cast<uintptr_t>(pool)) >> 8) + uint64_t(box_rows)) * 0x9E3779B97F4A7C15ull;
     Entry& e = cache[h >> 57];
-    if (e.pool != pool || e.num_blocks != num_blocks || e.rows != rows || e.row_bytes != row_bytes) {
+    if (e.pool != pool || e.num_blocks != num_blocks || e.rows != rows || e.row_bytes != row_bytes ||
+        e.box_rows != box_rows) {
         const PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
         if (!enc) return PKV_ERR_CUDA;
         const cuuint64_t dims[3] = {cuuint64_t(row_bytes), cuuint64_t(rows), cuuint64_t(num_blocks)};
         const cuuint64_t strides[2] = {cuuint64_t(row_bytes), cuuint64_t(rows) * cuuint64_t(row_bytes)};
-        const cuuint32_t box[3] = {128, 16, 1};
+        const cuuint32_t box[3] = {128, cuuint32_t(box_rows), 1};
         const cuuint32_t elem[3] = {1, 1, 1};
         e.pool = nullptr;
         if (enc(&e.map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(pool), dims, strides, box, elem,
@@ -253,6 +255,7 @@ int pool_tensor_map(const void* pool, int32_t num_blocks, int32_t rows, int32_t 
         e.num_blocks = num_blocks;
         e.rows = rows;
         e.row_bytes = row_bytes;
+        e.box_rows = box_rows;
     }
     *out = e.map;
     return PKV_OK;

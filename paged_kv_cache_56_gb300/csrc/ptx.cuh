@@ -120,6 +120,11 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
     return v;
 }
 
+__device__ __forceinline__ void sts128(uint32_t addr, const uint4& v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                 : "memory");
+}
+
 // Global load through L2 only: sees global writes made earlier in this kernel
 // by other threads of the CTA (after a barrier), unlike the read-only path.
 __device__ __forceinline__ uint4 ldcg128(const void* p) {

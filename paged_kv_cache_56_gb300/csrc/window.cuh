@@ -18,6 +18,7 @@ namespace pkv {
 struct WindowParams {
     CUtensorMap tm_k;  // the pools, as in DecodeParams
     CUtensorMap tm_v;
+    CUtensorMap tm_q;  // q as [tokens][Hkv][G][D], boxes of 128 rows x 64 elements (window_tc_kernel)
     BatchView bt;
     CacheView c;
     const uint16_t* q;

@@ -13,6 +13,8 @@ WindowFn window_rows_fn_d64_bf16(int nt);
 WindowFn window_rows_fn_d64_int8(int nt);
 WindowFn window_rows_fn_d128_bf16(int nt);
 WindowFn window_rows_fn_d128_int8(int nt);
+WindowFn window_tc_fn_d64_bf16(size_t* smem, int* threads);
+WindowFn window_tc_fn_d128_bf16(size_t* smem, int* threads);
 
 namespace {
 
@@ -27,6 +29,7 @@ struct Plan {
     WindowFn fn;
     size_t smem;
     int threads;
+    bool tc;          // window_tc_kernel
     int row_tiles;    // row tiles of max_tokens tokens
     int key_tiles;    // most 16-token tiles that one row tile sees
     int ctas_per_sm;
@@ -74,25 +77,36 @@ int sm_count(int* out) {
     return PKV_OK;
 }
 
-// Most 16-token tiles that `span` tokens in a row see.
-int most_key_tiles(const pkv_cache_desc* c, const pkv_batch_desc* bt, int window, int sinks, int span) {
-    const int64_t all = (int64_t(bt->max_blocks) * c->block_size + kTile - 1) / kTile;
+// Most 16-token tiles in the list of keys (in units of `unit` tokens) that
+// `span` tokens in a row see.
+int most_key_tiles(const pkv_cache_desc* c, const pkv_batch_desc* bt, int window, int sinks, int span, int unit) {
+    const int64_t all = int64_t(bt->max_blocks) * c->block_size / kTile;
     if (window <= 0) return int(all);
-    const int64_t seen = (int64_t(window) + span + kTile - 2) / kTile + 1 + (int64_t(sinks) + kTile - 1) / kTile;
-    return int(std::min(all, seen));
+    const int64_t seen = (int64_t(window) + span + unit - 2) / unit + 1 + (int64_t(sinks) + unit - 1) / unit;
+    return int(std::min(all, seen * (unit / kTile)));
 }
 
 int make_plan(const pkv_cache_desc* c, const pkv_batch_desc* bt, int window, int sinks, Plan* pl) {
     const bool int8 = c->dtype == PKV_DTYPE_INT8;
     const int g = c->num_q_heads / c->num_kv_heads;
     const int64_t rows = int64_t(bt->max_tokens) * g;
+    // The row kernel reads each key once for up to 16 rows and is bound by that;
+    // more rows would have it read them again, and the tensor cores take over.
+    pl->tc = rows > 16 && !int8;
+    if (pl->tc) {
+        pl->fn = c->head_dim == 128 ? window_tc_fn_d128_bf16(&pl->smem, &pl->threads)
+                                    : window_tc_fn_d64_bf16(&pl->smem, &pl->threads);
+        pl->row_tiles = int((rows + 255) / 256);
+        pl->key_tiles = most_key_tiles(c, bt, window, sinks, int(std::min<int64_t>(256 / g, bt->max_tokens)), c->block_size);
+        return prepare_kernel(pl->fn, pl->smem, pl->threads, &pl->ctas_per_sm);
+    }
     const int nt = rows <= 8 ? 1 : 2;
     if (c->head_dim == 128) pl->fn = int8 ? window_rows_fn_d128_int8(nt) : window_rows_fn_d128_bf16(nt);
     else pl->fn = int8 ? window_rows_fn_d64_int8(nt) : window_rows_fn_d64_bf16(nt);
     pl->smem = window_rows_smem(c->head_dim, int8);
     pl->threads = kThreads;
     pl->row_tiles = int((rows + 8 * nt - 1) / (8 * nt));
-    pl->key_tiles = most_key_tiles(c, bt, window, sinks, std::max(1, 8 * nt / g));
+    pl->key_tiles = most_key_tiles(c, bt, window, sinks, std::max(1, 8 * nt / g), kTile);
     return prepare_kernel(pl->fn, pl->smem, pl->threads, &pl->ctas_per_sm);
 }
 
@@ -120,6 +134,44 @@ int check_window(const pkv_cache_desc* c, const pkv_batch_desc* batch, int windo
     const int st = check_batch(c, batch, bt, cv);
     if (st != PKV_OK) return st;
     if (window < 0 || sinks < 0 || split_tokens < 0 || split_tokens % kTile) return PKV_ERR_INVALID;
+    return PKV_OK;
+}
+
+// Tensor map of the queries for window_tc_kernel: [tokens][Hkv][G][d] with
+// boxes of 128 rows (128 / G tokens x the group) x 64 elements, 128-byte
+// swizzle. The last maps are kept per thread, as the pools' are.
+int q_tensor_map(const pkv_cache_desc* c, int tokens, const void* q, int64_t stride, CUtensorMap* out) {
+    struct Entry {
+        CUtensorMap map;
+        const void* q;
+        int64_t stride;
+        int tokens, hq, hkv, d;
+    };
+    thread_local Entry cache[64] = {};
+    const uint64_t h = (uint64_t(reinterpret_cast<uintptr_t>(q)) >> 4) * 0x9E3779B97F4A7C15ull;
+    Entry& e = cache[h >> 58];
+    if (e.q != q || e.stride != stride || e.tokens != tokens || e.hq != c->num_q_heads || e.hkv != c->num_kv_heads ||
+        e.d != c->head_dim) {
+        const PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+        if (!enc) return PKV_ERR_CUDA;
+        const cuuint64_t g = cuuint64_t(c->num_q_heads / c->num_kv_heads), d = cuuint64_t(c->head_dim);
+        const cuuint64_t dims[4] = {d, g, cuuint64_t(c->num_kv_heads), cuuint64_t(tokens)};
+        const cuuint64_t strides[3] = {d * 2, g * d * 2, cuuint64_t(stride) * 2};
+        const cuuint32_t box[4] = {64, cuuint32_t(g), 1, cuuint32_t(128 / g)};
+        const cuuint32_t elem[4] = {1, 1, 1, 1};
+        e.q = nullptr;
+        if (enc(&e.map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(q), dims, strides, box, elem,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return PKV_ERR_CUDA;
+        e.q = q;
+        e.stride = stride;
+        e.tokens = tokens;
+        e.hq = c->num_q_heads;
+        e.hkv = c->num_kv_heads;
+        e.d = c->head_dim;
+    }
+    *out = e.map;
     return PKV_OK;
 }
 
@@ -154,7 +206,9 @@ int pkv_window_split_tokens(const pkv_cache_desc* c, const pkv_batch_desc* batch
     const int64_t splits = int64_t(sms) * pl.ctas_per_sm / units;
     if (splits <= 1) return 0;
     // at least two tiles a warp: shorter splits spend their time on the start and the merge
-    const int64_t tiles = std::max<int64_t>((pl.key_tiles + splits - 1) / splits, 2 * kWarps);
+    // (tensor-core kernel: two key tiles)
+    int64_t tiles = std::max<int64_t>((pl.key_tiles + splits - 1) / splits, pl.tc ? 16 : 2 * kWarps);
+    if (pl.tc) tiles = (tiles + 7) / 8 * 8;
     return tiles >= pl.key_tiles ? 0 : int(tiles * kTile);
 }
 
@@ -175,7 +229,7 @@ int pkv_window_attention(const pkv_cache_desc* c, const pkv_batch_desc* batch, c
     WindowParams p;
     int st = check_window(c, batch, window, sinks, split_tokens, &p.bt, &p.c);
     if (st != PKV_OK) return st;
-    if (!(sm_scale == sm_scale)) return PKV_ERR_INVALID;
+    if (!(sm_scale >= 0.f) || sm_scale > 3.0e38f) return PKV_ERR_INVALID;
     if (is_empty(batch)) return PKV_OK;
     const int64_t row = int64_t(c->num_q_heads) * c->head_dim;
     if (!q || !out || !aligned16(q) || !aligned16(out) || q_stride < row || out_stride < row ||
@@ -189,7 +243,12 @@ int pkv_window_attention(const pkv_cache_desc* c, const pkv_batch_desc* batch, c
 
     const bool int8 = c->dtype == PKV_DTYPE_INT8;
     const int32_t row_bytes = c->head_dim * (int8 ? 1 : 2);
-    if (row_bytes >= 128) {
+    if (pl.tc) {
+        const int32_t rows = c->num_kv_heads * c->block_size;
+        if ((st = pool_tensor_map(c->k_pool, c->num_blocks, rows, row_bytes, &p.tm_k, c->block_size)) != PKV_OK) return st;
+        if ((st = pool_tensor_map(c->v_pool, c->num_blocks, rows, row_bytes, &p.tm_v, c->block_size)) != PKV_OK) return st;
+        if ((st = q_tensor_map(c, batch->num_tokens, q, q_stride, &p.tm_q)) != PKV_OK) return st;
+    } else if (row_bytes >= 128) {
         const int32_t rows = c->num_kv_heads * c->block_size;
         if ((st = pool_tensor_map(c->k_pool, c->num_blocks, rows, row_bytes, &p.tm_k)) != PKV_OK) return st;
         if ((st = pool_tensor_map(c->v_pool, c->num_blocks, rows, row_bytes, &p.tm_v)) != PKV_OK) return st;
@@ -210,7 +269,8 @@ int pkv_window_attention(const pkv_cache_desc* c, const pkv_batch_desc* batch, c
     p.split_tiles = splits > 1 ? split_tokens / kTile : 0;
     p.max_splits = splits;
     p.row_tiles = pl.row_tiles;
-    p.qscale = sm_scale * 1.4426950408889634f;
+    // never 0: a hidden token's score is -infinity, and 0 times that is not a number
+    p.qscale = std::max(sm_scale * 1.4426950408889634f, 1e-37f);
     const int64_t gx = int64_t(pl.row_tiles) * splits;
     if (gx > 0x7FFFFFFF) return PKV_ERR_INVALID;
     const dim3 grid(unsigned(gx), unsigned(c->num_kv_heads), unsigned(batch->B));

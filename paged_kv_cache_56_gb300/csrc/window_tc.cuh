@@ -1,0 +1,463 @@
+// Windowed attention for many query rows (prompts and chunks) on the tensor
+// cores of sm_103a (tcgen05, accumulators in tensor memory).
+//
+// One CTA per (split, 256 rows, kv head, sequence): two tiles of 128 rows, a
+// row a (token, query head of the group), so that a kv head's whole group
+// shares each K and V tile that the CTA loads. Keys come in tiles of 128
+// tokens, gathered block by block through the block table.
+//
+//   warps 0-3, 4-7: softmax of row tile 0 and 1, one row a thread -- no shuffle
+//                   anywhere; scores from tensor memory, weights back to it
+//   then            the loader: one warp of tensor copies (bf16 cache), or four
+//                   warps that turn int8 codes into bf16 (an integer up to 128
+//                   is exact in bf16) on their way to shared memory; the
+//                   block's scales go to the scores' and weights' columns
+//   last warp       one thread that issues the multiplies
+//
+//   S_i = Q_i K^T   128 x 128 x D, operands in shared memory
+//   O_i += P_i V    128 x D x 128, P_i in tensor memory over the scores it came
+//                   from; V as it lies in the cache (MN-major B)
+// The two row tiles take turns: while one's softmax runs the tensor core works
+// for the other. S_i of the next key tile is issued right behind O_i += P_i V,
+// so one commit tells the softmax both that its scores are there and that O_i
+// may be corrected.
+//
+// The running maximum is a reference that follows the true one only when that
+// is more than 2^8 ahead, so O_i is rarely rescaled. Weights are kept in units
+// of 2^-24 (an exponent bias, free), so that neither they times V nor their
+// sum leaves fp32 for any bf16 V. Weights are rounded to bf16 for the multiply
+// (half a step, 2^-8 of each weight, as the outputs are); their sum is fp32.
+#pragma once
+
+#include "ptx_tc.cuh"
+#include "window.cuh"
+
+namespace pkv {
+
+constexpr int kTcRows = 128;   // rows of a row tile
+constexpr int kTcKeys = 128;   // tokens of a key tile
+constexpr float kTcShift = 24.f;
+constexpr float kTcAhead = 8.f;
+
+template <int D, bool INT8>
+struct TcTraits {
+    static constexpr int kLoadWarps = INT8 ? 4 : 1;
+    static constexpr int kThreads = (8 + kLoadWarps + 1) * 32;
+    static constexpr int kTileBytes = kTcKeys * D * 2;          // one K or V tile (bf16) = one row tile of Q
+    static constexpr int kStages = D == 128 ? 4 : 6;
+    static constexpr int kSmem = 1024 + (2 + kStages) * kTileBytes;
+    static constexpr int kSlab = kTcKeys * 128;                 // 64 of a tile's D columns
+};
+
+// Barriers of a CTA.
+template <int STAGES>
+struct TcBars {
+    uint64_t q_full;
+    uint64_t kv_full[STAGES];
+    uint64_t kv_empty[STAGES];
+    uint64_t raw_full;      // a V tile whose dead rows have to be cleared first
+    uint64_t s_full[2];     // S_i is there and O_i += P_i V of the tile before is done
+    uint64_t p_full[2];     // P_i is there, O_i corrected
+    uint64_t drain;
+};
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+
+template <int D, bool INT8>
+__global__ void __launch_bounds__(TcTraits<D, INT8>::kThreads, 1)
+window_tc_kernel(const __grid_constant__ WindowParams p) {
+    using T = TcTraits<D, INT8>;
+    constexpr int STAGES = T::kStages;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ TcBars<STAGES> bars;
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_last;
+    __shared__ uint32_t s_bad[8];          // units of a key tile that are not there, by tile % 8
+    __shared__ float2 s_sc[INT8 ? 8 : 1][8];  // (K, V) scales of a key tile's units
+
+    pdl_wait();
+    pdl_launch_dependents();
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int S = p.max_splits;
+    const int j = int(blockIdx.x) % S, rt = p.row_tiles - 1 - int(blockIdx.x) / S;  // the longest first
+    const int kvh = blockIdx.y, b = blockIdx.z;
+    const int G = p.c.Hq / p.c.Hkv, bs = p.c.bs;
+    const SeqRange sq = seq_range(p.bt, b, bs, p.c.err, tid == 0 && blockIdx.x == 0 && kvh == 0);
+    const int r_first = rt * 2 * kTcRows, r_end = min(sq.n * G, r_first + 2 * kTcRows);
+    if (r_first >= r_end) return;
+    const int nrow = r_end - r_first, nq = nrow > kTcRows ? 2 : 1;
+    if (sq.bad) {
+        if (j == 0)
+            for (int e = tid; e < nrow * D; e += T::kThreads) {
+                const int r = r_first + e / D;
+                p.out[int64_t(sq.row0 + r / G) * p.out_stride + (kvh * G + r % G) * D + e % D] = 0;
+            }
+        return;
+    }
+    const int pos0 = sq.ctx - sq.n;
+    const int p_first = pos0 + r_first / G, p_last = pos0 + (r_end - 1) / G;
+    const KeyTiles kt = key_tiles(p_first, p_last, p.window, p.sinks, bs);  // in blocks
+    const int U = kTcKeys / bs, lg = bs == 16 ? 4 : 6;                        // blocks a key tile
+    const int tiles = (kt.n + U - 1) / U;
+    int per = tiles;
+    if (p.split_tiles > 0) per = max(p.split_tiles * kTile / kTcKeys, (tiles + S - 1) / S);
+    const int ns = (tiles + per - 1) / per;
+    if (j >= ns) return;
+    const int k0 = j * per, n = min(tiles, k0 + per) - k0;  // this split's key tiles
+
+    uint8_t* q_smem = smem + ((1024u - (smem_addr(smem) & 1023u)) & 1023u);
+    const uint32_t q_addr = smem_addr(q_smem), kv_addr = q_addr + 2 * T::kTileBytes;
+    const uint32_t bar0 = smem_addr(&bars);
+    const auto bar = [&](const uint64_t* x) {
+        return bar0 + uint32_t(reinterpret_cast<const uint8_t*>(x) - reinterpret_cast<const uint8_t*>(&bars));
+    };
+    constexpr int kMmaWarp = 8 + T::kLoadWarps;
+    if (tid == 0) {
+        mbar_init(bar(&bars.q_full), 1);
+        mbar_init(bar(&bars.raw_full), 1);
+        mbar_init(bar(&bars.drain), 1);
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(bar(&bars.kv_full[s]), INT8 ? T::kLoadWarps * 32 : 1);
+            mbar_init(bar(&bars.kv_empty[s]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(&bars.s_full[i]), 1);
+            mbar_init(bar(&bars.p_full[i]), kTcRows);
+        }
+        fence_mbar_init();
+    }
+    if (warp == kMmaWarp) tmem_alloc(smem_addr(&s_tmem), 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    const auto s_col = [&](int i) { return tmem + uint32_t(i) * 128u; };
+    const auto o_col = [&](int i) { return tmem + 256u + uint32_t(i) * 128u; };
+    // Waits for a phase; after about a second without it a role gives up (and
+    // so, one after the other, do those that wait for it).
+    const auto wait = [&](const uint64_t* x, uint32_t parity) { return wait_phase(bar(x), parity & 1u); };
+    // ... for a whole warp, which it leaves converged
+    const auto wait_warp = [&](const uint64_t* x, uint32_t parity) {
+        return __all_sync(kFull, wait_phase(bar(x), parity & 1u)) != 0;
+    };
+    // tokens that no row of the CTA sees: their V rows count as zero
+    const int dead_lo = max(0, p_first - p.window + 1);
+    const auto dead = [&](int t) { return t > p_last || (t < dead_lo && t >= p.sinks); };
+    const int32_t* table = p.bt.tables + size_t(b) * p.bt.max_blocks;
+
+    if (warp < 8) {
+        // ================= softmax of row tile i, a row a thread =================
+        const int i = warp >> 2, row = r_first + tid;  // tid < 256: rows of the CTA in order
+        const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
+        const uint32_t s_addr = s_col(i) + lane_base, o_addr = o_col(i) + lane_base;
+        const bool have = row < r_end;
+        const int hi = have ? pos0 + row / G : -1;
+        const int lo = max(0, hi - p.window + 1);
+        // the row tile's first and last position
+        const int pf = pos0 + (r_first + i * kTcRows) / G;
+        const int pl = pos0 + (min(r_end, r_first + (i + 1) * kTcRows) - 1) / G;
+        const float scale = p.qscale;
+        float m_ref = -INFINITY;  // reference of the exponent, in score units
+        float2 l2 = make_float2(0.f, 0.f);
+        bool ok = true;
+        if (i < nq) {
+            for (int jj = 0; jj < n; ++jj) {
+                if (!(ok = wait_warp(&bars.s_full[i], jj))) break;
+                tc_fence_after();
+                uint32_t r[128];
+                tmem_ld(r, s_addr);
+                const int u0 = (k0 + jj) * U;  // first block of the tile in the list
+                const uint32_t bad = s_bad[jj & 7];
+                const int t_first = kt.tile(u0) * bs;
+                float2 vs2[8];
+                if (INT8) {
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        const float2 sc = s_sc[jj & 7][(c * 16) >> lg];
+                        vs2[c] = make_float2(sc.y, sc.y);
+#pragma unroll
+                        for (int e = 0; e < 16; e += 2) {
+                            const float2 x = mul2(make_float2(__uint_as_float(r[c * 16 + e]), __uint_as_float(r[c * 16 + e + 1])),
+                                                  make_float2(sc.x, sc.x));
+                            r[c * 16 + e] = __float_as_uint(x.x);
+                            r[c * 16 + e + 1] = __float_as_uint(x.y);
+                        }
+                    }
+                }
+                const bool masked = bad != 0 || u0 < kt.nsink || t_first + kTcKeys - 1 > pf || t_first < pl - p.window + 1;
+                if (masked) {
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        const int u = (c * 16) >> lg;
+                        const int t0 = (kt.tile(u0 + u) << lg) + ((c * 16) & (bs - 1));
+                        // bit e: this row sees token t0 + e
+                        const auto below = [](int x) { return (1u << min(16, max(0, x))) - 1u; };
+                        uint32_t see = below(hi - t0 + 1) & (below(p.sinks - t0) | ~below(lo - t0));
+                        if ((bad >> u) & 1u) see = 0u;
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            if (!((see >> e) & 1u)) r[c * 16 + e] = 0xFF800000u;  // -inf
+                    }
+                }
+                float mx = __uint_as_float(r[0]), my = __uint_as_float(r[1]);
+#pragma unroll
+                for (int e = 2; e < 128; e += 4) {
+                    mx = fmaxf(fmaxf(mx, __uint_as_float(r[e])), e + 2 < 128 ? __uint_as_float(r[e + 2]) : mx);
+                    my = fmaxf(fmaxf(my, __uint_as_float(r[e + 1])), e + 3 < 128 ? __uint_as_float(r[e + 3]) : my);
+                }
+                mx = fmaxf(mx, my);
+                const bool up = (mx - m_ref) * scale > kTcAhead;  // false while nothing has been seen
+                if (__any_sync(kFull, up)) {
+                    const float f = up ? fast_exp2((m_ref - mx) * scale) : 1.f;
+                    if (up) m_ref = mx;
+                    l2.x *= f;
+                    l2.y *= f;
+                    if (jj > 0) {
+#pragma unroll
+                        for (int c = 0; c < D; c += 32) {
+                            uint32_t o[32];
+                            tmem_ld(o, o_addr + c);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            tmem_st(o_addr + c, o);
+                        }
+                    }
+                }
+                const float neg = (m_ref == -INFINITY ? 0.f : -m_ref * scale) - kTcShift;
+                uint32_t w[2][32];
+#pragma unroll
+                for (int e = 0; e < 128; e += 2) {
+                    const float2 x = __ffma2_rn(make_float2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])),
+                                                make_float2(scale, scale), make_float2(neg, neg));
+                    float2 y = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+                    l2 = __fadd2_rn(l2, y);
+                    if (INT8) y = mul2(y, vs2[e / 16]);
+                    w[e / 64][e / 2 % 32] = f2_to_bf16x2(y.x, y.y);
+                }
+                tmem_st(s_addr, w[0]);
+                tmem_st(s_addr + 32, w[1]);
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(bar(&bars.p_full[i]));
+            }
+            if (ok) ok = wait_warp(&bars.s_full[i], n);  // the last O_i += P_i V
+            tc_fence_after();
+        }
+        // ---- write the row
+        if (i < nq && ok) {
+            const float l = l2.x + l2.y;
+            const int64_t tok = sq.row0 + (have ? row / G : 0);
+            const int head = kvh * G + (have ? row % G : 0);
+            const float f = ns > 1 ? 1.f : (l > 0.f ? 1.f / l : 0.f);
+            const size_t at = (size_t(tok) * p.c.Hq + head) * S + j;
+#pragma unroll
+            for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
+                __syncwarp();
+                tmem_ld(o, o_addr + c);
+                if (!have) {
+                } else if (ns > 1) {
+                    float4* dst = reinterpret_cast<float4*>(p.ws_o + at * D + c);
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4)
+                        dst[e / 4] = make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]),
+                                                 __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
+                } else {
+                    uint4* dst = reinterpret_cast<uint4*>(p.out + tok * p.out_stride + head * D + c);
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) {
+                        uint32_t x[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            x[k] = f2_to_bf16x2(__uint_as_float(o[e + 2 * k]) * f, __uint_as_float(o[e + 2 * k + 1]) * f);
+                        dst[e / 8] = make_uint4(x[0], x[1], x[2], x[3]);
+                    }
+                }
+            }
+            if (ns > 1 && have) {
+                p.ws_ml[at * 2] = m_ref == -INFINITY ? -1e30f : m_ref * scale;
+                p.ws_ml[at * 2 + 1] = l;
+            }
+        }
+        if (!ok && lane == 0) report(p.c.err, kErrTimeout);
+    } else if (warp < kMmaWarp) {
+        if constexpr (!INT8) {
+            // ================= loader: tensor copies through the block table =================
+            if (lane == 0) {
+                prefetch_tensormap(&p.tm_q);
+                prefetch_tensormap(&p.tm_k);
+                prefetch_tensormap(&p.tm_v);
+                mbar_arrive_expect_tx(bar(&bars.q_full), uint32_t(nq) * T::kTileBytes);
+                for (int i = 0; i < nq; ++i)
+                    for (int h = 0; h < D / 64; ++h)
+                        tma_load_4d(q_addr + i * T::kTileBytes + h * T::kSlab, &p.tm_q, h * 64, 0, kvh,
+                                    sq.row0 + (r_first + i * kTcRows) / G, bar(&bars.q_full));
+            }
+            int pending = -1, raw_phase = 0;  // the V item whose dead rows are still to be cleared
+            const auto clear_pending = [&] {
+                if (!wait_warp(&bars.raw_full, raw_phase)) return false;
+                ++raw_phase;
+                const int tile = k0 + pending / 2;
+                const uint32_t base = kv_addr + uint32_t(pending % STAGES) * T::kTileBytes;
+                for (int u = 0; u < U && tile * U + u < kt.n; ++u) {
+                    const int t0 = kt.tile(tile * U + u) * bs;
+                    for (int e = lane; e < bs * (D / 8); e += 32) {
+                        const int rr = e / (D / 8), ch = e % (D / 8);
+                        if (dead(t0 + rr))
+                            sts128(base + uint32_t((ch / 8) * T::kSlab + (u * bs + rr) * 128 + (ch % 8) * 16),
+                                   make_uint4(0u, 0u, 0u, 0u));
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(&bars.kv_full[pending % STAGES]));
+                pending = -1;
+                return true;
+            };
+            bool ok = true;
+            int issued = 0;
+            int id = -1;      // lane u: the block of unit u of the tile
+            bool dirty = false;  // lane u: the unit is there and holds dead tokens
+            for (int it = 0; it < 2 * n && ok; ++it) {
+                const int tile = k0 + it / 2, s = it % STAGES;
+                if (it % 2 == 0) {
+                    id = p.c.num_blocks;  // behind the pool: the copy fills zeros
+                    bool miss = false;
+                    dirty = false;
+                    if (lane < U) {
+                        miss = true;
+                        const int u = tile * U + lane;
+                        if (u < kt.n) {
+                            const int t0 = kt.tile(u) * bs;
+                            const int x = table[t0 / bs];
+                            if (x >= 0 && x < p.c.num_blocks) {
+                                id = x;
+                                miss = false;
+                                dirty = t0 + bs - 1 > p_last || (t0 < dead_lo && t0 + bs > p.sinks);
+                            } else {
+                                report(p.c.err, kErrBlockId);
+                            }
+                        }
+                    }
+                    const uint32_t missing = __ballot_sync(kFull, miss);
+                    if (lane == 0) s_bad[(it / 2) & 7] = missing;
+                }
+                const bool fix = it % 2 == 1 && __any_sync(kFull, dirty);
+                // clear an earlier V tile once further copies are under way, and before the ring is full
+                if (pending >= 0 && (fix || it - pending >= 2)) ok = clear_pending();
+                if (ok && it >= STAGES) ok = wait_warp(&bars.kv_empty[s], it / STAGES - 1);
+                if (!ok) break;
+                const uint32_t full = fix ? bar(&bars.raw_full) : bar(&bars.kv_full[s]);
+                if (lane == 0) mbar_arrive_expect_tx(full, T::kTileBytes);
+                __syncwarp();
+                // a lane copies block lane % U, half lane / U of its rows
+                const int u = lane % U, h = lane / U, uid = __shfl_sync(kFull, id, u);
+                if (h < D / 64)
+                    tma_load_3d(kv_addr + uint32_t(s) * T::kTileBytes + h * T::kSlab + u * bs * 128,
+                                it % 2 ? &p.tm_v : &p.tm_k, h * 128, kvh * bs, uid, full);
+                if (fix) pending = it;
+                issued = it + 1;
+            }
+            if (ok && pending >= 0) ok = clear_pending();
+            if (!ok) {
+                // let the copies in flight land before the CTA ends
+                if (pending >= 0) (void)wait(&bars.raw_full, raw_phase);
+                for (int it = max(0, issued - STAGES); it < issued; ++it)
+                    if (it != pending) (void)wait(&bars.kv_full[it % STAGES], it / STAGES);
+                if (lane == 0) report(p.c.err, kErrTimeout);
+            }
+        }
+    } else {
+      if (lane == 0) {
+        // ================= the multiplies =================
+        constexpr uint32_t kDescS = mma_desc_bf16(kTcKeys, false), kDescO = mma_desc_bf16(D, true);
+        const auto kv_tile = [&](int it) { return kv_addr + uint32_t(it % STAGES) * T::kTileBytes; };
+        const auto issue_s = [&](int i, int jj) {
+            const uint32_t qa = q_addr + uint32_t(i) * T::kTileBytes, ka = kv_tile(2 * jj);
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) {
+                const uint32_t off = uint32_t(ks / 4) * T::kSlab + uint32_t(ks % 4) * 32u;
+                mma_ss(s_col(i), smem_desc(qa + off, 16), smem_desc(ka + off, 16), kDescS, ks > 0);
+            }
+        };
+        bool ok = wait(&bars.q_full, 0) && wait(&bars.kv_full[0], 0);
+        if (ok) {
+            tc_fence_after();
+            for (int i = 0; i < nq; ++i) {
+                issue_s(i, 0);
+                mma_commit(bar(&bars.s_full[i]));
+            }
+            mma_commit(bar(&bars.kv_empty[0]));
+        }
+        for (int jj = 0; jj < n && ok; ++jj) {
+            const int iv = 2 * jj + 1, ik = 2 * jj + 2;
+            ok = wait(&bars.kv_full[iv % STAGES], iv / STAGES);
+            for (int i = 0; i < nq && ok; ++i) {
+                if (!(ok = wait(&bars.p_full[i], jj))) break;
+                tc_fence_after();
+                const uint32_t va = kv_tile(iv);
+#pragma unroll
+                for (int ks = 0; ks < kTcKeys / 16; ++ks)
+                    mma_ts(o_col(i), s_col(i) + uint32_t(ks) * 8u, smem_desc(va + uint32_t(ks) * 2048u, T::kSlab), kDescO,
+                           jj > 0 || ks > 0);
+                if (i == nq - 1) mma_commit(bar(&bars.kv_empty[iv % STAGES]));
+                if (jj + 1 < n) {
+                    if (i == 0 && !(ok = wait(&bars.kv_full[ik % STAGES], ik / STAGES))) break;
+                    tc_fence_after();
+                    issue_s(i, jj + 1);
+                }
+                mma_commit(bar(&bars.s_full[i]));
+                if (i == nq - 1 && jj + 1 < n) mma_commit(bar(&bars.kv_empty[ik % STAGES]));
+            }
+        }
+        if (!ok) {
+            mma_commit(bar(&bars.drain));
+            (void)wait_phase(bar(&bars.drain), 0);
+            report(p.c.err, kErrTimeout);
+        }
+      }
+        __syncwarp();
+    }
+
+    // ---- the last split of the row tile to arrive merges all of them
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+    if (ns == 1) return;
+    int32_t* cnt = p.ws_count + (size_t(b) * p.c.Hkv + kvh) * p.row_tiles + rt;
+    if (tid == 0) s_last = atom_add_acq_rel_gpu(cnt, 1) == ns - 1;
+    __syncthreads();
+    if (!s_last) return;
+    // a warp a row: the splits' weights in its lanes, then D elements
+    for (int r = warp; r < nrow; r += T::kThreads / 32) {
+        const int rr = r_first + r;
+        const size_t tok = sq.row0 + rr / G, head = kvh * G + rr % G, at = (tok * p.c.Hq + head) * S;
+        const float2* ml = reinterpret_cast<const float2*>(p.ws_ml) + at;
+        float mm = -1e30f;
+        for (int q = lane; q < ns; q += 32) mm = fmaxf(mm, __ldcg(ml + q).x);
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) mm = fmaxf(mm, __shfl_xor_sync(kFull, mm, off));
+        float acc[D / 32], L = 0.f;
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) acc[e] = 0.f;
+        for (int q = 0; q < ns; ++q) {
+            const float2 x = __ldcg(ml + q);
+            const float c = fast_exp2(x.x - mm);
+            L += c * x.y;
+#pragma unroll
+            for (int e = 0; e < D / 32; ++e) acc[e] += c * __ldcg(p.ws_o + (at + q) * D + e * 32 + lane);
+        }
+        const float f = L > 0.f ? 1.f / L : 0.f;
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e)
+            reinterpret_cast<__nv_bfloat16*>(p.out)[int64_t(tok) * p.out_stride + head * D + e * 32 + lane] =
+                __float2bfloat16_rn(acc[e] * f);
+    }
+    if (tid == 0) *cnt = 0;  // ready for the next call
+}
+
+template <int D, bool INT8>
+constexpr size_t window_tc_smem() { return TcTraits<D, INT8>::kSmem; }
+
+}  // namespace pkv
