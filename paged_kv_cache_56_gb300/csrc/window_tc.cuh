@@ -41,11 +41,23 @@ constexpr float kTcAhead = 8.f;
 
 template <int D, bool INT8>
 struct TcTraits {
+    // warpgroups: softmax 0, softmax 1, then loader and multiplies together
+    // (bf16: warps 8 and 11) or apart (INT8: four loading warps, then warp 12)
     static constexpr int kLoadWarps = INT8 ? 4 : 1;
-    static constexpr int kThreads = (8 + kLoadWarps + 1) * 32;
+    static constexpr int kMmaWarp = INT8 ? 12 : 11;
+    static constexpr int kThreads = INT8 ? 512 : 384;
+    // Registers a thread after the warpgroups' split; their sum is what the
+    // block is launched with (65536 / threads, down to a multiple of 8).
+    static constexpr int kLaunchRegs = INT8 ? kTcLaunchRegsInt8 : kTcLaunchRegsBf16;
+    static constexpr int kSoftmaxRegs = INT8 ? 192 : 208;
+    static constexpr int kLoadRegs = INT8 ? 80 : 88;
+    static constexpr int kMmaRegs = INT8 ? 48 : 0;
+    static_assert(256 * kSoftmaxRegs + 128 * (kLoadRegs + kMmaRegs) == kThreads * kLaunchRegs, "register split");
     static constexpr int kTileBytes = kTcKeys * D * 2;          // one K or V tile (bf16) = one row tile of Q
     static constexpr int kStages = D == 128 ? 4 : 6;
-    static constexpr int kSmem = 1024 + (2 + kStages) * kTileBytes;
+    static constexpr int kRawStages = INT8 ? 2 : 0;             // int8 tiles on their way to bf16
+    static constexpr int kRawBytes = kTcKeys * D;
+    static constexpr int kSmem = 1024 + (2 + kStages) * kTileBytes + kRawStages * kRawBytes;
     static constexpr int kSlab = kTcKeys * 128;                 // 64 of a tile's D columns
 };
 
@@ -55,13 +67,23 @@ struct TcBars {
     uint64_t q_full;
     uint64_t kv_full[STAGES];
     uint64_t kv_empty[STAGES];
-    uint64_t raw_full;      // a V tile whose dead rows have to be cleared first
+    uint64_t raw_full[2];   // INT8: codes to convert; bf16 [0]: a V tile whose dead rows have to be cleared first
+    uint64_t raw_empty[2];
     uint64_t s_full[2];     // S_i is there and O_i += P_i V of the tile before is done
     uint64_t p_full[2];     // P_i is there, O_i corrected
     uint64_t drain;
 };
 
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+
+// Four int8 codes -> bf16, exact: a code with bit pattern s:m (one and seven
+// bits) is (128 + m) - (s ? 256 : 128), and 0x4300 | m, 0x4300 | s << 7 are
+// those numbers' bf16 patterns.
+__device__ __forceinline__ void s8_to_bf16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    const uint32_t a = __byte_perm(w, 0x43434343u, 0x4140), b = __byte_perm(w, 0x43434343u, 0x4342);
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(lo) : "r"(a & 0xFF7FFF7Fu), "r"(a & 0xFF80FF80u));
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(hi) : "r"(b & 0xFF7FFF7Fu), "r"(b & 0xFF80FF80u));
+}
 
 template <int D, bool INT8>
 __global__ void __launch_bounds__(TcTraits<D, INT8>::kThreads, 1)
@@ -111,16 +133,17 @@ window_tc_kernel(const __grid_constant__ WindowParams p) {
     const auto bar = [&](const uint64_t* x) {
         return bar0 + uint32_t(reinterpret_cast<const uint8_t*>(x) - reinterpret_cast<const uint8_t*>(&bars));
     };
-    constexpr int kMmaWarp = 8 + T::kLoadWarps;
+    constexpr int kMmaWarp = T::kMmaWarp;
     if (tid == 0) {
         mbar_init(bar(&bars.q_full), 1);
-        mbar_init(bar(&bars.raw_full), 1);
         mbar_init(bar(&bars.drain), 1);
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(bar(&bars.kv_full[s]), INT8 ? T::kLoadWarps * 32 : 1);
             mbar_init(bar(&bars.kv_empty[s]), 1);
         }
         for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(&bars.raw_full[i]), 1);
+            mbar_init(bar(&bars.raw_empty[i]), T::kLoadWarps * 32);
             mbar_init(bar(&bars.s_full[i]), 1);
             mbar_init(bar(&bars.p_full[i]), kTcRows);
         }
@@ -144,8 +167,12 @@ window_tc_kernel(const __grid_constant__ WindowParams p) {
     const int dead_lo = max(0, p_first - p.window + 1);
     const auto dead = [&](int t) { return t > p_last || (t < dead_lo && t >= p.sinks); };
     const int32_t* table = p.bt.tables + size_t(b) * p.bt.max_blocks;
+    // INT8: tokens from nfull on are in the slot's bf16 tail
+    const int nfull = INT8 ? sq.ctx / bs * bs : sq.ctx;
+    const int slot = INT8 ? p.bt.slots[b] : 0;
 
     if (warp < 8) {
+        reg_inc<T::kSoftmaxRegs>();
         // ================= softmax of row tile i, a row a thread =================
         const int i = warp >> 2, row = r_first + tid;  // tid < 256: rows of the CTA in order
         const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
@@ -165,7 +192,8 @@ window_tc_kernel(const __grid_constant__ WindowParams p) {
                 if (!(ok = wait_warp(&bars.s_full[i], jj))) break;
                 tc_fence_after();
                 uint32_t r[128];
-                tmem_ld(r, s_addr);
+                tmem_ld(reinterpret_cast<uint32_t(&)[64]>(r[0]), s_addr);
+                tmem_ld(reinterpret_cast<uint32_t(&)[64]>(r[64]), s_addr + 64);
                 const int u0 = (k0 + jj) * U;  // first block of the tile in the list
                 const uint32_t bad = s_bad[jj & 7];
                 const int t_first = kt.tile(u0) * bs;
@@ -280,7 +308,12 @@ window_tc_kernel(const __grid_constant__ WindowParams p) {
             }
         }
         if (!ok && lane == 0) report(p.c.err, kErrTimeout);
-    } else if (warp < kMmaWarp) {
+    } else if (warp < 12) {
+        reg_dec<T::kLoadRegs>();
+    } else {
+        reg_dec<INT8 ? T::kMmaRegs : 24>();
+    }
+    if (warp >= 8 && warp < 8 + T::kLoadWarps) {
         if constexpr (!INT8) {
             // ================= loader: tensor copies through the block table =================
             if (lane == 0) {
@@ -295,7 +328,7 @@ window_tc_kernel(const __grid_constant__ WindowParams p) {
             }
             int pending = -1, raw_phase = 0;  // the V item whose dead rows are still to be cleared
             const auto clear_pending = [&] {
-                if (!wait_warp(&bars.raw_full, raw_phase)) return false;
+                if (!wait_warp(&bars.raw_full[0], raw_phase)) return false;
                 ++raw_phase;
                 const int tile = k0 + pending / 2;
                 const uint32_t base = kv_addr + uint32_t(pending % STAGES) * T::kTileBytes;
@@ -347,7 +380,7 @@ window_tc_kernel(const __grid_constant__ WindowParams p) {
                 if (pending >= 0 && (fix || it - pending >= 2)) ok = clear_pending();
                 if (ok && it >= STAGES) ok = wait_warp(&bars.kv_empty[s], it / STAGES - 1);
                 if (!ok) break;
-                const uint32_t full = fix ? bar(&bars.raw_full) : bar(&bars.kv_full[s]);
+                const uint32_t full = fix ? bar(&bars.raw_full[0]) : bar(&bars.kv_full[s]);
                 if (lane == 0) mbar_arrive_expect_tx(full, T::kTileBytes);
                 __syncwarp();
                 // a lane copies block lane % U, half lane / U of its rows
@@ -361,13 +394,119 @@ window_tc_kernel(const __grid_constant__ WindowParams p) {
             if (ok && pending >= 0) ok = clear_pending();
             if (!ok) {
                 // let the copies in flight land before the CTA ends
-                if (pending >= 0) (void)wait(&bars.raw_full, raw_phase);
+                if (pending >= 0) (void)wait(&bars.raw_full[0], raw_phase);
                 for (int it = max(0, issued - STAGES); it < issued; ++it)
                     if (it != pending) (void)wait(&bars.kv_full[it % STAGES], it / STAGES);
                 if (lane == 0) report(p.c.err, kErrTimeout);
             }
+        } else {
+            // ================= INT8: codes (or tail rows) to bf16 tiles, 128 threads =================
+            constexpr int CPR = D / 16;               // 16-element chunks a row
+            constexpr int NC = kTcKeys * CPR / 128;   // chunks a thread
+            const int th = tid - 256;
+            const uint32_t raw0 = kv_addr + STAGES * T::kTileBytes;
+            bool ok = true;
+            for (int it = 0; it < 2 * n; ++it) {
+                const int tile = k0 + it / 2, s = it % STAGES, rs = it % 2;
+                ok = wait_warp(&bars.raw_full[rs], it / 2) && (it < STAGES || wait_warp(&bars.kv_empty[s], it / STAGES - 1));
+                if (!ok) break;
+                const uint32_t raw = raw0 + uint32_t(rs) * T::kRawBytes, dst = kv_addr + uint32_t(s) * T::kTileBytes;
+                const uint32_t bad = s_bad[(it / 2) & 7];
+                const int u0 = tile * U, t0 = kt.tile(u0) * bs;
+                // a plain tile: every block is in the pool and (V) some row sees every token
+                const bool plain = bad == 0 && u0 >= kt.nsink && t0 + kTcKeys <= min(nfull, p_last + 1) && t0 >= dead_lo;
+                const uint16_t* tail = it % 2 ? p.c.v_tail : p.c.k_tail;
+#pragma unroll
+                for (int q = 0; q < NC; ++q) {
+                    const int x = th + q * 128, row = x / CPR, c = x % CPR;
+                    const uint32_t at = dst + uint32_t(row * 128 + (c / 4) * T::kSlab);
+                    const uint32_t ca = uint32_t((2 * c) % 8), sw = uint32_t(row & 7);
+                    uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
+                    int kind = 1;  // 0: zero, 1: codes, 2: tail
+                    if (!plain) {
+                        const int u = row >> lg, t = (kt.tile(u0 + u) << lg) + (row & (bs - 1));
+                        kind = ((bad >> u) & 1u) || (it % 2 && dead(t)) ? 0 : t >= nfull ? 2 : 1;
+                        if (kind == 2) {
+                            const uint16_t* r = tail + ((size_t(slot) * p.c.Hkv + kvh) * bs + (t - nfull)) * D + c * 16;
+                            lo = ldcg128(r);
+                            hi = ldcg128(r + 8);
+                        }
+                    }
+                    if (kind == 1) {
+                        const uint4 w = lds128(raw + uint32_t(x) * 16u);
+                        s8_to_bf16(w.x, lo.x, lo.y);
+                        s8_to_bf16(w.y, lo.z, lo.w);
+                        s8_to_bf16(w.z, hi.x, hi.y);
+                        s8_to_bf16(w.w, hi.z, hi.w);
+                    }
+                    sts128(at + ((ca ^ sw) << 4), lo);
+                    sts128(at + (((ca + 1) ^ sw) << 4), hi);
+                }
+                fence_proxy_async_smem();
+                mbar_arrive(bar(&bars.kv_full[s]));
+                mbar_arrive(bar(&bars.raw_empty[rs]));
+            }
+            if (!ok && lane == 0) report(p.c.err, kErrTimeout);
         }
-    } else {
+    } else if (INT8 && warp == 13) {
+        // ================= INT8: queries, codes and scales =================
+        if (lane == 0) {
+            prefetch_tensormap(&p.tm_q);
+            mbar_arrive_expect_tx(bar(&bars.q_full), uint32_t(nq) * T::kTileBytes);
+            for (int i = 0; i < nq; ++i)
+                for (int h = 0; h < D / 64; ++h)
+                    tma_load_4d(q_addr + i * T::kTileBytes + h * T::kSlab, &p.tm_q, h * 64, 0, kvh,
+                                sq.row0 + (r_first + i * kTcRows) / G, bar(&bars.q_full));
+        }
+        const uint32_t raw0 = kv_addr + STAGES * T::kTileBytes;
+        const uint32_t bytes = uint32_t(bs) * D;  // a block's rows of one kv head lie in a row
+        bool ok = true;
+        int issued = 0, id = -1;  // lane u: the pool block of unit u, or -1
+        for (int it = 0; it < 2 * n; ++it) {
+            const int tile = k0 + it / 2, rs = it % 2;
+            if (it % 2 == 0) {
+                id = -1;
+                bool miss = false;
+                if (lane < U) {
+                    const int u = tile * U + lane, t0 = kt.tile(u) * bs;
+                    float2 sc = make_float2(1.f, 1.f);
+                    if (u >= kt.n) {
+                        miss = true;
+                    } else if (t0 >= nfull) {
+                        miss = slot < 0 || slot >= p.c.max_slots;
+                        if (miss) report(p.c.err, kErrSlot);
+                    } else {
+                        id = table[t0 / bs];
+                        if (id < 0 || id >= p.c.num_blocks) {
+                            report(p.c.err, kErrBlockId);
+                            id = -1;
+                            miss = true;
+                        } else {
+                            sc = __ldcg(reinterpret_cast<const float2*>(p.c.scales) + size_t(id) * p.c.Hkv + kvh);
+                        }
+                    }
+                    s_sc[(it / 2) & 7][lane] = sc;
+                }
+                const uint32_t missing = __ballot_sync(kFull, miss);
+                if (lane == 0) s_bad[(it / 2) & 7] = missing;
+            }
+            if (it >= 2) ok = wait_warp(&bars.raw_empty[rs], it / 2 - 1);
+            if (!ok) break;
+            const uint32_t have = __ballot_sync(kFull, id >= 0);
+            const uint32_t full = bar(&bars.raw_full[rs]);
+            if (lane == 0) mbar_arrive_expect_tx(full, uint32_t(__popc(have)) * bytes);
+            __syncwarp();
+            if (id >= 0)
+                bulk_g2s(raw0 + uint32_t(rs) * T::kRawBytes + uint32_t(lane) * bytes,
+                         static_cast<const uint8_t*>(it % 2 ? p.c.v_pool : p.c.k_pool) +
+                             (size_t(id) * p.c.Hkv + kvh) * bytes, bytes, full);
+            issued = it + 1;
+        }
+        if (!ok) {  // let the copies in flight land before the CTA ends
+            for (int it = max(0, issued - 2); it < issued; ++it) (void)wait(&bars.raw_full[it % 2], it / 2);
+            if (lane == 0) report(p.c.err, kErrTimeout);
+        }
+    } else if (warp == kMmaWarp) {
       if (lane == 0) {
         // ================= the multiplies =================
         constexpr uint32_t kDescS = mma_desc_bf16(kTcKeys, false), kDescO = mma_desc_bf16(D, true);
