@@ -55,10 +55,6 @@ __device__ __forceinline__ KeyTiles key_tiles(int p_first, int p_last, int windo
     return kt;
 }
 
-// Registers a thread that window_tc_kernel is launched with.
-constexpr int kTcLaunchRegsBf16 = 168;
-constexpr int kTcLaunchRegsInt8 = 128;
-
 using WindowFn = void (*)(WindowParams);
 
 WindowFn window_rows_fn(int d, bool int8, int nt);

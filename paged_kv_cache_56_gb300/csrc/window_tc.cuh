@@ -41,18 +41,10 @@ constexpr float kTcAhead = 8.f;
 
 template <int D, bool INT8>
 struct TcTraits {
-    // warpgroups: softmax 0, softmax 1, then loader and multiplies together
-    // (bf16: warps 8 and 11) or apart (INT8: four loading warps, then warp 12)
+    // warps: softmax 0-7, the loader(s), the multiplies, INT8: the copies of codes
     static constexpr int kLoadWarps = INT8 ? 4 : 1;
-    static constexpr int kMmaWarp = INT8 ? 12 : 11;
-    static constexpr int kThreads = INT8 ? 512 : 384;
-    // Registers a thread after the warpgroups' split; their sum is what the
-    // block is launched with (65536 / threads, down to a multiple of 8).
-    static constexpr int kLaunchRegs = INT8 ? kTcLaunchRegsInt8 : kTcLaunchRegsBf16;
-    static constexpr int kSoftmaxRegs = INT8 ? 192 : 208;
-    static constexpr int kLoadRegs = INT8 ? 80 : 88;
-    static constexpr int kMmaRegs = INT8 ? 48 : 0;
-    static_assert(256 * kSoftmaxRegs + 128 * (kLoadRegs + kMmaRegs) == kThreads * kLaunchRegs, "register split");
+    static constexpr int kMmaWarp = 8 + kLoadWarps;
+    static constexpr int kThreads = (kMmaWarp + 1 + INT8) * 32;
     static constexpr int kTileBytes = kTcKeys * D * 2;          // one K or V tile (bf16) = one row tile of Q
     static constexpr int kStages = D == 128 ? 4 : 6;
     static constexpr int kRawStages = INT8 ? 2 : 0;             // int8 tiles on their way to bf16
@@ -172,7 +164,6 @@ window_tc_kernel(const __grid_constant__ WindowParams p) {
     const int slot = INT8 ? p.bt.slots[b] : 0;
 
     if (warp < 8) {
-        reg_inc<T::kSoftmaxRegs>();
         // ================= softmax of row tile i, a row a thread =================
         const int i = warp >> 2, row = r_first + tid;  // tid < 256: rows of the CTA in order
         const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
@@ -191,48 +182,69 @@ window_tc_kernel(const __grid_constant__ WindowParams p) {
             for (int jj = 0; jj < n; ++jj) {
                 if (!(ok = wait_warp(&bars.s_full[i], jj))) break;
                 tc_fence_after();
-                uint32_t r[128];
-                tmem_ld(reinterpret_cast<uint32_t(&)[64]>(r[0]), s_addr);
-                tmem_ld(reinterpret_cast<uint32_t(&)[64]>(r[64]), s_addr + 64);
                 const int u0 = (k0 + jj) * U;  // first block of the tile in the list
                 const uint32_t bad = s_bad[jj & 7];
-                const int t_first = kt.tile(u0) * bs;
-                float2 vs2[8];
-                if (INT8) {
+                const int t_first = kt.tile(u0) << lg;
+                const bool masked = bad != 0 || u0 < kt.nsink || t_first + kTcKeys - 1 > pf || t_first < pl - p.window + 1;
+                // Scores are worked on in four chunks of 32 columns, two register
+                // buffers taking turns, so that one chunk's load from tensor memory
+                // flies while the other is worked on. The maximum needs all four
+                // before the first weight, so they are read twice: 3, 2, 1, 0 and,
+                // chunk 0 still being there, 1, 2, 3. Weights of chunk c go over
+                // score columns 16c .. 16c + 15, which are used up by then.
+                uint32_t ra[32], rb[32];
+                // scales (INT8) and hides: chunk c of the tile
+                const auto finish = [&](uint32_t (&r)[32], int c) {
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        const float2 sc = s_sc[jj & 7][(c * 16) >> lg];
-                        vs2[c] = make_float2(sc.y, sc.y);
+                    for (int h = 0; h < 2; ++h) {
+                        const int col = c * 32 + h * 16, u = col >> lg;
+                        if (INT8) {
+                            const float ks = s_sc[jj & 7][u].x;
 #pragma unroll
-                        for (int e = 0; e < 16; e += 2) {
-                            const float2 x = mul2(make_float2(__uint_as_float(r[c * 16 + e]), __uint_as_float(r[c * 16 + e + 1])),
-                                                  make_float2(sc.x, sc.x));
-                            r[c * 16 + e] = __float_as_uint(x.x);
-                            r[c * 16 + e + 1] = __float_as_uint(x.y);
+                            for (int e = h * 16; e < h * 16 + 16; e += 2) {
+                                const float2 x = mul2(make_float2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])),
+                                                      make_float2(ks, ks));
+                                r[e] = __float_as_uint(x.x);
+                                r[e + 1] = __float_as_uint(x.y);
+                            }
+                        }
+                        if (masked) {
+                            const int t0 = (kt.tile(u0 + u) << lg) + (col & (bs - 1));
+                            // bit e: this row sees token t0 + e
+                            const auto below = [](int x) { return (1u << min(16, max(0, x))) - 1u; };
+                            uint32_t see = below(hi - t0 + 1) & (below(p.sinks - t0) | ~below(lo - t0));
+                            if ((bad >> u) & 1u) see = 0u;
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                if (!((see >> e) & 1u)) r[h * 16 + e] = 0xFF800000u;
                         }
                     }
-                }
-                const bool masked = bad != 0 || u0 < kt.nsink || t_first + kTcKeys - 1 > pf || t_first < pl - p.window + 1;
-                if (masked) {
+                };
+                float mx = -INFINITY, my = -INFINITY;
+                const auto maximum = [&](const uint32_t (&r)[32]) {
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        const int u = (c * 16) >> lg;
-                        const int t0 = (kt.tile(u0 + u) << lg) + ((c * 16) & (bs - 1));
-                        // bit e: this row sees token t0 + e
-                        const auto below = [](int x) { return (1u << min(16, max(0, x))) - 1u; };
-                        uint32_t see = below(hi - t0 + 1) & (below(p.sinks - t0) | ~below(lo - t0));
-                        if ((bad >> u) & 1u) see = 0u;
-#pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            if (!((see >> e) & 1u)) r[c * 16 + e] = 0xFF800000u;  // -inf
+                    for (int e = 0; e < 32; e += 4) {
+                        mx = fmaxf(fmaxf(mx, __uint_as_float(r[e])), __uint_as_float(r[e + 2]));
+                        my = fmaxf(fmaxf(my, __uint_as_float(r[e + 1])), __uint_as_float(r[e + 3]));
                     }
-                }
-                float mx = __uint_as_float(r[0]), my = __uint_as_float(r[1]);
-#pragma unroll
-                for (int e = 2; e < 128; e += 4) {
-                    mx = fmaxf(fmaxf(mx, __uint_as_float(r[e])), e + 2 < 128 ? __uint_as_float(r[e + 2]) : mx);
-                    my = fmaxf(fmaxf(my, __uint_as_float(r[e + 1])), e + 3 < 128 ? __uint_as_float(r[e + 3]) : my);
-                }
+                };
+                tmem_ld_start(ra, s_addr + 96);
+                tmem_ld_wait(ra);
+                tmem_ld_start(rb, s_addr + 64);
+                finish(ra, 3);
+                maximum(ra);
+                tmem_ld_wait(rb);
+                tmem_ld_start(ra, s_addr + 32);
+                finish(rb, 2);
+                maximum(rb);
+                tmem_ld_wait(ra);
+                tmem_ld_start(rb, s_addr);
+                finish(ra, 1);
+                maximum(ra);
+                tmem_ld_wait(rb);
+                tmem_ld_start(ra, s_addr + 32);
+                finish(rb, 0);
+                maximum(rb);
                 mx = fmaxf(mx, my);
                 const bool up = (mx - m_ref) * scale > kTcAhead;  // false while nothing has been seen
                 if (__any_sync(kFull, up)) {
@@ -241,7 +253,7 @@ window_tc_kernel(const __grid_constant__ WindowParams p) {
                     l2.x *= f;
                     l2.y *= f;
                     if (jj > 0) {
-#pragma unroll
+#pragma unroll 1
                         for (int c = 0; c < D; c += 32) {
                             uint32_t o[32];
                             tmem_ld(o, o_addr + c);
@@ -252,18 +264,34 @@ window_tc_kernel(const __grid_constant__ WindowParams p) {
                     }
                 }
                 const float neg = (m_ref == -INFINITY ? 0.f : -m_ref * scale) - kTcShift;
-                uint32_t w[2][32];
+                const auto weights = [&](const uint32_t (&r)[32], int c) {
+                    uint32_t w[16];
 #pragma unroll
-                for (int e = 0; e < 128; e += 2) {
-                    const float2 x = __ffma2_rn(make_float2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])),
-                                                make_float2(scale, scale), make_float2(neg, neg));
-                    float2 y = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-                    l2 = __fadd2_rn(l2, y);
-                    if (INT8) y = mul2(y, vs2[e / 16]);
-                    w[e / 64][e / 2 % 32] = f2_to_bf16x2(y.x, y.y);
-                }
-                tmem_st(s_addr, w[0]);
-                tmem_st(s_addr + 32, w[1]);
+                    for (int e = 0; e < 32; e += 2) {
+                        const float2 x = __ffma2_rn(make_float2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])),
+                                                    make_float2(scale, scale), make_float2(neg, neg));
+                        float2 y = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+                        l2 = __fadd2_rn(l2, y);
+                        if (INT8) {
+                            const float vs = s_sc[jj & 7][(c * 32 + (e & 16)) >> lg].y;
+                            y = mul2(y, make_float2(vs, vs));
+                        }
+                        w[e / 2] = f2_to_bf16x2(y.x, y.y);
+                    }
+                    tmem_st(s_addr + c * 16, w);
+                };
+                weights(rb, 0);
+                tmem_ld_wait(ra);
+                tmem_ld_start(rb, s_addr + 64);
+                finish(ra, 1);
+                weights(ra, 1);
+                tmem_ld_wait(rb);
+                tmem_ld_start(ra, s_addr + 96);
+                finish(rb, 2);
+                weights(rb, 2);
+                tmem_ld_wait(ra);
+                finish(ra, 3);
+                weights(ra, 3);
                 tmem_wait_st();
                 tc_fence_before();
                 mbar_arrive(bar(&bars.p_full[i]));
@@ -308,12 +336,7 @@ window_tc_kernel(const __grid_constant__ WindowParams p) {
             }
         }
         if (!ok && lane == 0) report(p.c.err, kErrTimeout);
-    } else if (warp < 12) {
-        reg_dec<T::kLoadRegs>();
-    } else {
-        reg_dec<INT8 ? T::kMmaRegs : 24>();
-    }
-    if (warp >= 8 && warp < 8 + T::kLoadWarps) {
+    } else if (warp < kMmaWarp) {
         if constexpr (!INT8) {
             // ================= loader: tensor copies through the block table =================
             if (lane == 0) {
@@ -416,39 +439,39 @@ window_tc_kernel(const __grid_constant__ WindowParams p) {
                 // a plain tile: every block is in the pool and (V) some row sees every token
                 const bool plain = bad == 0 && u0 >= kt.nsink && t0 + kTcKeys <= min(nfull, p_last + 1) && t0 >= dead_lo;
                 const uint16_t* tail = it % 2 ? p.c.v_tail : p.c.k_tail;
+                uint4 w[NC];  // all loads first: shared memory's latency is paid once a tile
+#pragma unroll
+                for (int q = 0; q < NC; ++q) w[q] = lds128(raw + uint32_t(th + q * 128) * 16u);
+                mbar_arrive(bar(&bars.raw_empty[rs]));
 #pragma unroll
                 for (int q = 0; q < NC; ++q) {
                     const int x = th + q * 128, row = x / CPR, c = x % CPR;
                     const uint32_t at = dst + uint32_t(row * 128 + (c / 4) * T::kSlab);
                     const uint32_t ca = uint32_t((2 * c) % 8), sw = uint32_t(row & 7);
-                    uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
-                    int kind = 1;  // 0: zero, 1: codes, 2: tail
+                    uint4 lo, hi;
+                    s8_to_bf16(w[q].x, lo.x, lo.y);
+                    s8_to_bf16(w[q].y, lo.z, lo.w);
+                    s8_to_bf16(w[q].z, hi.x, hi.y);
+                    s8_to_bf16(w[q].w, hi.z, hi.w);
                     if (!plain) {
                         const int u = row >> lg, t = (kt.tile(u0 + u) << lg) + (row & (bs - 1));
-                        kind = ((bad >> u) & 1u) || (it % 2 && dead(t)) ? 0 : t >= nfull ? 2 : 1;
-                        if (kind == 2) {
+                        if (((bad >> u) & 1u) || (it % 2 && dead(t))) {
+                            lo = hi = make_uint4(0u, 0u, 0u, 0u);
+                        } else if (t >= nfull) {
                             const uint16_t* r = tail + ((size_t(slot) * p.c.Hkv + kvh) * bs + (t - nfull)) * D + c * 16;
                             lo = ldcg128(r);
                             hi = ldcg128(r + 8);
                         }
-                    }
-                    if (kind == 1) {
-                        const uint4 w = lds128(raw + uint32_t(x) * 16u);
-                        s8_to_bf16(w.x, lo.x, lo.y);
-                        s8_to_bf16(w.y, lo.z, lo.w);
-                        s8_to_bf16(w.z, hi.x, hi.y);
-                        s8_to_bf16(w.w, hi.z, hi.w);
                     }
                     sts128(at + ((ca ^ sw) << 4), lo);
                     sts128(at + (((ca + 1) ^ sw) << 4), hi);
                 }
                 fence_proxy_async_smem();
                 mbar_arrive(bar(&bars.kv_full[s]));
-                mbar_arrive(bar(&bars.raw_empty[rs]));
             }
             if (!ok && lane == 0) report(p.c.err, kErrTimeout);
         }
-    } else if (INT8 && warp == 13) {
+    } else if (INT8 && warp == kMmaWarp + 1) {
         // ================= INT8: queries, codes and scales =================
         if (lane == 0) {
             prefetch_tensormap(&p.tm_q);
