@@ -42,7 +42,7 @@ constexpr float kTcAhead = 8.f;
 template <int D, bool INT8>
 struct TcTraits {
     // warps: softmax 0-7, the loader(s), the multiplies, INT8: the copies of codes
-    static constexpr int kLoadWarps = INT8 ? 4 : 1;
+    static constexpr int kLoadWarps = INT8 ? 4 : 2;
     static constexpr int kMmaWarp = 8 + kLoadWarps;
     static constexpr int kThreads = (kMmaWarp + 1 + INT8) * 32;
     static constexpr int kTileBytes = kTcKeys * D * 2;          // one K or V tile (bf16) = one row tile of Q
@@ -338,88 +338,86 @@ window_tc_kernel(const __grid_constant__ WindowParams p) {
         if (!ok && lane == 0) report(p.c.err, kErrTimeout);
     } else if (warp < kMmaWarp) {
         if constexpr (!INT8) {
-            // ================= loader: tensor copies through the block table =================
-            if (lane == 0) {
-                prefetch_tensormap(&p.tm_q);
-                prefetch_tensormap(&p.tm_k);
-                prefetch_tensormap(&p.tm_v);
-                mbar_arrive_expect_tx(bar(&bars.q_full), uint32_t(nq) * T::kTileBytes);
-                for (int i = 0; i < nq; ++i)
-                    for (int h = 0; h < D / 64; ++h)
-                        tma_load_4d(q_addr + i * T::kTileBytes + h * T::kSlab, &p.tm_q, h * 64, 0, kvh,
-                                    sq.row0 + (r_first + i * kTcRows) / G, bar(&bars.q_full));
-            }
-            int pending = -1, raw_phase = 0;  // the V item whose dead rows are still to be cleared
-            const auto clear_pending = [&] {
-                if (!wait_warp(&bars.raw_full[0], raw_phase)) return false;
-                ++raw_phase;
-                const int tile = k0 + pending / 2;
-                const uint32_t base = kv_addr + uint32_t(pending % STAGES) * T::kTileBytes;
-                for (int u = 0; u < U && tile * U + u < kt.n; ++u) {
-                    const int t0 = kt.tile(tile * U + u) * bs;
-                    for (int e = lane; e < bs * (D / 8); e += 32) {
-                        const int rr = e / (D / 8), ch = e % (D / 8);
-                        if (dead(t0 + rr))
-                            sts128(base + uint32_t((ch / 8) * T::kSlab + (u * bs + rr) * 128 + (ch % 8) * 16),
-                                   make_uint4(0u, 0u, 0u, 0u));
-                    }
+            // ================= loaders: tensor copies through the block table =================
+            // One warp for K (and Q), one for V: copies of 16 rows x 128 bytes are issued
+            // one by one, and a single warp's issue would not keep up with the multiplies.
+            // The ids come one tile ahead, so their latency is off the path.
+            const int role = warp - 8;  // 0: K, 1: V
+            const CUtensorMap* tm = role ? &p.tm_v : &p.tm_k;
+            const bool leader = elect_one();
+            if (leader) {
+                prefetch_tensormap(tm);
+                if (role == 0) {
+                    prefetch_tensormap(&p.tm_q);
+                    mbar_arrive_expect_tx(bar(&bars.q_full), uint32_t(nq) * T::kTileBytes);
+                    for (int i = 0; i < nq; ++i)
+                        for (int h = 0; h < D / 64; ++h)
+                            tma_load_4d(q_addr + i * T::kTileBytes + h * T::kSlab, &p.tm_q, h * 64, 0, kvh,
+                                        sq.row0 + (r_first + i * kTcRows) / G, bar(&bars.q_full));
                 }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(&bars.kv_full[pending % STAGES]));
-                pending = -1;
-                return true;
+            }
+            __syncwarp();
+            const auto entry = [&](int tile) {  // lane u: the table's entry for unit u of a tile
+                const int u = tile * U + lane;
+                return lane < U && u < kt.n ? table[kt.tile(u)] : -1;
             };
             bool ok = true;
-            int issued = 0;
-            int id = -1;      // lane u: the block of unit u of the tile
-            bool dirty = false;  // lane u: the unit is there and holds dead tokens
-            for (int it = 0; it < 2 * n && ok; ++it) {
-                const int tile = k0 + it / 2, s = it % STAGES;
-                if (it % 2 == 0) {
-                    id = p.c.num_blocks;  // behind the pool: the copy fills zeros
-                    bool miss = false;
-                    dirty = false;
-                    if (lane < U) {
-                        miss = true;
-                        const int u = tile * U + lane;
-                        if (u < kt.n) {
-                            const int t0 = kt.tile(u) * bs;
-                            const int x = table[t0 / bs];
-                            if (x >= 0 && x < p.c.num_blocks) {
-                                id = x;
-                                miss = false;
-                                dirty = t0 + bs - 1 > p_last || (t0 < dead_lo && t0 + bs > p.sinks);
-                            } else {
-                                report(p.c.err, kErrBlockId);
-                            }
+            uint32_t raw_phase = 0;
+            int jj = 0, next = entry(k0);
+            for (; jj < n; ++jj) {
+                const int tile = k0 + jj, it = 2 * jj + role, s = it % STAGES;
+                const int got = next, u = tile * U + lane;
+                if (jj + 1 < n) next = entry(tile + 1);
+                const bool there = got >= 0 && got < p.c.num_blocks;
+                const int id = there ? got : p.c.num_blocks;  // behind the pool: the copy fills zeros
+                bool fix = false;
+                if (role == 0) {
+                    if (lane < U && u < kt.n && !there) report(p.c.err, kErrBlockId);
+                    const uint32_t missing = __ballot_sync(kFull, lane < U && !there);
+                    if (lane == 0) s_bad[jj & 7] = missing;
+                } else {
+                    const int t0 = kt.tile(u) << lg;
+                    fix = __any_sync(kFull, there && (t0 + bs - 1 > p_last || (t0 < dead_lo && t0 + bs > p.sinks)));
+                }
+                if (it >= STAGES && !(ok = wait_warp(&bars.kv_empty[s], it / STAGES - 1))) break;
+                const uint32_t full = fix ? bar(&bars.raw_full[0]) : bar(&bars.kv_full[s]);
+                const uint32_t dst = kv_addr + uint32_t(s) * T::kTileBytes;
+                if (leader) mbar_arrive_expect_tx(full, T::kTileBytes);
+                __syncwarp();
+#pragma unroll
+                for (int x = 0; x < kTcKeys / 16; ++x) {
+                    if (x >= U) break;
+                    const int uid = __shfl_sync(kFull, id, x);
+                    if (leader) {
+#pragma unroll
+                        for (int h = 0; h < D / 64; ++h)
+                            tma_load_3d(dst + uint32_t(h * T::kSlab + x * bs * 128), tm, h * 128, kvh * bs, uid, full);
+                    }
+                }
+                if (fix) {
+                    // clear the rows of V that no row of the CTA sees
+                    if (!(ok = wait_warp(&bars.raw_full[0], raw_phase))) break;
+                    ++raw_phase;
+                    for (int x = 0; x < U && tile * U + x < kt.n; ++x) {
+                        const int t0 = kt.tile(tile * U + x) << lg;
+                        for (int e = lane; e < bs * (D / 8); e += 32) {
+                            const int rr = e / (D / 8), ch = e % (D / 8);
+                            if (dead(t0 + rr))
+                                sts128(dst + uint32_t((ch / 8) * T::kSlab + (x * bs + rr) * 128 + (ch % 8) * 16),
+                                       make_uint4(0u, 0u, 0u, 0u));
                         }
                     }
-                    const uint32_t missing = __ballot_sync(kFull, miss);
-                    if (lane == 0) s_bad[(it / 2) & 7] = missing;
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (leader) mbar_arrive(bar(&bars.kv_full[s]));
                 }
-                const bool fix = it % 2 == 1 && __any_sync(kFull, dirty);
-                // clear an earlier V tile once further copies are under way, and before the ring is full
-                if (pending >= 0 && (fix || it - pending >= 2)) ok = clear_pending();
-                if (ok && it >= STAGES) ok = wait_warp(&bars.kv_empty[s], it / STAGES - 1);
-                if (!ok) break;
-                const uint32_t full = fix ? bar(&bars.raw_full[0]) : bar(&bars.kv_full[s]);
-                if (lane == 0) mbar_arrive_expect_tx(full, T::kTileBytes);
-                __syncwarp();
-                // a lane copies block lane % U, half lane / U of its rows
-                const int u = lane % U, h = lane / U, uid = __shfl_sync(kFull, id, u);
-                if (h < D / 64)
-                    tma_load_3d(kv_addr + uint32_t(s) * T::kTileBytes + h * T::kSlab + u * bs * 128,
-                                it % 2 ? &p.tm_v : &p.tm_k, h * 128, kvh * bs, uid, full);
-                if (fix) pending = it;
-                issued = it + 1;
             }
-            if (ok && pending >= 0) ok = clear_pending();
             if (!ok) {
                 // let the copies in flight land before the CTA ends
-                if (pending >= 0) (void)wait(&bars.raw_full[0], raw_phase);
-                for (int it = max(0, issued - STAGES); it < issued; ++it)
-                    if (it != pending) (void)wait(&bars.kv_full[it % STAGES], it / STAGES);
+                for (int x = max(0, jj - STAGES / 2); x < jj; ++x) {
+                    const int it = 2 * x + role;
+                    (void)wait_warp(&bars.kv_full[it % STAGES], it / STAGES);
+                }
                 if (lane == 0) report(p.c.err, kErrTimeout);
             }
         } else {
@@ -530,55 +528,65 @@ window_tc_kernel(const __grid_constant__ WindowParams p) {
             if (lane == 0) report(p.c.err, kErrTimeout);
         }
     } else if (warp == kMmaWarp) {
-      if (lane == 0) {
         // ================= the multiplies =================
+        // The whole warp walks through the loop, so that addresses and descriptors
+        // stay warp-uniform; one thread issues. A step along K is an addition to a
+        // descriptor's address field (16-byte units).
         constexpr uint32_t kDescS = mma_desc_bf16(kTcKeys, false), kDescO = mma_desc_bf16(D, true);
-        const auto kv_tile = [&](int it) { return kv_addr + uint32_t(it % STAGES) * T::kTileBytes; };
-        const auto issue_s = [&](int i, int jj) {
-            const uint32_t qa = q_addr + uint32_t(i) * T::kTileBytes, ka = kv_tile(2 * jj);
+        constexpr uint64_t kTile16 = T::kTileBytes / 16;
+        const bool leader = elect_one();
+        const uint32_t tm = __shfl_sync(kFull, tmem, 0);
+        const uint64_t dq = smem_desc(q_addr, 16), dk = smem_desc(kv_addr, 16), dv = smem_desc(kv_addr, T::kSlab);
+        const auto issue_s = [&](int i, int stage) {
+            if (leader) {
 #pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks) {
-                const uint32_t off = uint32_t(ks / 4) * T::kSlab + uint32_t(ks % 4) * 32u;
-                mma_ss(s_col(i), smem_desc(qa + off, 16), smem_desc(ka + off, 16), kDescS, ks > 0);
+                for (int ks = 0; ks < D / 16; ++ks) {
+                    constexpr uint64_t kSlab16 = T::kSlab / 16;
+                    const uint64_t off = uint64_t(ks / 4) * kSlab16 + uint64_t(ks % 4) * 2u;
+                    mma_ss(tm + uint32_t(i) * 128u, dq + uint64_t(i) * kTile16 + off, dk + uint64_t(stage) * kTile16 + off,
+                           kDescS, ks > 0);
+                }
             }
         };
-        bool ok = wait(&bars.q_full, 0) && wait(&bars.kv_full[0], 0);
+        const auto commit = [&](const uint64_t* x) {
+            if (leader) mma_commit(bar(x));
+        };
+        bool ok = wait_warp(&bars.q_full, 0) && wait_warp(&bars.kv_full[0], 0);
         if (ok) {
             tc_fence_after();
             for (int i = 0; i < nq; ++i) {
                 issue_s(i, 0);
-                mma_commit(bar(&bars.s_full[i]));
+                commit(&bars.s_full[i]);
             }
-            mma_commit(bar(&bars.kv_empty[0]));
+            commit(&bars.kv_empty[0]);
         }
         for (int jj = 0; jj < n && ok; ++jj) {
-            const int iv = 2 * jj + 1, ik = 2 * jj + 2;
-            ok = wait(&bars.kv_full[iv % STAGES], iv / STAGES);
+            const int iv = 2 * jj + 1, ik = 2 * jj + 2, sv = iv % STAGES, sk = ik % STAGES;
+            ok = wait_warp(&bars.kv_full[sv], iv / STAGES);
             for (int i = 0; i < nq && ok; ++i) {
-                if (!(ok = wait(&bars.p_full[i], jj))) break;
+                if (!(ok = wait_warp(&bars.p_full[i], jj))) break;
                 tc_fence_after();
-                const uint32_t va = kv_tile(iv);
+                if (leader) {
 #pragma unroll
-                for (int ks = 0; ks < kTcKeys / 16; ++ks)
-                    mma_ts(o_col(i), s_col(i) + uint32_t(ks) * 8u, smem_desc(va + uint32_t(ks) * 2048u, T::kSlab), kDescO,
-                           jj > 0 || ks > 0);
-                if (i == nq - 1) mma_commit(bar(&bars.kv_empty[iv % STAGES]));
-                if (jj + 1 < n) {
-                    if (i == 0 && !(ok = wait(&bars.kv_full[ik % STAGES], ik / STAGES))) break;
-                    tc_fence_after();
-                    issue_s(i, jj + 1);
+                    for (int ks = 0; ks < kTcKeys / 16; ++ks)
+                        mma_ts(tm + 256u + uint32_t(i) * 128u, tm + uint32_t(i) * 128u + uint32_t(ks) * 8u,
+                               dv + uint64_t(sv) * kTile16 + uint64_t(ks) * 128u, kDescO, jj > 0 || ks > 0);
                 }
-                mma_commit(bar(&bars.s_full[i]));
-                if (i == nq - 1 && jj + 1 < n) mma_commit(bar(&bars.kv_empty[ik % STAGES]));
+                if (i == nq - 1) commit(&bars.kv_empty[sv]);
+                if (jj + 1 < n) {
+                    if (i == 0 && !(ok = wait_warp(&bars.kv_full[sk], ik / STAGES))) break;
+                    tc_fence_after();
+                    issue_s(i, sk);
+                }
+                commit(&bars.s_full[i]);
+                if (i == nq - 1 && jj + 1 < n) commit(&bars.kv_empty[sk]);
             }
         }
         if (!ok) {
-            mma_commit(bar(&bars.drain));
-            (void)wait_phase(bar(&bars.drain), 0);
-            report(p.c.err, kErrTimeout);
+            commit(&bars.drain);
+            (void)wait_warp(&bars.drain, 0);
+            if (lane == 0) report(p.c.err, kErrTimeout);
         }
-      }
-        __syncwarp();
     }
 
     // ---- the last split of the row tile to arrive merges all of them
