@@ -66,6 +66,11 @@ struct TcBars {
     uint64_t drain;
 };
 
+template <bool V>
+struct Const {
+    static constexpr bool value = V;
+};
+
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
 
 // Four int8 codes -> bf16, exact: a code with bit pattern s:m (one and seven
@@ -186,29 +191,21 @@ window_tc_kernel(const __grid_constant__ WindowParams p) {
                 const uint32_t bad = s_bad[jj & 7];
                 const int t_first = kt.tile(u0) << lg;
                 const bool masked = bad != 0 || u0 < kt.nsink || t_first + kTcKeys - 1 > pf || t_first < pl - p.window + 1;
-                // Scores are worked on in four chunks of 32 columns, two register
-                // buffers taking turns, so that one chunk's load from tensor memory
-                // flies while the other is worked on. The maximum needs all four
-                // before the first weight, so they are read twice: 3, 2, 1, 0 and,
-                // chunk 0 still being there, 1, 2, 3. Weights of chunk c go over
-                // score columns 16c .. 16c + 15, which are used up by then.
-                uint32_t ra[32], rb[32];
-                // scales (INT8) and hides: chunk c of the tile
-                const auto finish = [&](uint32_t (&r)[32], int c) {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int col = c * 32 + h * 16, u = col >> lg;
-                        if (INT8) {
-                            const float ks = s_sc[jj & 7][u].x;
-#pragma unroll
-                            for (int e = h * 16; e < h * 16 + 16; e += 2) {
-                                const float2 x = mul2(make_float2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])),
-                                                      make_float2(ks, ks));
-                                r[e] = __float_as_uint(x.x);
-                                r[e + 1] = __float_as_uint(x.y);
-                            }
-                        }
-                        if (masked) {
+                // One pass: weights against the reference as it stands, and the true
+                // maximum beside them. Where a row's maximum is too far ahead (its
+                // first tile, and rarely later) the reference follows, the sums and
+                // O_i are rescaled, and the pass is made again: the weights wait in
+                // registers (w), so the scores are still there. 16 columns at a time,
+                // one chunk's load in flight while the other is worked on.
+                uint32_t w[8][8];
+                float2 sum;
+                for (;;) {
+                    const float neg = (m_ref == -INFINITY ? 0.f : -m_ref * scale) - kTcShift;
+                    float mx = -INFINITY, my = -INFINITY;
+                    sum = make_float2(0.f, 0.f);
+                    const auto chunk = [&](auto hide, uint32_t (&r)[16], int c) {
+                        const int col = c * 16, u = col >> lg;
+                        if constexpr (hide.value) {
                             const int t0 = (kt.tile(u0 + u) << lg) + (col & (bs - 1));
                             // bit e: this row sees token t0 + e
                             const auto below = [](int x) { return (1u << min(16, max(0, x))) - 1u; };
@@ -216,38 +213,51 @@ window_tc_kernel(const __grid_constant__ WindowParams p) {
                             if ((bad >> u) & 1u) see = 0u;
 #pragma unroll
                             for (int e = 0; e < 16; ++e)
-                                if (!((see >> e) & 1u)) r[h * 16 + e] = 0xFF800000u;
+                                if (!((see >> e) & 1u)) r[e] = 0xFF800000u;
                         }
-                    }
-                };
-                float mx = -INFINITY, my = -INFINITY;
-                const auto maximum = [&](const uint32_t (&r)[32]) {
+                        float2 sc = make_float2(1.f, 1.f);  // INT8: the block's K and V scales
+                        if (INT8) sc = s_sc[jj & 7][u];
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        mx = fmaxf(fmaxf(mx, __uint_as_float(r[e])), __uint_as_float(r[e + 2]));
-                        my = fmaxf(fmaxf(my, __uint_as_float(r[e + 1])), __uint_as_float(r[e + 3]));
-                    }
-                };
-                tmem_ld_start(ra, s_addr + 96);
-                tmem_ld_wait(ra);
-                tmem_ld_start(rb, s_addr + 64);
-                finish(ra, 3);
-                maximum(ra);
-                tmem_ld_wait(rb);
-                tmem_ld_start(ra, s_addr + 32);
-                finish(rb, 2);
-                maximum(rb);
-                tmem_ld_wait(ra);
-                tmem_ld_start(rb, s_addr);
-                finish(ra, 1);
-                maximum(ra);
-                tmem_ld_wait(rb);
-                tmem_ld_start(ra, s_addr + 32);
-                finish(rb, 0);
-                maximum(rb);
-                mx = fmaxf(mx, my);
-                const bool up = (mx - m_ref) * scale > kTcAhead;  // false while nothing has been seen
-                if (__any_sync(kFull, up)) {
+                        for (int e = 0; e < 16; e += 4) {
+                            float2 x0 = make_float2(__uint_as_float(r[e]), __uint_as_float(r[e + 1]));
+                            float2 x1 = make_float2(__uint_as_float(r[e + 2]), __uint_as_float(r[e + 3]));
+                            if (INT8) {
+                                x0 = mul2(x0, make_float2(sc.x, sc.x));
+                                x1 = mul2(x1, make_float2(sc.x, sc.x));
+                            }
+                            mx = fmaxf(fmaxf(mx, x0.x), x1.x);
+                            my = fmaxf(fmaxf(my, x0.y), x1.y);
+                            x0 = __ffma2_rn(x0, make_float2(scale, scale), make_float2(neg, neg));
+                            x1 = __ffma2_rn(x1, make_float2(scale, scale), make_float2(neg, neg));
+                            x0 = make_float2(fast_exp2(x0.x), fast_exp2(x0.y));
+                            x1 = make_float2(fast_exp2(x1.x), fast_exp2(x1.y));
+                            sum = __fadd2_rn(sum, __fadd2_rn(x0, x1));
+                            if (INT8) {
+                                x0 = mul2(x0, make_float2(sc.y, sc.y));
+                                x1 = mul2(x1, make_float2(sc.y, sc.y));
+                            }
+                            w[c][e / 2] = f2_to_bf16x2(x0.x, x0.y);
+                            w[c][e / 2 + 1] = f2_to_bf16x2(x1.x, x1.y);
+                        }
+                    };
+                    const auto pass = [&](auto hide) {
+                        uint32_t ra[16], rb[16];
+                        tmem_ld_start(ra, s_addr);
+#pragma unroll
+                        for (int c = 0; c < 8; c += 2) {
+                            tmem_ld_wait(ra);
+                            tmem_ld_start(rb, s_addr + c * 16 + 16);
+                            chunk(hide, ra, c);
+                            tmem_ld_wait(rb);
+                            if (c < 6) tmem_ld_start(ra, s_addr + c * 16 + 32);
+                            chunk(hide, rb, c + 1);
+                        }
+                    };
+                    if (masked) pass(Const<true>{});
+                    else pass(Const<false>{});
+                    mx = fmaxf(mx, my);
+                    const bool up = (mx - m_ref) * scale > kTcAhead;  // false while nothing has been seen
+                    if (!__any_sync(kFull, up)) break;
                     const float f = up ? fast_exp2((m_ref - mx) * scale) : 1.f;
                     if (up) m_ref = mx;
                     l2.x *= f;
@@ -263,35 +273,9 @@ window_tc_kernel(const __grid_constant__ WindowParams p) {
                         }
                     }
                 }
-                const float neg = (m_ref == -INFINITY ? 0.f : -m_ref * scale) - kTcShift;
-                const auto weights = [&](const uint32_t (&r)[32], int c) {
-                    uint32_t w[16];
+                l2 = __fadd2_rn(l2, sum);
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        const float2 x = __ffma2_rn(make_float2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])),
-                                                    make_float2(scale, scale), make_float2(neg, neg));
-                        float2 y = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-                        l2 = __fadd2_rn(l2, y);
-                        if (INT8) {
-                            const float vs = s_sc[jj & 7][(c * 32 + (e & 16)) >> lg].y;
-                            y = mul2(y, make_float2(vs, vs));
-                        }
-                        w[e / 2] = f2_to_bf16x2(y.x, y.y);
-                    }
-                    tmem_st(s_addr + c * 16, w);
-                };
-                weights(rb, 0);
-                tmem_ld_wait(ra);
-                tmem_ld_start(rb, s_addr + 64);
-                finish(ra, 1);
-                weights(ra, 1);
-                tmem_ld_wait(rb);
-                tmem_ld_start(ra, s_addr + 96);
-                finish(rb, 2);
-                weights(rb, 2);
-                tmem_ld_wait(ra);
-                finish(ra, 3);
-                weights(ra, 3);
+                for (int c = 0; c < 8; ++c) tmem_st(s_addr + c * 8, w[c]);
                 tmem_wait_st();
                 tc_fence_before();
                 mbar_arrive(bar(&bars.p_full[i]));
@@ -461,8 +445,10 @@ window_tc_kernel(const __grid_constant__ WindowParams p) {
                             hi = ldcg128(r + 8);
                         }
                     }
-                    sts128(at + ((ca ^ sw) << 4), lo);
-                    sts128(at + (((ca + 1) ^ sw) << 4), hi);
+                    // the two slabs' threads take the halves in opposite order: different banks
+                    const bool second = c >= 4;
+                    sts128(at + (((ca + second) ^ sw) << 4), second ? hi : lo);
+                    sts128(at + (((ca + !second) ^ sw) << 4), second ? lo : hi);
                 }
                 fence_proxy_async_smem();
                 mbar_arrive(bar(&bars.kv_full[s]));
