@@ -1,12 +1,13 @@
 // Rows of the paged cache read back in token order (pkv_gather_kv), and the
 // checks that the chunk entry points share.
 //
-// One CTA per (16 tokens, sequence): their K and V rows of every kv head. A
-// thread moves 16 elements at a time -- 16 bytes of an INT8 row, 32 of a bf16
-// one -- with several loads in flight; consecutive threads take consecutive
-// elements of the output rows, so that the writes are whole lines and the
-// reads whole rows of a block. Bound by memory: every cached byte is read
-// once and every output byte written once.
+// One CTA per (16 tokens, sequence): their K and V rows of every kv head, 256
+// rows at a time. A thread first works out where one row lies and goes to --
+// the divisions and the block table are paid once a row -- then the CTA moves
+// the rows, 8 elements a thread and several loads in flight: consecutive
+// threads take consecutive elements of the output, so that writes are whole
+// lines and reads whole rows of a block. Bound by memory: every cached byte is
+// read once and every output byte written once.
 #include "batch.cuh"
 #include "host.h"
 
@@ -24,36 +25,18 @@ struct GatherParams {
 constexpr int kGatherThreads = 256;
 constexpr int kGatherTokens = 16;
 
-// 16 values as two bf16 pairs of words each, stored as bf16 or fp32.
-template <bool F32>
-__device__ __forceinline__ void store16(void* out, int64_t at, const float (&x)[16]) {
-    if (F32) {
-        float4* o = reinterpret_cast<float4*>(static_cast<float*>(out) + at);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] = make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
-    } else {
-        uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at);
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-            o[e] = make_uint4(f2_to_bf16x2(x[8 * e], x[8 * e + 1]), f2_to_bf16x2(x[8 * e + 2], x[8 * e + 3]),
-                              f2_to_bf16x2(x[8 * e + 4], x[8 * e + 5]), f2_to_bf16x2(x[8 * e + 6], x[8 * e + 7]));
-    }
-}
-
-__device__ __forceinline__ void bf16x8_to_f(const uint4& w, float* x) {
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const float2 f = bf16x2_to_f2(u[e]);
-        x[2 * e] = f.x;
-        x[2 * e + 1] = f.y;
-    }
-}
+struct GatherRow {
+    const uint8_t* src;  // nullptr: left out
+    float scale;         // INT8; 0: a bf16 row of the tail
+    uint32_t pad;
+    int64_t dst;         // element offset in the outputs
+};
 
 template <int D, bool INT8, bool F32>
 __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const __grid_constant__ GatherParams p) {
-    constexpr int PR = D / 16;
+    constexpr int CH = D / 8;  // pieces of 8 elements a row
     __shared__ int s_id[kGatherTokens];  // block of each token; -1: from the tail; -2: left out
+    __shared__ GatherRow s_row[kGatherThreads];
     pdl_wait();
     pdl_launch_dependents();
     const int b = blockIdx.y, tid = threadIdx.x;
@@ -85,59 +68,83 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const __grid_con
         }
         s_id[tid] = id;
     }
-    __syncthreads();
 
-    constexpr int NB = 4;  // loads of 16 elements in flight a thread
-    const int items = 2 * m * Hkv * PR;
-    for (int i = tid; i < items; i += NB * kGatherThreads) {
-        uint4 w[NB][2];
-        float sc[NB];
-#pragma unroll
-        for (int u = 0; u < NB; ++u) {
-            const int e = i + u * kGatherThreads;
-            if (e >= items) continue;
-            const int c = e % PR, h = e / PR % Hkv, tl = e / (PR * Hkv) % m, kv = e / (PR * Hkv * m);
+    // rows in the order (token, kv head) of the outputs, all of K, then all of V
+    const int per = m * Hkv;
+    for (int r0 = 0; r0 < 2 * per; r0 += kGatherThreads) {
+        const int rows = min(kGatherThreads, 2 * per - r0);
+        __syncthreads();
+        if (tid < rows) {
+            const int kv = r0 + tid >= per, e = r0 + tid - kv * per, tl = e / Hkv, h = e % Hkv;
             const int id = s_id[tl], off = (t_first + i0 + tl) % bs;
+            GatherRow r;
+            r.src = nullptr;
+            r.scale = 0.f;
+            r.dst = int64_t(sq.row0 + i0 + tl) * p.out_stride + h * D;
             if (id >= 0) {
-                const size_t row = (size_t(id) * Hkv + h) * bs + off;
-                const uint8_t* pool = static_cast<const uint8_t*>(kv ? p.c.v_pool : p.c.k_pool);
-                if (INT8) {
-                    w[u][0] = ldg128(pool + row * D + c * 16);
-                    sc[u] = __ldg(p.c.scales + (size_t(id) * Hkv + h) * 2 + kv);
-                } else {
-                    w[u][0] = ldg128(pool + (row * D + c * 16) * 2);
-                    w[u][1] = ldg128(pool + (row * D + c * 16) * 2 + 16);
-                }
+                r.src = static_cast<const uint8_t*>(kv ? p.c.v_pool : p.c.k_pool) +
+                        ((size_t(id) * Hkv + h) * bs + off) * D * (INT8 ? 1 : 2);
+                if (INT8) r.scale = __ldg(p.c.scales + (size_t(id) * Hkv + h) * 2 + kv);
             } else if (INT8 && id == -1) {
-                const uint16_t* r = (kv ? p.c.v_tail : p.c.k_tail) + ((size_t(slot) * Hkv + h) * bs + off) * D + c * 16;
-                w[u][0] = ldg128(r);
-                w[u][1] = ldg128(r + 8);
+                r.src = reinterpret_cast<const uint8_t*>((kv ? p.c.v_tail : p.c.k_tail) +
+                                                         ((size_t(slot) * Hkv + h) * bs + off) * D);
             }
+            r.pad = uint32_t(kv);
+            s_row[tid] = r;
         }
+        __syncthreads();
+        constexpr int NB = 8;  // loads in flight a thread
+#pragma unroll 1
+        for (int i = tid; i < rows * CH; i += NB * kGatherThreads) {
+            uint4 w[NB];
 #pragma unroll
-        for (int u = 0; u < NB; ++u) {
-            const int e = i + u * kGatherThreads;
-            if (e >= items) continue;
-            const int c = e % PR, h = e / PR % Hkv, tl = e / (PR * Hkv) % m, kv = e / (PR * Hkv * m);
-            const int id = s_id[tl];
-            if (id == -2) continue;
-            float x[16];
-            if (INT8 && id >= 0) {
-                const uint32_t q[4] = {w[u][0].x, w[u][0].y, w[u][0].z, w[u][0].w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    float2 lo, hi;
-                    s8x4_to_f4(q[k], lo, hi);
-                    x[4 * k] = lo.x * sc[u];
-                    x[4 * k + 1] = lo.y * sc[u];
-                    x[4 * k + 2] = hi.x * sc[u];
-                    x[4 * k + 3] = hi.y * sc[u];
+            for (int u = 0; u < NB; ++u) {
+                const int e = i + u * kGatherThreads;
+                if (e >= rows * CH) break;
+                const GatherRow& r = s_row[e / CH];
+                if (!r.src) continue;
+                if (INT8 && r.scale != 0.f) {
+                    const uint2 x = __ldg(reinterpret_cast<const uint2*>(r.src + e % CH * 8));
+                    w[u].x = x.x;
+                    w[u].y = x.y;
+                } else {
+                    w[u] = ldg128(r.src + e % CH * 16);
                 }
-            } else {
-                bf16x8_to_f(w[u][0], x);
-                bf16x8_to_f(w[u][1], x + 8);
             }
-            store16<F32>(kv ? p.v_out : p.k_out, int64_t(sq.row0 + i0 + tl) * p.out_stride + h * D + c * 16, x);
+#pragma unroll
+            for (int u = 0; u < NB; ++u) {
+                const int e = i + u * kGatherThreads;
+                if (e >= rows * CH) break;
+                const GatherRow& r = s_row[e / CH];
+                if (!r.src) continue;
+                void* out = r.pad ? p.v_out : p.k_out;
+                const int64_t at = r.dst + e % CH * 8;
+                if (!F32 && (!INT8 || r.scale == 0.f)) {
+                    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at) = w[u];
+                    continue;
+                }
+                float2 x[4];
+                if (INT8 && r.scale != 0.f) {
+                    s8x4_to_f4(w[u].x, x[0], x[1]);
+                    s8x4_to_f4(w[u].y, x[2], x[3]);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) x[k] = make_float2(x[k].x * r.scale, x[k].y * r.scale);
+                } else {
+                    x[0] = bf16x2_to_f2(w[u].x);
+                    x[1] = bf16x2_to_f2(w[u].y);
+                    x[2] = bf16x2_to_f2(w[u].z);
+                    x[3] = bf16x2_to_f2(w[u].w);
+                }
+                if (F32) {
+                    float4* o = reinterpret_cast<float4*>(static_cast<float*>(out) + at);
+                    o[0] = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
+                    o[1] = make_float4(x[2].x, x[2].y, x[3].x, x[3].y);
+                } else {
+                    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at) =
+                        make_uint4(f2_to_bf16x2(x[0].x, x[0].y), f2_to_bf16x2(x[1].x, x[1].y),
+                                   f2_to_bf16x2(x[2].x, x[2].y), f2_to_bf16x2(x[3].x, x[3].y));
+                }
+            }
         }
     }
 }

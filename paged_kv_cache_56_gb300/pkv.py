@@ -560,9 +560,16 @@ def _rows(t: torch.Tensor, name: str, batch: BatchDesc, heads: int, dim: int, dt
     return t.data_ptr(), stride[0] if shape[0] > 1 else max(stride[0], heads * dim)
 
 
+# the current stream's handle without a Stream object around it, which costs
+# more than the launch of a small kernel
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _batch_stream(batch: BatchDesc, stream) -> int:
     if batch.device.index != torch.cuda.current_device():
         raise ValueError(f"the batch is on {batch.device}, which is not the current device")
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(batch.device.index)
     return _stream(stream)
 
 
