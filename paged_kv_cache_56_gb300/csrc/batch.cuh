@@ -57,4 +57,36 @@ __device__ __forceinline__ SeqRange seq_range(const BatchView& bt, int b, int bs
     return s;
 }
 
+// Work of ragged sequences as one list: sequence 0's count(0) items, then
+// sequence 1's, and so on. Finds item `item`; every lane of the warp calls it
+// and gets the same answer. b == -1: past the end.
+struct WorkItem {
+    int b, i;
+};
+template <class Count>
+__device__ __forceinline__ WorkItem locate(int item, int B, Count count) {
+    const int lane = int(threadIdx.x) & 31;
+    for (int b0 = 0; b0 < B; b0 += 32) {
+        const int mine = b0 + lane < B ? count(b0 + lane) : 0;
+        int upto = mine;  // items of this lane's sequence and those before it
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(kFull, upto, o);
+            if (lane >= o) upto += x;
+        }
+        const uint32_t past = __ballot_sync(kFull, item < upto);
+        if (past) {
+            const int l = __ffs(past) - 1;
+            return WorkItem{b0 + l, item - __shfl_sync(kFull, upto - mine, l)};
+        }
+        item -= __shfl_sync(kFull, upto, 31);
+    }
+    return WorkItem{-1, 0};
+}
+
+// Reports what is wrong with the batch's lengths: one CTA a launch.
+__device__ __forceinline__ void check_lengths(const BatchView& bt, int bs, int32_t* err) {
+    for (int b = int(threadIdx.x); b < bt.B; b += int(blockDim.x)) (void)seq_range(bt, b, bs, err, true);
+}
+
 }  // namespace pkv

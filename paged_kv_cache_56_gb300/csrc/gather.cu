@@ -8,6 +8,8 @@
 // threads take consecutive elements of the output, so that writes are whole
 // lines and reads whole rows of a block. Bound by memory: every cached byte is
 // read once and every output byte written once.
+#include <algorithm>
+
 #include "batch.cuh"
 #include "host.h"
 
@@ -20,6 +22,7 @@ struct GatherParams {
     void* k_out;
     void* v_out;
     int64_t out_stride;
+    int32_t ragged;
 };
 
 constexpr int kGatherThreads = 256;
@@ -39,15 +42,29 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const __grid_con
     __shared__ GatherRow s_row[kGatherThreads];
     pdl_wait();
     pdl_launch_dependents();
-    const int b = blockIdx.y, tid = threadIdx.x;
-    const SeqRange sq = seq_range(p.bt, b, p.c.bs, p.c.err, tid == 0 && blockIdx.x == 0);
-    const int i0 = int(blockIdx.x) * kGatherTokens;
+    const int tid = threadIdx.x;
+    // one CTA a sequence at most, or the x-th of all sequences' CTAs and one
+    // more that checks the lengths
+    WorkItem it{int(blockIdx.x), 0};
+    if (p.ragged) {
+        if (blockIdx.x == gridDim.x - 1) {
+            check_lengths(p.bt, p.c.bs, p.c.err);
+            return;
+        }
+        it = locate(int(blockIdx.x), p.bt.B, [&](int s) {
+            return (seq_range(p.bt, s, p.c.bs, nullptr, false).n + kGatherTokens - 1) / kGatherTokens;
+        });
+        if (it.b < 0) return;
+    }
+    const int b = it.b;
+    const SeqRange sq = seq_range(p.bt, b, p.c.bs, p.c.err, !p.ragged && tid == 0);
+    const int i0 = it.i * kGatherTokens;
     if (i0 >= sq.n || (sq.bad && !p.first)) return;
     const int t_first = p.first ? p.first[b] : sq.ctx - sq.n;
     // with `first` the rows may be any range inside the context
     if (p.first && (t_first < 0 || sq.ctx < 0 || int64_t(sq.ctx) > int64_t(p.bt.max_blocks) * p.c.bs ||
                     int64_t(t_first) + sq.n > sq.ctx)) {
-        if (tid == 0 && blockIdx.x == 0) report(p.c.err, kErrCtxLen);
+        if (tid == 0 && i0 == 0) report(p.c.err, kErrCtxLen);
         return;
     }
     const int m = min(kGatherTokens, sq.n - i0), Hkv = p.c.Hkv, bs = p.c.bs;
@@ -189,7 +206,9 @@ extern "C" int pkv_gather_kv(const pkv_cache_desc* c, const pkv_batch_desc* batc
     p.k_out = k_out;
     p.v_out = v_out;
     p.out_stride = out_stride;
-    const dim3 grid(unsigned((batch->max_tokens - 1) / kGatherTokens + 1), unsigned(batch->B));
+    const int64_t most = (batch->max_tokens - 1) / kGatherTokens + 1;
+    p.ragged = most > 1;
+    const dim3 grid(unsigned(std::min(most * batch->B, batch->num_tokens / kGatherTokens + int64_t(batch->B)) + p.ragged));
     const bool int8 = c->dtype == PKV_DTYPE_INT8;
     void (*fn)(GatherParams) = nullptr;
     if (c->head_dim == 128)

@@ -1,11 +1,13 @@
 // Rotary turn of a batch's new q and k rows fused with the write of k and v
 // into the paged cache (pkv_rope_append).
 //
-// One CTA per (chunk of CT tokens aligned to the cache's blocks, kv head,
-// sequence): it turns the chunk's rows of the kv head and of its group of
-// query heads, so q, k and v are read once and the cache is written once. In
-// INT8 mode CT is the block size and the CTA that holds a full block
-// quantizes it from registers: the block's bf16 rows never go to memory.
+// One CTA per (chunk of CT tokens aligned to the cache's blocks, group of kv
+// heads); a thread has one token and one pair of 16-byte chunks of a row -- the
+// eight pairs of elements that turn by the same angles in every head -- so it
+// works out its eight angles once, keeps their sines and cosines in registers
+// and walks through the heads, four rows in flight. In INT8 mode CT is the
+// block size and a full block is quantized from registers: its bf16 rows
+// never go to memory, and the only shared memory is the block's maximum.
 //
 // Angles. The position is an integer p, so only the fraction of p * f / 2 pi
 // matters. f / 2 pi modulo 1 is held as a 64-bit binary fraction u -- the fp64
@@ -18,6 +20,8 @@
 //
 // Bound by memory: 2 * (Hq + Hkv + Hkv) * d bytes read a token, and as much
 // written (the INT8 cache half of its part).
+#include <algorithm>
+
 #include "batch.cuh"
 #include "host.h"
 
@@ -35,11 +39,11 @@ struct RopeParams {
     int64_t q_stride, k_stride, v_stride, q_out_stride;
     int32_t half;  // rotary_dim / 2 (0: nothing turns)
     int32_t interleaved;
-    int32_t heads;  // kv heads a CTA
+    int32_t heads;   // kv heads a CTA
+    int32_t groups;  // CTAs a chunk: neighbours in the grid, as their rows are in memory
+    int32_t ragged;
     float scale;
 };
-
-constexpr int kRopeThreads = 256;
 
 // 16 elements of a row: two 16-byte chunks, at element offsets lo and hi.
 struct Pair16 {
@@ -58,35 +62,28 @@ __device__ __forceinline__ void pair_offsets(int i, int half, bool interleaved, 
     }
 }
 
-// (cos, sin) of a token's pairs in shared memory: pair 8 i + k at k * (half / 8)
-// + i, so that threads of neighbouring i read neighbouring entries; tokens are
-// half + 8 entries apart, which puts two tokens' entries in different banks.
-__device__ __forceinline__ int cs_stride(int half) { return half + 8; }
-
-// Turns the i-th pair of chunks of a row; cs: its token's entries.
-__device__ __forceinline__ void turn(Pair16& w, int i, int half, bool interleaved, const float2* cs) {
-    const int n = half / 8;
-    if (i >= n) return;
-    uint32_t x[4] = {w.a.x, w.a.y, w.a.z, w.a.w}, y[4] = {w.b.x, w.b.y, w.b.z, w.b.w};
-    if (interleaved) {
+// Turns a pair of chunks by the thread's eight angles, two pairs of elements at
+// a time in packed fp32.
+struct Angles {
+    float2 c[4], s[4];  // of pairs 2e and 2e + 1
+};
+template <bool INTER>
+__device__ __forceinline__ void turn_pairs(Pair16& w, const Angles& an) {
+    uint32_t x[8] = {w.a.x, w.a.y, w.a.z, w.a.w, w.b.x, w.b.y, w.b.z, w.b.w};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float2 p = bf16x2_to_f2(x[e]), r = bf16x2_to_f2(y[e]);
-            const float2 c0 = cs[e * n + i], c1 = cs[(e + 4) * n + i];
-            x[e] = f2_to_bf16x2(p.x * c0.x - p.y * c0.y, p.y * c0.x + p.x * c0.y);
-            y[e] = f2_to_bf16x2(r.x * c1.x - r.y * c1.y, r.y * c1.x + r.x * c1.y);
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float2 p = bf16x2_to_f2(x[e]), r = bf16x2_to_f2(y[e]);
-            const float2 c0 = cs[2 * e * n + i], c1 = cs[(2 * e + 1) * n + i];
-            x[e] = f2_to_bf16x2(p.x * c0.x - r.x * c0.y, p.y * c1.x - r.y * c1.y);
-            y[e] = f2_to_bf16x2(r.x * c0.x + p.x * c0.y, r.y * c1.x + p.y * c1.y);
-        }
+    for (int e = 0; e < 4; ++e) {
+        const uint32_t a = INTER ? x[2 * e] : x[e], b = INTER ? x[2 * e + 1] : x[e + 4];
+        // (p, q): the first and second elements of the two pairs
+        const float2 p = INTER ? make_float2(__uint_as_float(a << 16), __uint_as_float(b << 16)) : bf16x2_to_f2(a);
+        const float2 q = INTER ? make_float2(__uint_as_float(a & 0xFFFF0000u), __uint_as_float(b & 0xFFFF0000u))
+                               : bf16x2_to_f2(b);
+        const float2 ns = make_float2(-an.s[e].x, -an.s[e].y);
+        const float2 u = __ffma2_rn(p, an.c[e], __fmul2_rn(q, ns)), v = __ffma2_rn(q, an.c[e], __fmul2_rn(p, an.s[e]));
+        x[INTER ? 2 * e : e] = INTER ? f2_to_bf16x2(u.x, v.x) : f2_to_bf16x2(u.x, u.y);
+        x[INTER ? 2 * e + 1 : e + 4] = INTER ? f2_to_bf16x2(u.y, v.y) : f2_to_bf16x2(v.x, v.y);
     }
     w.a = make_uint4(x[0], x[1], x[2], x[3]);
-    w.b = make_uint4(y[0], y[1], y[2], y[3]);
+    w.b = make_uint4(x[4], x[5], x[6], x[7]);
 }
 
 // f / (2 pi) modulo 1 in units of 2^-64: the significand (53 bits, put to the
@@ -111,64 +108,108 @@ __device__ __forceinline__ unsigned long long turns_of(double f) {
     return bits >> 63 ? 0ull - u : u;
 }
 
-__device__ __forceinline__ float absmax8(const uint4& w) {
+// Sine and cosine of a / 2^32 turns. The nearest quarter turn is taken off in
+// integers; on the rest, |x| <= pi/4, the Taylor sums through x^9 and x^8 are
+// off by less than x^11/11! < 2e-9 and x^10/10! < 3e-8, fp32's own rounding.
+__device__ __forceinline__ void sincos_turn(uint32_t a, float& sn, float& cn) {
+    const uint32_t quarter = (a + 0x20000000u) >> 30;
+    const float x = float(int32_t(a - (quarter << 30))) * 1.4629180792671596e-9f;  // 2 pi / 2^32
+    const float y = x * x;
+    float s = fmaf(y, 1.f / 362880.f, -1.f / 5040.f);
+    s = fmaf(y, s, 1.f / 120.f);
+    s = fmaf(y, s, -1.f / 6.f);
+    s = fmaf(x * y, s, x);
+    float c = fmaf(y, 1.f / 40320.f, -1.f / 720.f);
+    c = fmaf(y, c, 1.f / 24.f);
+    c = fmaf(y, c, -0.5f);
+    c = fmaf(y, c, 1.f);
+    // a quarter turn on: (sin, cos) -> (cos, -sin)
+    const bool odd = quarter & 1u;
+    const float u = odd ? c : s, v = odd ? s : c;
+    sn = (quarter & 2u) ? -u : u;
+    cn = ((quarter + 1u) & 2u) ? -v : v;
+}
+
+// Largest |x| of eight bf16 values, as bf16 pairs (not-a-numbers do not count).
+__device__ __forceinline__ __nv_bfloat162 absmax8(const uint4& w, __nv_bfloat162 m) {
     const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-    float m = 0.f;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const float2 f = bf16x2_to_f2(x[e]);
-        m = fmaxf(m, fmaxf(fabsf(f.x), fabsf(f.y)));
-    }
+    for (int e = 0; e < 4; ++e) m = __hmax2(m, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&x[e])));
     return m;
 }
 
-// Eight codes clamp(rint(x / scale)) as the cache's quantizer defines them (see
-// quantize_slab), inv = 1 / scale. x * inv is off by at most 127 * 2^-22 < 4e-5
-// from the rounded quotient, so away from a tie it rounds to the same integer;
-// within 1e-4 of one the division decides (one value in 5000).
-__device__ __forceinline__ int code1(float x, float scale, float inv) {
-    const float t = x * inv;
-    int q = __float2int_rn(t);
-    if (fabsf(t - float(q)) > 0.4999f) q = __float2int_rn(__fdiv_rn(x, scale));
-    return min(127, max(-127, q));
-}
+// Eight codes rint(x / scale) as the cache's quantizer defines them (see
+// quantize_slab), with the quotient rounded to fp32 first. inv is the rounded
+// reciprocal; from q = x * inv, q + (x - q * scale) * inv is within an ulp and,
+// by Markstein's theorem (a quotient within an ulp, a correctly rounded
+// reciprocal, the remainder by a fused multiply-add), the same step again gives
+// the correctly rounded quotient. Ties are common here (bf16 over bf16 * 127),
+// so that a branch for them would be taken by most warps. |q| <= 127 but for
+// rounding, so no code passes +-127. Not-a-numbers become 0.
 __device__ __forceinline__ uint2 codes8(const uint4& w, float scale, float inv) {
     const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-    uint32_t out[2] = {0u, 0u};
+    const float2 i2 = make_float2(inv, inv), ns = make_float2(-scale, -scale);
+    uint32_t out[2];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const float2 f = bf16x2_to_f2(x[e]);
-        const int q0 = code1(f.x, scale, inv), q1 = code1(f.y, scale, inv);
-        out[e >> 1] |= ((uint32_t(q0) & 0xFFu) | ((uint32_t(q1) & 0xFFu) << 8)) << (16 * (e & 1));
+    for (int h = 0; h < 2; ++h) {
+        int n[4];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const float2 f = bf16x2_to_f2(x[2 * h + e]);
+            float2 q = __fmul2_rn(f, i2);
+            q = __ffma2_rn(__ffma2_rn(q, ns, f), i2, q);
+            q = __ffma2_rn(__ffma2_rn(q, ns, f), i2, q);
+            n[2 * e] = __float2int_rn(q.x);
+            n[2 * e + 1] = __float2int_rn(q.y);
+        }
+        uint32_t upper;
+        asm("cvt.pack.sat.s8.s32.b32 %0, %1, %2, 0;" : "=r"(upper) : "r"(n[3]), "r"(n[2]));
+        asm("cvt.pack.sat.s8.s32.b32 %0, %1, %2, %3;" : "=r"(out[h]) : "r"(n[1]), "r"(n[0]), "r"(upper));
     }
     return make_uint2(out[0], out[1]);
 }
 
 template <int D, bool INT8, int CT>
-__global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_constant__ RopeParams p) {
-    constexpr int PR = D / 16;                             // chunk pairs a row
-    constexpr int HT = kRopeThreads / 2;                   // threads for K, and for V
-    constexpr int NI = (CT * PR + HT - 1) / HT;            // chunk pairs a thread holds of K or V
-    constexpr int NB = 4;                                  // chunk pairs of q in flight a thread
-    __shared__ float2 cs[CT * (D / 2 + 8)];
+__global__ void __launch_bounds__(CT * D / 16, CT == 64 ? 2048 / (CT * D / 16) / 2 : (INT8 ? 768 : 896) / (CT * D / 16))
+rope_append_kernel(const __grid_constant__ RopeParams p) {
+    constexpr int PR = D / 16;               // chunk pairs a row
+    constexpr int THREADS = CT * PR;
+    constexpr int HB = 1;                    // kv heads at a time: their K and V rows are in flight together
+    constexpr int NB = 2;                    // query rows in flight
     __shared__ unsigned long long s_turns[D / 2];
-    __shared__ float s_max[kRopeThreads / 32];
+    __shared__ float s_max[2 * HB][THREADS / 32];
     pdl_wait();
     pdl_launch_dependents();
 
-    const int b = blockIdx.z, tid = threadIdx.x, half = p.half;
-    const int G = p.c.Hq / p.c.Hkv, lgG = 31 - __clz(G);   // 1, 2, 4 or 8
-    const SeqRange sq = seq_range(p.bt, b, p.c.bs, p.c.err, tid == 0 && blockIdx.y == 0 && blockIdx.x == 0);
+    const int tid = threadIdx.x, half = p.half;
+    const int G = p.c.Hq / p.c.Hkv;
+    if (tid < half) s_turns[tid] = turns_of(__ldg(p.inv_freq + tid));
+    // one chunk a sequence at most: item x is sequence x; otherwise the x-th of
+    // the chunks of all sequences, and one more CTA that checks the lengths
+    const int item = int(blockIdx.x) / p.groups, group = int(blockIdx.x) % p.groups;
+    WorkItem it{item, 0};
+    if (p.ragged) {
+        if (blockIdx.x == gridDim.x - 1) {
+            check_lengths(p.bt, p.c.bs, p.c.err);
+            return;
+        }
+        it = locate(item, p.bt.B, [&](int s) {
+            const SeqRange r = seq_range(p.bt, s, p.c.bs, nullptr, false);
+            return r.n == 0 || r.bad ? 0 : (r.ctx - 1) / CT - (r.ctx - r.n) / CT + 1;
+        });
+        if (it.b < 0) return;
+    }
+    const int b = it.b;
+    const SeqRange sq = seq_range(p.bt, b, p.c.bs, p.c.err, !p.ragged && group == 0 && tid == 0);
     if (sq.n == 0 || sq.bad) return;
     const int start = sq.ctx - sq.n;                       // first new token
     const int chunk0 = start / CT, last = (sq.ctx - 1) / CT;
-    const int chunk = chunk0 + int(blockIdx.x);
+    const int chunk = chunk0 + it.i;
     if (chunk > last) return;
     const int slot = INT8 ? p.bt.slots[b] : 0;
     const bool slot_ok = !INT8 || (slot >= 0 && slot < p.c.max_slots);
     const int32_t* table = p.bt.tables + size_t(b) * p.bt.max_blocks;
     const bool inter = p.interleaved != 0;
-
     // INT8: the CTA of a block that earlier tokens began reads their rows from
     // the tail; if the last block is another one and partly filled, its rows
     // go to the same tail. So that CTA writes them too, after its reads, and
@@ -177,77 +218,69 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_
     const bool last_partial = INT8 && sq.ctx % CT != 0;
     const int jobs = (from_tail && last_partial && chunk == chunk0 && last > chunk0) ? 2 : 1;
     const bool leave_kv = from_tail && last_partial && chunk == last && last > chunk0;
-    const int kv = tid / HT, th = tid % HT;  // half of the threads take K, half V
-    const int kvh0 = int(blockIdx.y) * p.heads, kvh1 = min(p.c.Hkv, kvh0 + p.heads);
+    const int kvh0 = group * p.heads, kvh1 = min(p.c.Hkv, kvh0 + p.heads);
+    const int tl = tid / PR, pr = tid % PR;                // this thread's token of the chunk, chunk pair of a row
+    int lo, hi;
+    pair_offsets(pr, half, inter, lo, hi);
+    const bool turns = pr < half / 8;
+    const auto turn = [&](Pair16& w, const Angles& an) {
+        if (!turns) return;
+        if (inter) turn_pairs<true>(w, an);
+        else turn_pairs<false>(w, an);
+    };
 
     for (int job = 0; job < jobs; ++job) {
-        const int base = (job == 0 ? chunk : last) * CT;
-        const int t0 = max(start, base), t1 = min(sq.ctx, base + CT);  // new tokens of the chunk
-        const int m = t1 - t0, rows = m << lgG;
+        const int base = (job == 0 ? chunk : last) * CT, tok = base + tl;
+        const bool fresh = tok >= start && tok < sq.ctx;   // this thread's token is a new one
+        const int64_t row = sq.row0 + tok - start;
         const bool do_kv = !(leave_kv && job == 0), do_q = job == 0 && p.q;
         const bool full = INT8 && base + CT <= sq.ctx;
         int id = -1;
         if (do_kv && (!INT8 || full)) id = table[base / p.c.bs];
 
-        Pair16 w[NI], x[NB];
+        Pair16 w[2 * HB], x[NB];  // K, V of kvh, then of kvh + 1; query rows
         const auto load_kv = [&](int kvh) {
-            const uint16_t* src = kv ? p.v : p.k;
-            const int64_t stride = kv ? p.v_stride : p.k_stride;
-            const uint16_t* tail = (kv ? p.c.v_tail : p.c.k_tail) + (size_t(slot) * p.c.Hkv + kvh) * p.c.bs * D;
 #pragma unroll
-            for (int u = 0; u < NI; ++u) {
-                const int i = th + u * HT, tl = i / PR, tok = base + tl;
-                int lo, hi;
-                pair_offsets(i % PR, half, inter, lo, hi);
+            for (int u = 0; u < 2 * HB; ++u) {
+                const int kv = u & 1, h = kvh + u / 2;
                 w[u].a = w[u].b = make_uint4(0u, 0u, 0u, 0u);
-                if (CT * PR % HT != 0 && i >= CT * PR) continue;
-                if (tok >= t0 && tok < t1) {
-                    const uint16_t* r = src + int64_t(sq.row0 + tok - start) * stride + kvh * D;
+                if (h >= kvh1) continue;
+                if (fresh) {
+                    const uint16_t* r = (kv ? p.v + row * p.v_stride : p.k + row * p.k_stride) + h * D;
                     w[u].a = ldg128(r + lo);
                     w[u].b = ldg128(r + hi);
-                } else if (full && slot_ok && tok < t0) {
-                    w[u].a = ldcg128(tail + tl * D + lo);
-                    w[u].b = ldcg128(tail + tl * D + hi);
+                } else if (full && slot_ok) {  // an earlier token of the block
+                    const uint16_t* r = (kv ? p.c.v_tail : p.c.k_tail) + ((size_t(slot) * p.c.Hkv + h) * CT + tl) * D;
+                    w[u].a = ldcg128(r + lo);
+                    w[u].b = ldcg128(r + hi);
                 }
             }
         };
-        // q rows (token, head of the group), NB of a thread's chunk pairs from i0 on
-        const auto load_q = [&](int kvh, int i0) {
+        const uint16_t* q_in = p.q + row * p.q_stride;
+        uint16_t* q_to = p.q_out + row * p.q_out_stride;
+        const auto load_q = [&](int h) {
 #pragma unroll
             for (int u = 0; u < NB; ++u) {
-                const int i = i0 + u * kRopeThreads, r = i / PR;
-                if (r >= rows) break;
-                int lo, hi;
-                pair_offsets(i % PR, half, inter, lo, hi);
-                const uint16_t* at = p.q + int64_t(sq.row0 + t0 - start + (r >> lgG)) * p.q_stride +
-                                     (kvh * G + (r & (G - 1))) * D;
-                x[u].a = ldcg128(at + lo);  // q may be turned in place
-                x[u].b = ldcg128(at + hi);
+                if (h + u >= kvh1 * G) break;
+                x[u].a = ldcg128(q_in + (h + u) * D + lo);  // q may be turned in place
+                x[u].b = ldcg128(q_in + (h + u) * D + hi);
             }
         };
-        // the first head's rows are under way while the angles are worked out
+        // the first rows are under way while the angles are worked out
         if (do_kv) load_kv(kvh0);
-        if (do_q) load_q(kvh0, tid);
-        __syncthreads();  // the previous job's use of cs
-        if (half > 0) {
-            if (job == 0) {
-                if (tid < half) s_turns[tid] = turns_of(p.inv_freq[tid]);
-                __syncthreads();
-            }
-            int tl = tid / half, j = tid % half;
-            const int dt = kRopeThreads / half, dj = kRopeThreads % half;
-            for (; tl < m; tl += dt, j += dj) {
-                if (j >= half) {
-                    j -= half;
-                    if (++tl >= m) break;
-                }
-                const int row = sq.row0 + t0 + tl - start;
-                const int pos = p.positions ? p.positions[row] : t0 + tl;
-                const unsigned long long a = static_cast<unsigned long long>(static_cast<long long>(pos)) * s_turns[j];
-                float sn, cn;
-                // the top half as a signed number of half turns, in [-1, 1)
-                sincospif(float(int32_t(a >> 32)) * 4.656612873077393e-10f, &sn, &cn);
-                cs[(t0 + tl - base) * cs_stride(half) + (j % 8) * (half / 8) + j / 8] = make_float2(cn * p.scale, sn * p.scale);
+        if (do_q && fresh) load_q(kvh0 * G);
+        if (job == 0) __syncthreads();  // s_turns
+
+        Angles an;
+        if (turns && fresh) {
+            const int pos = p.positions ? p.positions[row] : tok;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const unsigned long long at = static_cast<unsigned long long>(static_cast<long long>(pos));
+                sincos_turn(uint32_t(at * s_turns[pr * 8 + 2 * e] >> 32), an.s[e].x, an.c[e].x);
+                sincos_turn(uint32_t(at * s_turns[pr * 8 + 2 * e + 1] >> 32), an.s[e].y, an.c[e].y);
+                an.s[e] = __fmul2_rn(an.s[e], make_float2(p.scale, p.scale));
+                an.c[e] = __fmul2_rn(an.c[e], make_float2(p.scale, p.scale));
             }
         }
         if (do_kv && (!INT8 || full) && (id < 0 || id >= p.c.num_blocks)) {
@@ -256,81 +289,78 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_
         }
         if (INT8 && do_kv && !slot_ok && (!full || start > base) && tid == 0) report(p.c.err, kErrSlot);
         const bool write = do_kv && (INT8 && !full ? slot_ok : id >= 0 && (slot_ok || start <= base));
-        __syncthreads();
 
-        for (int kvh = kvh0; kvh < kvh1; ++kvh) {
-            if (kvh > kvh0) {
-                if (do_kv) load_kv(kvh);
-                if (do_q) load_q(kvh, tid);
-            }
-            // ---- K and V
-            if (write) {
-                float mx = 0.f;
+        // Neighbouring CTAs take the two parts in opposite order: one's arithmetic
+        // on K and V beside the other's stream of queries
+        for (int part = 0; part < 2; ++part) {
+        // ---- K and V rows of HB heads at a time
+        if (part == int(blockIdx.x & 1) && write) {
+            for (int kvh = kvh0; kvh < kvh1; kvh += HB) {
+                if (kvh > kvh0) load_kv(kvh);
+                if (fresh) {
 #pragma unroll
-                for (int u = 0; u < NI; ++u) {
-                    const int i = th + u * HT, tl = i / PR, tok = base + tl;
-                    if (kv == 0 && tok >= t0 && tok < t1) turn(w[u], i % PR, half, inter, cs + tl * cs_stride(half));
-                    if (full) mx = fmaxf(mx, fmaxf(absmax8(w[u].a), absmax8(w[u].b)));
+                    for (int u = 0; u < 2 * HB; u += 2) turn(w[u], an);
                 }
                 if (full) {
+                    float mx[2 * HB];
 #pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
-                    if ((tid & 31) == 0) s_max[tid >> 5] = mx;
+                    for (int u = 0; u < 2 * HB; ++u) {
+                        const __nv_bfloat162 top = absmax8(w[u].b, absmax8(w[u].a, __floats2bfloat162_rn(0.f, 0.f)));
+                        mx[u] = fmaxf(__low2float(top), __high2float(top));
+                    }
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+                        for (int u = 0; u < 2 * HB; ++u) mx[u] = fmaxf(mx[u], __shfl_xor_sync(kFull, mx[u], o));
+                    if (kvh > kvh0) __syncthreads();  // the heads before are done with s_max
+                    if ((tid & 31) == 0) {
+#pragma unroll
+                        for (int u = 0; u < 2 * HB; ++u) s_max[u][tid >> 5] = mx[u];
+                    }
                     __syncthreads();  // `full` and `write` are the CTA's
-                    mx = 0.f;
 #pragma unroll
-                    for (int k = 0; k < HT / 32; ++k) mx = fmaxf(mx, s_max[kv * (HT / 32) + k]);
-                    const float scale = mx < 1e-6f ? 1.0f : __fdiv_rn(mx, 127.0f), inv = __fdiv_rn(1.0f, scale);
-                    int8_t* dst = static_cast<int8_t*>(kv ? p.c.v_pool : p.c.k_pool) +
-                                  (size_t(id) * p.c.Hkv + kvh) * CT * D;
+                    for (int u = 0; u < 2 * HB; ++u) {
+                        const int kv = u & 1, h = kvh + u / 2;
+                        if (h >= kvh1) continue;
+                        float m = 0.f;
 #pragma unroll
-                    for (int u = 0; u < NI; ++u) {
-                        const int i = th + u * HT, tl = i / PR;
-                        if (CT * PR % HT != 0 && i >= CT * PR) continue;
-                        int lo, hi;
-                        pair_offsets(i % PR, half, inter, lo, hi);
-                        *reinterpret_cast<uint2*>(dst + tl * D + lo) = codes8(w[u].a, scale, inv);
-                        *reinterpret_cast<uint2*>(dst + tl * D + hi) = codes8(w[u].b, scale, inv);
+                        for (int k = 0; k < THREADS / 32; ++k) m = fmaxf(m, s_max[u][k]);
+                        const float scale = m < 1e-6f ? 1.0f : __fdiv_rn(m, 127.0f), inv = __fdiv_rn(1.0f, scale);
+                        int8_t* dst = static_cast<int8_t*>(kv ? p.c.v_pool : p.c.k_pool) +
+                                      ((size_t(id) * p.c.Hkv + h) * CT + tl) * D;
+                        *reinterpret_cast<uint2*>(dst + lo) = codes8(w[u].a, scale, inv);
+                        *reinterpret_cast<uint2*>(dst + hi) = codes8(w[u].b, scale, inv);
+                        if (tid == 0) p.c.scales[(size_t(id) * p.c.Hkv + h) * 2 + kv] = scale;
                     }
-                    if (th == 0) p.c.scales[(size_t(id) * p.c.Hkv + kvh) * 2 + kv] = scale;
-                    if (kvh + 1 < kvh1) __syncthreads();  // s_max
-                } else {
+                } else if (fresh) {
                     // rows of the pool block, or of the tail
-                    uint16_t* dst = INT8 ? (kv ? p.c.v_tail : p.c.k_tail) + (size_t(slot) * p.c.Hkv + kvh) * p.c.bs * D
-                                         : static_cast<uint16_t*>(kv ? p.c.v_pool : p.c.k_pool) +
-                                               ((size_t(id) * p.c.Hkv + kvh) * p.c.bs + base % p.c.bs) * D;
 #pragma unroll
-                    for (int u = 0; u < NI; ++u) {
-                        const int i = th + u * HT, tl = i / PR, tok = base + tl;
-                        if (tok < t0 || tok >= t1) continue;
-                        int lo, hi;
-                        pair_offsets(i % PR, half, inter, lo, hi);
-                        *reinterpret_cast<uint4*>(dst + tl * D + lo) = w[u].a;
-                        *reinterpret_cast<uint4*>(dst + tl * D + hi) = w[u].b;
+                    for (int u = 0; u < 2 * HB; ++u) {
+                        const int kv = u & 1, h = kvh + u / 2;
+                        if (h >= kvh1) continue;
+                        uint16_t* dst = INT8 ? (kv ? p.c.v_tail : p.c.k_tail) + ((size_t(slot) * p.c.Hkv + h) * CT + tl) * D
+                                             : static_cast<uint16_t*>(kv ? p.c.v_pool : p.c.k_pool) +
+                                                   ((size_t(id) * p.c.Hkv + h) * p.c.bs + tok % p.c.bs) * D;
+                        *reinterpret_cast<uint4*>(dst + lo) = w[u].a;
+                        *reinterpret_cast<uint4*>(dst + hi) = w[u].b;
                     }
                 }
             }
+        }
 
-            // ---- the group's queries
-            if (do_q) {
-                for (int i0 = tid;;) {
+        // ---- the groups' queries, NB rows in flight
+        if (part != int(blockIdx.x & 1) && do_q && fresh) {
+            for (int h = kvh0 * G; h < kvh1 * G; h += NB) {
+                if (h > kvh0 * G) load_q(h);
 #pragma unroll
-                    for (int u = 0; u < NB; ++u) {
-                        const int i = i0 + u * kRopeThreads, r = i / PR;
-                        if (r >= rows) break;
-                        int lo, hi;
-                        pair_offsets(i % PR, half, inter, lo, hi);
-                        turn(x[u], i % PR, half, inter, cs + (t0 - base + (r >> lgG)) * cs_stride(half));
-                        uint16_t* at = p.q_out + int64_t(sq.row0 + t0 - start + (r >> lgG)) * p.q_out_stride +
-                                       (kvh * G + (r & (G - 1))) * D;
-                        *reinterpret_cast<uint4*>(at + lo) = x[u].a;
-                        *reinterpret_cast<uint4*>(at + hi) = x[u].b;
-                    }
-                    i0 += NB * kRopeThreads;
-                    if (i0 / PR >= rows) break;
-                    load_q(kvh, i0);
+                for (int u = 0; u < NB; ++u) {
+                    if (h + u >= kvh1 * G) break;
+                    turn(x[u], an);
+                    *reinterpret_cast<uint4*>(q_to + (h + u) * D + lo) = x[u].a;
+                    *reinterpret_cast<uint4*>(q_to + (h + u) * D + hi) = x[u].b;
                 }
             }
+        }
         }
     }
 }
@@ -385,13 +415,19 @@ extern "C" int pkv_rope_append(const pkv_cache_desc* c, const pkv_batch_desc* ba
     const int ct = int8 ? c->block_size : 16;
     // the most aligned chunks that max_tokens tokens in a row can touch
     const unsigned chunks = unsigned((batch->max_tokens + ct - 2) / ct + 1);
-    // Angles are worked out once a CTA: where there are CTAs enough for several
-    // waves (8 fit on an SM) a CTA takes several kv heads.
+    // Angles are worked out once a CTA, so it takes as many kv heads as leave
+    // CTAs for a wave or two (7 of 128 threads fit on an SM).
+    const int64_t real = std::min<int64_t>(int64_t(chunks) * batch->B, batch->num_tokens / ct + 2 * int64_t(batch->B));
     p.heads = 1;
-    while (p.heads < 4 && p.heads * 2 <= c->num_kv_heads &&
-           int64_t(chunks) * batch->B * c->num_kv_heads / (p.heads * 2) >= 152 * 8 * 2)
-        p.heads *= 2;
-    const dim3 grid(chunks, unsigned((c->num_kv_heads + p.heads - 1) / p.heads), unsigned(batch->B));
+    while (p.heads * 2 <= c->num_kv_heads && real * c->num_kv_heads / (p.heads * 2) >= 152 * 7 * 2) p.heads *= 2;
+    // chunks of all sequences: no more than B times the longest's, nor than
+    // the tokens fill, two begun ones a sequence
+    p.ragged = chunks > 1;
+    const int64_t gx = p.ragged ? real : batch->B;
+    p.groups = (c->num_kv_heads + p.heads - 1) / p.heads;
+    if (gx * p.groups >= 0x7FFFFFFF) return PKV_ERR_INVALID;
+    const dim3 grid(unsigned(gx * p.groups + p.ragged));
+    const unsigned threads = unsigned(ct * d / 16);
     void (*fn)(RopeParams) = nullptr;
     if (d == 128)
         fn = !int8 ? rope_append_kernel<128, false, 16>
@@ -400,7 +436,7 @@ extern "C" int pkv_rope_append(const pkv_cache_desc* c, const pkv_batch_desc* ba
         fn = !int8 ? rope_append_kernel<64, false, 16>
                    : ct == 16 ? rope_append_kernel<64, true, 16> : rope_append_kernel<64, true, 64>;
     auto s = static_cast<cudaStream_t>(stream);
-    if ((st = launch(fn, grid, dim3(kRopeThreads), 0, s, p)) != PKV_OK) return st;
+    if ((st = launch(fn, grid, dim3(threads), 0, s, p)) != PKV_OK) return st;
     if (g_pdl.load(std::memory_order_relaxed) && batch->max_tokens > 1) {
         empty_kernel<<<1, 1, 0, s>>>();
         return cuda_status(cudaGetLastError());
