@@ -125,6 +125,20 @@ __device__ __forceinline__ void sts128(uint32_t addr, const uint4& v) {
                  : "memory");
 }
 
+template <int OFF>
+__device__ __forceinline__ uint4 lds128_at(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4 + %5];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr), "n"(OFF));
+    return v;
+}
+template <int OFF>
+__device__ __forceinline__ void sts128_at(uint32_t addr, const uint4& v) {
+    asm volatile("st.shared.v4.u32 [%0 + %5], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w), "n"(OFF)
+                 : "memory");
+}
+
 // Global load through L2 only: sees global writes made earlier in this kernel
 // by other threads of the CTA (after a barrier), unlike the read-only path.
 __device__ __forceinline__ uint4 ldcg128(const void* p) {

@@ -123,6 +123,42 @@ __device__ __forceinline__ void mma_commit(uint32_t bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 
+// Registers a thread of this warpgroup (all of its warps, converged).
+template <int N>
+__device__ __forceinline__ void reg_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void reg_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// ---- the next CTA of the grid
+// Asks the hardware for a CTA of this grid that has not started: 16 bytes of
+// answer to shared memory, counted on the mbarrier.
+__device__ __forceinline__ void next_cta(uint32_t answer, uint32_t bar) {
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(answer),
+                 "r"(bar)
+                 : "memory");
+}
+// The answer: false if there was none left, else the CTA's x and y.
+__device__ __forceinline__ bool next_cta_read(uint32_t answer, int& x, int& y) {
+    uint32_t got, a = 0, b = 0, c;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t"
+        "ld.shared.b128 r, [%4];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+        "selp.u32 %3, 1, 0, p;\n\t"
+        "mov.u32 %0, 0;\n\tmov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%0, %1, %2, _}, r;\n\t}"
+        : "=&r"(a), "=&r"(b), "=&r"(c), "=&r"(got)
+        : "r"(answer)
+        : "memory");
+    x = int(a);
+    y = int(b);
+    return got != 0;
+}
+
 // ---- tensor copies that other CTAs will read again (no cache hint)
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int x, int y, int z, uint32_t bar) {
     asm volatile(

@@ -32,6 +32,7 @@ struct WindowParams {
     int32_t split_tiles;  // 16-token tiles a split (0: no split)
     int32_t max_splits;
     int32_t row_tiles;  // row tiles of max_tokens tokens
+    int32_t item_tiles;  // window_tc_kernel: row tiles that the batch can have
     float qscale;       // sm_scale * log2(e)
 };
 
@@ -54,6 +55,10 @@ __device__ __forceinline__ KeyTiles key_tiles(int p_first, int p_last, int windo
     kt.n = kt.nsink + p_last / unit - kt.lo + 1;
     return kt;
 }
+
+// Registers a thread that window_tc_kernel is launched with.
+constexpr int kTcLaunchRegsBf16 = 168;
+constexpr int kTcLaunchRegsInt8 = 128;
 
 using WindowFn = void (*)(WindowParams);
 

@@ -39,7 +39,7 @@ struct Plan {
 
 // Raises a kernel's dynamic shared-memory limit once per kernel and device
 // and returns how many of its CTAs fit on an SM.
-int prepare_kernel(WindowFn fn, size_t smem, int threads, int* ctas) {
+int prepare_kernel(WindowFn fn, size_t smem, int threads, int launch_regs, int* ctas) {
     struct Entry {
         WindowFn fn;
         int dev;
@@ -61,6 +61,11 @@ int prepare_kernel(WindowFn fn, size_t smem, int threads, int* ctas) {
         cudaFuncSetAttribute(f, cudaFuncAttributePreferredSharedMemoryCarveout, int(cudaSharedmemCarveoutMaxShared)) !=
             cudaSuccess ||
         cudaOccupancyMaxActiveBlocksPerMultiprocessor(ctas, fn, threads, smem) != cudaSuccess)
+        return PKV_ERR_CUDA;
+    // window_tc_kernel's warpgroups share out the registers that the block was
+    // launched with, and would wait forever for more than that
+    cudaFuncAttributes at;
+    if (launch_regs > 0 && (cudaFuncGetAttributes(&at, f) != cudaSuccess || at.numRegs != launch_regs))
         return PKV_ERR_CUDA;
     if (n < 256) seen[n++] = Entry{fn, dev, *ctas};
     return PKV_OK;
@@ -102,7 +107,8 @@ int make_plan(const pkv_cache_desc* c, const pkv_batch_desc* bt, int window, int
             pl->fn = int8 ? window_tc_fn_d64_int8(&pl->smem, &pl->threads) : window_tc_fn_d64_bf16(&pl->smem, &pl->threads);
         pl->row_tiles = int((rows + 255) / 256);
         pl->key_tiles = most_key_tiles(c, bt, window, sinks, int(std::min<int64_t>(256 / g, bt->max_tokens)), c->block_size);
-        return prepare_kernel(pl->fn, pl->smem, pl->threads, &pl->ctas_per_sm);
+        return prepare_kernel(pl->fn, pl->smem, pl->threads, int8 ? kTcLaunchRegsInt8 : kTcLaunchRegsBf16,
+                              &pl->ctas_per_sm);
     }
     const int nt = rows <= 8 ? 1 : 2;
     if (c->head_dim == 128) pl->fn = int8 ? window_rows_fn_d128_int8(nt) : window_rows_fn_d128_bf16(nt);
@@ -111,7 +117,7 @@ int make_plan(const pkv_cache_desc* c, const pkv_batch_desc* bt, int window, int
     pl->threads = kThreads;
     pl->row_tiles = int((rows + 8 * nt - 1) / (8 * nt));
     pl->key_tiles = most_key_tiles(c, bt, window, sinks, std::max(1, 8 * nt / g), kTile);
-    return prepare_kernel(pl->fn, pl->smem, pl->threads, &pl->ctas_per_sm);
+    return prepare_kernel(pl->fn, pl->smem, pl->threads, 0, &pl->ctas_per_sm);
 }
 
 int max_splits_of(const pkv_cache_desc* c, const pkv_batch_desc* bt, const Plan& pl, int split_tokens) {
@@ -277,9 +283,14 @@ int pkv_window_attention(const pkv_cache_desc* c, const pkv_batch_desc* batch, c
     p.row_tiles = pl.row_tiles;
     // never 0: a hidden token's score is -infinity, and 0 times that is not a number
     p.qscale = std::max(sm_scale * 1.4426950408889634f, 1e-37f);
-    const int64_t gx = int64_t(pl.row_tiles) * splits;
+    // window_tc_kernel: the row tiles of all sequences are one list
+    const int64_t g = c->num_q_heads / c->num_kv_heads;
+    p.item_tiles = 0;
+    if (pl.tc)
+        p.item_tiles = int(std::min<int64_t>(int64_t(pl.row_tiles) * batch->B, batch->num_tokens * g / 256 + batch->B));
+    const int64_t gx = int64_t(pl.tc ? p.item_tiles : pl.row_tiles) * splits;
     if (gx > 0x7FFFFFFF) return PKV_ERR_INVALID;
-    const dim3 grid(unsigned(gx), unsigned(c->num_kv_heads), unsigned(batch->B));
+    const dim3 grid(unsigned(gx), unsigned(c->num_kv_heads), pl.tc ? 1u : unsigned(batch->B));
     return launch(pl.fn, grid, dim3(unsigned(pl.threads)), pl.smem, static_cast<cudaStream_t>(stream), p);
 }
 
