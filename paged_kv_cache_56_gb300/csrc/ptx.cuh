@@ -125,6 +125,12 @@ __device__ __forceinline__ void sts128(uint32_t addr, const uint4& v) {
                  : "memory");
 }
 
+__device__ __forceinline__ float2 lds64(uint32_t addr) {
+    float2 v;
+    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr));
+    return v;
+}
+
 template <int OFF>
 __device__ __forceinline__ uint4 lds128_at(uint32_t addr) {
     uint4 v;

@@ -212,13 +212,31 @@ int pkv_window_split_tokens(const pkv_cache_desc* c, const pkv_batch_desc* batch
     Plan pl;
     int sms = 0;
     if ((st = make_plan(c, batch, window, sinks, &pl)) != PKV_OK || (st = sm_count(&sms)) != PKV_OK) return st;
+    if (pl.tc) {
+        // One CTA a SM walks through the items. n of them in s parts each take
+        // ceil(n s / SMs) rounds of (key tiles / s + o) tiles' time, where o stands for
+        // an item's beginning and end: 2, or 8 with the partial rows written, read back
+        // and merged. The s that makes it least. (Ragged batches: the rows of
+        // num_tokens, half a row tile more a sequence.)
+        const int64_t g = c->num_q_heads / c->num_kv_heads;
+        const int64_t n = std::min<int64_t>(int64_t(pl.row_tiles) * batch->B,
+                                            (batch->num_tokens * g + 128 * int64_t(batch->B) + 255) / 256) * c->num_kv_heads;
+        const int64_t tiles = (pl.key_tiles + 7) / 8;
+        int64_t best = 0, split = 1;
+        for (int64_t s = 1; s <= std::min<int64_t>(tiles / 2, kMaxSplits); ++s) {
+            const int64_t cost = (n * s + sms - 1) / sms * ((tiles + s - 1) / s + (s > 1 ? 8 : 2));
+            if (s == 1 || cost < best) {
+                best = cost;
+                split = s;
+            }
+        }
+        return split <= 1 ? 0 : int((tiles + split - 1) / split * 128);
+    }
     const int64_t units = int64_t(batch->B) * c->num_kv_heads * pl.row_tiles;
     const int64_t splits = int64_t(sms) * pl.ctas_per_sm / units;
     if (splits <= 1) return 0;
     // at least two tiles a warp: shorter splits spend their time on the start and the merge
-    // (tensor-core kernel: two key tiles)
-    int64_t tiles = std::max<int64_t>((pl.key_tiles + splits - 1) / splits, pl.tc ? 16 : 2 * kWarps);
-    if (pl.tc) tiles = (tiles + 7) / 8 * 8;
+    const int64_t tiles = std::max<int64_t>((pl.key_tiles + splits - 1) / splits, 2 * kWarps);
     return tiles >= pl.key_tiles ? 0 : int(tiles * kTile);
 }
 

@@ -135,7 +135,7 @@ window_tc_kernel(const __grid_constant__ WindowParams p) {
     __shared__ uint32_t s_tmem;
     __shared__ int s_last;
     __shared__ uint32_t s_bad[8];              // units of a key tile that are not there, by tile % 8
-    __shared__ float4 s_sc[INT8 ? 8 : 1][8];   // units' K scale, log2 of the V scale, 1 / V scale
+    __shared__ float2 s_sc[INT8 ? 8 : 1][8];   // units' K scale times p.qscale, log2 of the V scale
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int G = p.c.Hq / p.c.Hkv, lgG = 31 - __clz(G), bs = p.c.bs, lg = bs == 16 ? 4 : 6, U = kTcKeys >> lg;  // U: blocks a key tile
@@ -226,7 +226,7 @@ window_tc_kernel(const __grid_constant__ WindowParams p) {
             const KeyTiles kt = im.kt;
             const int n = im.n, k0 = im.k0;
             const bool used = im.r_first + i * kTcRows < im.r_end;
-            float m_ref = -INFINITY;  // reference of the exponent, in score units
+            float m_ref = -INFINITY;  // reference of the exponent (base 2)
             float2 l2 = make_float2(0.f, 0.f);
             if (used) {
                 const int hi = have ? im.pos0 + (row >> lgG) : -1;
@@ -251,8 +251,15 @@ window_tc_kernel(const __grid_constant__ WindowParams p) {
                     // one chunk's load in flight while the other is worked on.
                     uint32_t w[8][8];
                     float2 sum;
+                    // INT8: the columns' factors, read here at once: beside the multiplies
+                    // and the conversion a shared-memory load in the pass takes long
+                    float2 sc[INT8 ? 8 : 1];
+                    if (INT8) {
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) sc[c] = lds64(smem_addr(&s_sc[slot][(c * 16) >> lg]));
+                    }
                     for (;;) {
-                        const float neg = (m_ref == -INFINITY ? 0.f : -m_ref * scale) - kTcShift;
+                        const float neg = (m_ref == -INFINITY ? 0.f : -m_ref) - kTcShift;
                         float mx = -INFINITY;
                         sum = make_float2(0.f, 0.f);
                         const auto chunk = [&](auto hide, uint32_t (&r)[16], int c) {
@@ -263,15 +270,20 @@ window_tc_kernel(const __grid_constant__ WindowParams p) {
                                 const auto below = [](int x) { return (1u << min(16, max(0, x))) - 1u; };
                                 uint32_t see = below(hi - t0 + 1) & (below(p.sinks - t0) | ~below(lo - t0));
                                 if ((bad >> u) & 1u) see = 0u;
+                                if (__all_sync(kFull, (see & 0xFFFFu) == 0u)) {  // nothing for the whole warp
 #pragma unroll
-                                for (int e = 0; e < 16; ++e)
-                                    if (!((see >> e) & 1u)) r[e] = 0xFF800000u;
+                                    for (int e = 0; e < 8; ++e) w[c][e] = 0u;
+                                    return;
+                                }
+                                if (!__all_sync(kFull, (see & 0xFFFFu) == 0xFFFFu)) {
+#pragma unroll
+                                    for (int e = 0; e < 16; ++e)
+                                        if (!((see >> e) & 1u)) r[e] = 0xFF800000u;
+                                }
                             }
                             // INT8: a score is its K scale times the column, a weight its V
                             // scale times the softmax weight, by way of the exponent
-                            float4 sc = make_float4(1.f, 0.f, 1.f, 0.f);
-                            if (INT8) sc = s_sc[slot][u];
-                            const float a = INT8 ? scale * sc.x : scale, b = INT8 ? neg + sc.y : neg;
+                            const float a = INT8 ? sc[INT8 ? c : 0].x : scale, b = INT8 ? neg + sc[INT8 ? c : 0].y : neg;
                             const float2 a2 = make_float2(a, a), b2 = make_float2(b, b);
                             float mc = -INFINITY, md = -INFINITY;
                             float2 part = make_float2(0.f, 0.f);
@@ -289,9 +301,13 @@ window_tc_kernel(const __grid_constant__ WindowParams p) {
                                 w[c][e / 2] = f2_to_bf16x2(x0.x, x0.y);
                                 w[c][e / 2 + 1] = f2_to_bf16x2(x1.x, x1.y);
                             }
-                            mc = fmaxf(mc, md);
-                            mx = fmaxf(mx, INT8 ? mc * sc.x : mc);
-                            sum = INT8 ? __ffma2_rn(part, make_float2(sc.z, sc.z), sum) : __fadd2_rn(sum, part);
+                            mx = fmaxf(mx, fmaxf(mc, md) * a);
+                            if (INT8) {
+                                const float vi = fast_exp2(-sc[INT8 ? c : 0].y);
+                                sum = __ffma2_rn(part, make_float2(vi, vi), sum);
+                            } else {
+                                sum = __fadd2_rn(sum, part);
+                            }
                         };
                         const auto pass = [&](auto hide) {
                             uint32_t ra[16], rb[16];
@@ -308,9 +324,9 @@ window_tc_kernel(const __grid_constant__ WindowParams p) {
                         };
                         if (masked) pass(Const<true>{});
                         else pass(Const<false>{});
-                        const bool up = (mx - m_ref) * scale > kTcAhead;  // false while nothing has been seen
+                        const bool up = mx - m_ref > kTcAhead;  // false while nothing has been seen
                         if (!__any_sync(kFull, up)) break;
-                        const float f = up ? fast_exp2((m_ref - mx) * scale) : 1.f;
+                        const float f = up ? fast_exp2(m_ref - mx) : 1.f;
                         if (up) m_ref = mx;
                         l2.x *= f;
                         l2.y *= f;
@@ -355,7 +371,17 @@ window_tc_kernel(const __grid_constant__ WindowParams p) {
                 const bool partial = im.ns > 1;
                 const int steps = partial ? D / 32 : D / 64;
                 const int first = im.r_first + warp * 32, rows = min(32, im.r_end - first);
-                const int row_base = im.row0, head0 = im.kvh * G, split = im.j;
+                // a thread's pieces of rows lane / 8 + 4 e: every second e is 8 / G tokens on
+                const int ch = lane % 8;
+                int64_t to[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int rr = first + lane / 8 + 4 * e;
+                    const int64_t t = im.row0 + (rr >> lgG);
+                    const int h = im.kvh * G + (rr & (G - 1));
+                    to[e] = partial ? ((t * p.c.Hq + h) * S + im.j) * D + ch * 4 : t * p.out_stride + h * D + ch * 8;
+                }
+                const int64_t ahead = partial ? int64_t(8 >> lgG) * p.c.Hq * S * D : (8 >> lgG) * p.out_stride;
                 for (int c = 0; c < steps; ++c) {
                     __syncwarp();
                     if (partial) {
@@ -382,21 +408,17 @@ window_tc_kernel(const __grid_constant__ WindowParams p) {
                     __syncwarp();
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        const int r = e * 4 + lane / 8, ch = lane % 8;  // four rows at a time
+                        const int r = e * 4 + lane / 8;  // four rows at a time
                         const uint4 v = lds128(st + uint32_t(r) * 128u + ((uint32_t(ch) ^ uint32_t(r & 7)) << 4));
                         if (r < rows) {
-                            const int rr = first + r;
-                            const int64_t t = row_base + (rr >> lgG);
-                            const int h = head0 + (rr & (G - 1));
-                            if (partial)
-                                *reinterpret_cast<uint4*>(p.ws_o + ((size_t(t) * p.c.Hq + h) * S + split) * D + c * 32 + ch * 4) = v;
-                            else
-                                *reinterpret_cast<uint4*>(p.out + t * p.out_stride + h * D + c * 64 + ch * 8) = v;
+                            const int64_t at = to[e & 1] + (e >> 1) * ahead;
+                            if (partial) *reinterpret_cast<uint4*>(p.ws_o + at + c * 32) = v;
+                            else *reinterpret_cast<uint4*>(p.out + at + c * 64) = v;
                         }
                     }
                 }
                 if (im.ns > 1 && have) {
-                    p.ws_ml[at * 2] = m_ref == -INFINITY ? -1e30f : m_ref * scale;
+                    p.ws_ml[at * 2] = m_ref == -INFINITY ? -1e30f : m_ref;
                     p.ws_ml[at * 2 + 1] = l;
                 }
                 tc_fence_before();  // O_i has been read before the next item's P_i is announced
@@ -409,29 +431,59 @@ window_tc_kernel(const __grid_constant__ WindowParams p) {
             if (tid == 0) s_last = atom_add_acq_rel_gpu(cnt, 1) == im.ns - 1;
             if (!(ok = meet(merges++))) break;
             if (!s_last) continue;
-            for (int r = warp; r < im.r_end - im.r_first; r += 8) {
-                const int rr = im.r_first + r;
-                const size_t t = im.row0 + (rr >> lgG), h = im.kvh * G + (rr & (G - 1)), a = (t * p.c.Hq + h) * S;
-                const float2* ml = reinterpret_cast<const float2*>(p.ws_ml) + a;
-                float mm = -1e30f;
-                for (int x = lane; x < im.ns; x += 32) mm = fmaxf(mm, __ldcg(ml + x).x);
+            // A lane has the weights of one of the warp's 32 rows; eight rows' partials
+            // (16 bytes a lane) are in flight at a time.
+            const int first = im.r_first + warp * 32, rows = min(32, im.r_end - first), parts = im.ns;
+            const int head0 = im.kvh * G, row0 = im.row0;
+            const auto place = [&](int r) {  // of row first + r: its number among all rows and heads
+                return size_t(row0 + ((first + r) >> lgG)) * p.c.Hq + head0 + ((first + r) & (G - 1));
+            };
+            if (rows <= 0) continue;
+            const float2* ml = reinterpret_cast<const float2*>(p.ws_ml) + place(min(lane, rows - 1)) * S;
+            float mm = -1e30f, L = 0.f;
+            for (int x = 0; x < parts; ++x) {
+                const float2 v = __ldcg(ml + x);
+                const float up = fmaxf(mm, v.x);
+                L = L * fast_exp2(mm - up) + v.y * fast_exp2(v.x - up);
+                mm = up;
+            }
+            const float inv = L > 0.f ? 1.f / L : 0.f;
+            constexpr int E = D / 32;  // elements a lane
+            for (int g = 0; g < rows; g += 8) {
+                float acc[8][E];
 #pragma unroll
-                for (int off = 16; off > 0; off >>= 1) mm = fmaxf(mm, __shfl_xor_sync(kFull, mm, off));
-                float acc[D / 32], L = 0.f;
+                for (int r = 0; r < 8; ++r)
 #pragma unroll
-                for (int e = 0; e < D / 32; ++e) acc[e] = 0.f;
-                for (int x = 0; x < im.ns; ++x) {
-                    const float2 v = __ldcg(ml + x);
-                    const float c = fast_exp2(v.x - mm);
-                    L += c * v.y;
+                    for (int e = 0; e < E; ++e) acc[r][e] = 0.f;
+                for (int x = 0; x < parts; ++x) {
+                    const float c = fast_exp2(__ldcg(ml + x).x - mm) * inv;
+                    float v[8][E];
 #pragma unroll
-                    for (int e = 0; e < D / 32; ++e) acc[e] += c * __ldcg(p.ws_o + (a + x) * D + e * 32 + lane);
+                    for (int r = 0; r < 8; ++r) {
+                        const float* o = p.ws_o + (place(min(g + r, rows - 1)) * S + x) * D + lane * E;
+                        if constexpr (E == 4) {
+                            const float4 f = __ldcg(reinterpret_cast<const float4*>(o));
+                            v[r][0] = f.x; v[r][1] = f.y; v[r][2] = f.z; v[r][3] = f.w;
+                        } else {
+                            const float2 f = __ldcg(reinterpret_cast<const float2*>(o));
+                            v[r][0] = f.x; v[r][1] = f.y;
+                        }
+                    }
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) {
+                        const float w = __shfl_sync(kFull, c, min(g + r, 31));
+#pragma unroll
+                        for (int e = 0; e < E; ++e) acc[r][e] += w * v[r][e];
+                    }
                 }
-                const float f = L > 0.f ? 1.f / L : 0.f;
 #pragma unroll
-                for (int e = 0; e < D / 32; ++e)
-                    reinterpret_cast<__nv_bfloat16*>(p.out)[int64_t(t) * p.out_stride + h * D + e * 32 + lane] =
-                        __float2bfloat16_rn(acc[e] * f);
+                for (int r = 0; r < 8; ++r) {
+                    if (g + r >= rows) break;
+                    const int rr = first + g + r;
+                    uint16_t* at = p.out + int64_t(row0 + (rr >> lgG)) * p.out_stride + (head0 + (rr & (G - 1))) * D + lane * E;
+#pragma unroll
+                    for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t*>(at + e) = f2_to_bf16x2(acc[r][e], acc[r][e + 1]);
+                }
             }
             if (tid == 0) *cnt = 0;  // ready for the next call
         }
@@ -717,7 +769,7 @@ window_tc_kernel(const __grid_constant__ WindowParams p) {
                     if (v == 0) {
                         // scales are positive; a zero one would make hidden scores and weights not-a-numbers
                         const float vs = fmaxf(sc.y, 1e-30f);
-                        if (lane < U) s_sc[slot][lane] = make_float4(fmaxf(sc.x, 1e-30f), __log2f(vs), 1.f / vs, 0.f);
+                        if (lane < U) s_sc[slot][lane] = make_float2(fmaxf(sc.x * p.qscale, 1e-37f), __log2f(vs));
                         if (lane == 0) s_bad[slot] = missing;
                     }
                     __syncwarp();
