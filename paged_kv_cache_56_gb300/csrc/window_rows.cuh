@@ -302,7 +302,7 @@ window_rows_kernel(const __grid_constant__ WindowParams p) {
     for (int seg = k0;; seg += kSegTiles) {
         const int seg_end = min(kpool, seg + kSegTiles);
         if (seg > k0) __syncthreads();  // the last segment's ids are no longer read
-        int ev = kExpNone;
+        // ids first, so that the copies start without waiting for the scales
         for (int k = seg + tid; k < seg_end; k += kThreads) {
             int id = table[kt.tile(k) * kTile / bs];
             if (id < 0 || id >= p.c.num_blocks) {
@@ -310,16 +310,6 @@ window_rows_kernel(const __grid_constant__ WindowParams p) {
                 id = -1;
             }
             s_id[k - seg] = id;
-            if (INT8) {
-                const float2 sc = id < 0 ? make_float2(0.f, 0.f)
-                                         : __ldcg(reinterpret_cast<const float2*>(p.c.scales) + size_t(id) * p.c.Hkv + kvh);
-                s_sc[k - seg] = sc;
-                ev = max(ev, v_exp(sc.y));
-            }
-        }
-        if (INT8) {
-            ev = __reduce_max_sync(kFull, ev);
-            if (lane == 0) s_ev[warp] = ev;
         }
         __syncthreads();
         if (lane == 0)
@@ -327,6 +317,18 @@ window_rows_kernel(const __grid_constant__ WindowParams p) {
                 const int k = seg + warp + s * kWarps;
                 if (k < seg_end) issue(k, seg, (kk + s) % STAGES);
             }
+        int ev = kExpNone;
+        if (INT8) {
+            for (int k = seg + tid; k < seg_end; k += kThreads) {
+                const int id = s_id[k - seg];
+                const float2 sc = id < 0 ? make_float2(0.f, 0.f)
+                                         : __ldcg(reinterpret_cast<const float2*>(p.c.scales) + size_t(id) * p.c.Hkv + kvh);
+                s_sc[k - seg] = sc;
+                ev = max(ev, v_exp(sc.y));
+            }
+            ev = __reduce_max_sync(kFull, ev);
+            if (lane == 0) s_ev[warp] = ev;
+        }
         if (seg == k0) {
             // ---- INT8: the partly filled last block, from the slot's bf16 tail, in
             // plain units, while the ring's first copies fly
@@ -363,6 +365,7 @@ window_rows_kernel(const __grid_constant__ WindowParams p) {
         }
         float delta = 0.f;
         if (INT8) {
+            __syncthreads();  // the scales
             int e = ew;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) e = max(e, s_ev[w]);
