@@ -262,6 +262,56 @@ class PagedKVCache:
             self.seqs[r].length += 1
 
 
+    # -- a chunk of new tokens a sequence ------------------------------------
+    def plan_chunk(self, req_ids, counts) -> "ChunkPlan":
+        """Host part of writing and attending counts[i] >= 0 new tokens of each
+        sequence (a decode step, drafted tokens, a chunk of a prompt): grows the
+        block lists to hold them. All or nothing: if the pool cannot give every
+        block, PkvError(OOM) is raised with no list changed."""
+        B = len(req_ids)
+        counts = np.asarray(counts, np.int32).reshape(-1)
+        if counts.size != B or (counts < 0).any():
+            raise ValueError("counts needs one number >= 0 per sequence")
+        if len(set(req_ids)) != B:
+            raise ValueError("a sequence may be in a batch once")
+        start = np.array([self.seqs[r].length for r in req_ids], np.int32)
+        have = [len(self.table(r)) for r in req_ids]
+        need = [max(0, -(-int(s + n) // self.bs) - h) for s, n, h in zip(start, counts, have)]
+        if any(h + n > self.max_blocks for h, n in zip(have, need)):
+            raise ValueError("a sequence would pass max_blocks_per_seq")
+        shared = [r for r, s, n in zip(req_ids, start, counts) if self.forked and n and s % self.bs and
+                  pkv.pkv_block_refs(self.alloc, self.table(r)[s // self.bs]) > 1]
+        if sum(need) + len(shared) > pkv.pkv_num_free(self.alloc):
+            raise pkv.PkvError("pkv_append_block", pkv.PKV_ERR_OOM)
+        cow = []
+        for r in shared:  # the first rows go into a block that a fork left shared
+            pair = pkv.pkv_cow_block(self.alloc, r, self.seqs[r].length // self.bs)
+            if pair is not None:  # (the other holder may just have taken its own copy)
+                cow.append(pair)
+        for r, n in zip(req_ids, need):
+            for _ in range(n):
+                pkv.pkv_append_block(self.alloc, r)
+        tables = pkv.pkv_build_block_tables(self.alloc, req_ids, self.max_blocks)
+        return ChunkPlan(counts=counts, starts=np.concatenate([[0], np.cumsum(counts)]).astype(np.int32),
+                         ctx_lens=start + counts, slots=np.array([self.seqs[r].slot for r in req_ids], np.int32),
+                         tables=tables, cow=cow)
+
+    def commit_chunk(self, req_ids, counts) -> None:
+        for r, n in zip(req_ids, counts):
+            self.seqs[r].length += int(n)
+
+
+@dataclass
+class ChunkPlan:
+    """Host arrays describing counts[b] new tokens of each of B sequences."""
+    counts: np.ndarray         # [B]
+    starts: np.ndarray         # [B + 1] rows of sequence b in the token arrays
+    ctx_lens: np.ndarray       # [B] tokens, the new ones included
+    slots: np.ndarray          # [B]
+    tables: np.ndarray         # [B, max_blocks]
+    cow: list = None           # (old, new) block pairs to copy before the writes
+
+
 def sm_scale_for(head_dim: int) -> float:
     return 1.0 / math.sqrt(head_dim)
 
@@ -550,3 +600,128 @@ class PipelinedSteps:
             ev = torch.cuda.Event()
             ev.record(st)
             torch.cuda.current_stream().wait_event(ev)
+
+
+# ---------------------------------------------------------------------------
+# Chunks: any number of new tokens a sequence
+# ---------------------------------------------------------------------------
+
+def rope_frequencies(rotary_dim: int, base: float = 10000.0, stretch: float = 1.0, trained: int = 0,
+                     short_turns: float = 32.0, long_turns: float = 1.0):
+    """(frequencies, attention factor) of rotary positions: rotary_dim / 2
+    radians a position, fp64, base ** (-2 j / rotary_dim).
+
+    stretch > 1 scales them for contexts that many times the trained length. With
+    trained == 0 every frequency is divided by it (positions interpolated). With
+    trained > 0, a pair that makes at least short_turns turns over the trained
+    length keeps its frequency, one that makes at most long_turns is
+    interpolated, those between are blended, and the attention factor is
+    0.1 ln(stretch) + 1."""
+    if rotary_dim <= 0 or rotary_dim % 2 or stretch < 1 or not short_turns > long_turns:
+        raise ValueError("rotary_dim must be even and positive, stretch >= 1 and short_turns > long_turns")
+    f = base ** (-np.arange(0, rotary_dim, 2, dtype=np.float64) / rotary_dim)
+    if stretch == 1:
+        return f, 1.0
+    if trained <= 0:
+        return f / stretch, 1.0
+    turns = trained * f / (2 * math.pi)
+    keep = np.clip((turns - long_turns) / (short_turns - long_turns), 0.0, 1.0)
+    return f * keep + f / stretch * (1 - keep), 0.1 * math.log(stretch) + 1.0
+
+
+class ChunkBuffers:
+    """Device-side batch of up to max_batch sequences bringing up to max_tokens
+    tokens in all, at most max_new each; pinned mirrors make the uploads async.
+    The descriptor stays the same from batch to batch (its arrays are refilled),
+    so that a captured graph of the chunk operators can be replayed on it: a
+    batch of fewer sequences leaves the rest without tokens."""
+
+    def __init__(self, cache: PagedKVCache, max_batch: int, max_tokens: int, max_new: int):
+        dev = cache.device
+        self.cache, self.max_batch, self.max_tokens, self.max_new = cache, max_batch, max_tokens, max_new
+
+        def pair(shape):
+            return (torch.zeros(shape, dtype=torch.int32).pin_memory(),
+                    torch.zeros(shape, dtype=torch.int32, device=dev))
+        self.h_starts, self.starts = pair(max_batch + 1)
+        self.h_ctx, self.ctx = pair(max_batch)
+        self.h_slot, self.slot = pair(max_batch)
+        self.h_tab, self.tab = pair((max_batch, cache.max_blocks))
+        self.batch = pkv.make_batch(self.starts, self.tab, self.ctx, self.slot if cache.int8 else None,
+                                    num_tokens=max_tokens, max_tokens=max_new)
+        self._ws = {}
+        self.copied = torch.cuda.Event()
+        self.copied.record()
+
+    def upload(self, plan: ChunkPlan) -> None:
+        B, T = len(plan.counts), int(plan.starts[-1])
+        if B > self.max_batch or T > self.max_tokens or (B and plan.counts.max() > self.max_new):
+            raise ValueError("batch larger than the chunk buffers")
+        self.copied.synchronize()  # do not overwrite pinned data a pending copy still reads
+        for h, d, x, rest in ((self.h_starts, self.starts, plan.starts, T), (self.h_ctx, self.ctx, plan.ctx_lens, 0),
+                              (self.h_slot, self.slot, plan.slots, 0)):
+            a = h.numpy()
+            a[:len(x)] = x
+            a[len(x):] = rest
+            d.copy_(h, non_blocking=True)
+        self.h_tab[:B].numpy()[:] = plan.tables
+        self.tab[:B].copy_(self.h_tab[:B], non_blocking=True)
+        self.copied.record()
+
+    def workspace(self, desc: pkv.CacheDesc, window: int, sinks: int):
+        """(split_tokens, workspace) for the batch's largest shape; made once per window."""
+        key = (desc.dtype, window, sinks)
+        if key not in self._ws:
+            if torch.cuda.is_current_stream_capturing():
+                raise RuntimeError("run the chunk once before capturing it")
+            split = pkv.pkv_window_split_tokens(desc, self.batch, window, sinks)
+            n = pkv.pkv_window_ws_bytes(desc, self.batch, window, sinks, split)
+            self._ws[key] = (split, torch.zeros(n, dtype=torch.uint8, device=self.cache.device) if n else None)
+            torch.cuda.synchronize()  # zeroed, whichever stream uses it
+        return self._ws[key]
+
+
+def run_chunk(cache: PagedKVCache, bufs: ChunkBuffers, q, k, v, out, sm_scale: float, rope=None, window: int = 0,
+              sinks: int = 0, stream=None) -> None:
+    """Kernel launches of one uploaded chunk, per layer l: turn q[l] [T, Hq, d]
+    (in place) and k[l] and write k[l], v[l] [T, Hkv, d] into the cache, then attend into
+    out[l]. window and sinks may be lists with one entry per layer (models that
+    alternate windowed and full layers)."""
+    win = list(window) if isinstance(window, (list, tuple)) else [window] * cache.L
+    snk = list(sinks) if isinstance(sinks, (list, tuple)) else [sinks] * cache.L
+    for li, lc in enumerate(cache.layers):
+        pkv.pkv_rope_append(lc.desc, bufs.batch, rope, q[li], k[li], v[li], None, stream)
+        split, ws = bufs.workspace(lc.desc, win[li], snk[li])
+        pkv.pkv_window_attention(lc.desc, bufs.batch, q[li], out[li], win[li], snk[li], sm_scale, split, ws, stream)
+
+
+def extend_step(cache: PagedKVCache, bufs: ChunkBuffers, req_ids, counts, q, k, v, out, sm_scale: float, rope=None,
+                window=0, sinks=0, stream=None) -> ChunkPlan:
+    """Host plan + upload + kernels of counts[i] new tokens of each sequence;
+    advances the sequences. q, k, v, out: per layer, rows of the sequences one
+    after another, bufs.max_tokens rows long (rows behind the batch's are not
+    touched)."""
+    plan = cache.plan_chunk(req_ids, counts)
+    cache.apply_cow(plan, stream)
+    bufs.upload(plan)
+    run_chunk(cache, bufs, q, k, v, out, sm_scale, rope, window, sinks, stream)
+    cache.commit_chunk(req_ids, counts)
+    return plan
+
+
+def read_back(cache: PagedKVCache, layer: int, req_ids, dtype=torch.bfloat16, stream=None):
+    """(k, v, starts): the rows of whole contexts in token order, dequantized --
+    [sum of lengths, Hkv, d] each, those of req_ids[i] at starts[i] ..
+    starts[i+1]-1 -- e.g. to move sequences to another cache."""
+    lens = [cache.seqs[r].length for r in req_ids]
+    starts = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+    T, dev = int(starts[-1]), cache.layers[layer].k_pool.device
+    k, v = (torch.empty((T, cache.hkv, cache.d), dtype=dtype, device=dev) for _ in range(2))
+    if T:
+        def up(a):
+            return torch.from_numpy(np.ascontiguousarray(a, dtype=np.int32)).to(dev)
+        tables = pkv.pkv_build_block_tables(cache.alloc, req_ids, cache.max_blocks)
+        slots = up(np.array([cache.seqs[r].slot for r in req_ids])) if cache.layers[layer].int8 else None
+        batch = pkv.make_batch(up(starts), up(tables), up(np.array(lens)), slots, num_tokens=T, max_tokens=max(lens))
+        pkv.pkv_gather_kv(cache.layers[layer].desc, batch, k, v, None, stream)
+    return k, v, starts
