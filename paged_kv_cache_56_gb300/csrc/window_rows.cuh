@@ -192,14 +192,14 @@ window_rows_kernel(const __grid_constant__ WindowParams p) {
     const int g = lane >> 2, t = lane & 3;
     const int j = int(blockIdx.x) % p.max_splits, rt = int(blockIdx.x) / p.max_splits;
     const int kvh = blockIdx.y, b = blockIdx.z;
-    const int G = p.c.Hq / p.c.Hkv, bs = p.c.bs;
+    const int G = p.c.Hq / p.c.Hkv, lgG = 31 - __clz(G), bs = p.c.bs, lg = bs == 16 ? 4 : 6;
     const SeqRange sq = seq_range(p.bt, b, bs, p.c.err, tid == 0 && blockIdx.x == 0 && kvh == 0);
     const int r_first = rt * R, r_end = min(sq.n * G, r_first + R);
     if (r_first >= r_end) return;
     // output element e (row e / D of the tile, dim e % D)
     auto out_at = [&](int e) {
         const int r = r_first + e / D;
-        return p.out + int64_t(sq.row0 + r / G) * p.out_stride + (kvh * G + r % G) * D + e % D;
+        return p.out + int64_t(sq.row0 + (r >> lgG)) * p.out_stride + (kvh * G + (r & (G - 1))) * D + e % D;
     };
     const int nrow = r_end - r_first;
     if (sq.bad) {
@@ -208,17 +208,18 @@ window_rows_kernel(const __grid_constant__ WindowParams p) {
         return;
     }
     const int pos0 = sq.ctx - sq.n;
-    const int p_first = pos0 + r_first / G, p_last = pos0 + (r_end - 1) / G;
+    const int p_first = pos0 + (r_first >> lgG), p_last = pos0 + ((r_end - 1) >> lgG);
     const KeyTiles kt = key_tiles(p_first, p_last, p.window, p.sinks, kTile);
     int per = kt.n;
     if (p.split_tiles > 0) per = max(p.split_tiles, (kt.n + p.max_splits - 1) / p.max_splits);
     const int ns = (kt.n + per - 1) / per;
     if (j >= ns) return;
     const int k0 = j * per, k1 = min(kt.n, k0 + per);
-    const int nfull = INT8 ? sq.ctx / bs * bs : sq.ctx;
+    const int nfull = INT8 ? (sq.ctx >> lg) << lg : sq.ctx;
     // tiles of the list that lie in the pool come first, those of the tail last
     const int fullt = nfull / kTile;
     const int kpool = !INT8 ? k1 : min(k1, max(k0, fullt < kt.nsink ? fullt : kt.nsink + max(0, fullt - kt.lo)));
+    const int slot = INT8 ? p.bt.slots[b] : 0;
     const int32_t* table = p.bt.tables + size_t(b) * p.bt.max_blocks;
 
     uint8_t* stages = smem + (T::kSwz ? (1024u - (smem_addr(smem) & 1023u)) & 1023u : 0u);
@@ -243,12 +244,12 @@ window_rows_kernel(const __grid_constant__ WindowParams p) {
     for (int x = 0; x < NT; ++x) {
         const int r = r_first + x * 8 + g;
         const bool have = r < r_end;
-        const uint16_t* qrow = p.q + int64_t(sq.row0 + (have ? r / G : 0)) * p.q_stride + (kvh * G + (have ? r % G : 0)) * D;
+        const uint16_t* qrow = p.q + int64_t(sq.row0 + (have ? (r >> lgG) : 0)) * p.q_stride + (kvh * G + (have ? (r & (G - 1)) : 0)) * D;
         load_q_words<D, 8, HALVES>(qrow, have ? g : 8, t, qw[x]);
 #pragma unroll
         for (int jj = 0; jj < 2; ++jj) {
             const int rr = r_first + x * 8 + 2 * t + jj;
-            mk.hi[x][jj] = rr < r_end ? pos0 + rr / G : -1;
+            mk.hi[x][jj] = rr < r_end ? pos0 + (rr >> lgG) : -1;
             mk.lo[x][jj] = max(0, mk.hi[x][jj] - p.window + 1);
         }
     }
@@ -275,14 +276,14 @@ window_rows_kernel(const __grid_constant__ WindowParams p) {
         }
         mbar_arrive_expect_tx(bar, T::kStageBytes);
         if constexpr (T::kSwz) {
-            const int y = kvh * bs + tok % bs;
+            const int y = kvh * bs + (tok & (bs - 1));
 #pragma unroll
             for (int h = 0; h < T::kRowBytes / 128; ++h) {
                 tma_load_3d(stage_of(s) + h * 2048, &p.tm_k, h * 128, y, id, bar, pol);
                 tma_load_3d(stage_of(s) + T::kTileBytes + h * 2048, &p.tm_v, h * 128, y, id, bar, pol);
             }
         } else {
-            const size_t row = (size_t(id) * p.c.Hkv + kvh) * bs + (tok % bs);
+            const size_t row = (size_t(id) * p.c.Hkv + kvh) * bs + (tok & (bs - 1));
             bulk_g2s(stage_of(s), static_cast<const uint8_t*>(p.c.k_pool) + row * T::kRowBytes, T::kTileBytes, bar, pol);
             bulk_g2s(stage_of(s) + T::kTileBytes, static_cast<const uint8_t*>(p.c.v_pool) + row * T::kRowBytes,
                      T::kTileBytes, bar, pol);
@@ -304,7 +305,7 @@ window_rows_kernel(const __grid_constant__ WindowParams p) {
         if (seg > k0) __syncthreads();  // the last segment's ids are no longer read
         // ids first, so that the copies start without waiting for the scales
         for (int k = seg + tid; k < seg_end; k += kThreads) {
-            int id = table[kt.tile(k) * kTile / bs];
+            int id = table[(kt.tile(k) * kTile) >> lg];
             if (id < 0 || id >= p.c.num_blocks) {
                 report(p.c.err, kErrBlockId);
                 id = -1;
@@ -317,23 +318,21 @@ window_rows_kernel(const __grid_constant__ WindowParams p) {
                 const int k = seg + warp + s * kWarps;
                 if (k < seg_end) issue(k, seg, (kk + s) % STAGES);
             }
-        int ev = kExpNone;
+        // the scales' loads fly while the tail is worked on
+        static_assert(kSegTiles == 2 * kThreads, "two scales a thread");
+        float2 sc[2];
         if (INT8) {
-            for (int k = seg + tid; k < seg_end; k += kThreads) {
-                const int id = s_id[k - seg];
-                const float2 sc = id < 0 ? make_float2(0.f, 0.f)
-                                         : __ldcg(reinterpret_cast<const float2*>(p.c.scales) + size_t(id) * p.c.Hkv + kvh);
-                s_sc[k - seg] = sc;
-                ev = max(ev, v_exp(sc.y));
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int k = seg + tid + u * kThreads, id = k < seg_end ? s_id[k - seg] : -1;
+                sc[u] = id < 0 ? make_float2(0.f, 0.f)
+                               : __ldcg(reinterpret_cast<const float2*>(p.c.scales) + size_t(id) * p.c.Hkv + kvh);
             }
-            ev = __reduce_max_sync(kFull, ev);
-            if (lane == 0) s_ev[warp] = ev;
         }
         if (seg == k0) {
             // ---- INT8: the partly filled last block, from the slot's bf16 tail, in
             // plain units, while the ring's first copies fly
             if (INT8 && k1 > kpool) {
-                const int slot = p.bt.slots[b];
                 const bool ok = slot >= 0 && slot < p.c.max_slots;
                 if (!ok && tid == 0) report(p.c.err, kErrSlot);
                 const int k = kpool + kWarps - 1 - warp;  // at most bs / 16 <= kWarps tail tiles
@@ -365,6 +364,17 @@ window_rows_kernel(const __grid_constant__ WindowParams p) {
         }
         float delta = 0.f;
         if (INT8) {
+            int ev = kExpNone;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int k = seg + tid + u * kThreads;
+                if (k < seg_end) {
+                    s_sc[k - seg] = sc[u];
+                    ev = max(ev, v_exp(sc[u].y));
+                }
+            }
+            ev = __reduce_max_sync(kFull, ev);
+            if (lane == 0) s_ev[warp] = ev;
             __syncthreads();  // the scales
             int e = ew;
 #pragma unroll
@@ -453,30 +463,40 @@ window_rows_kernel(const __grid_constant__ WindowParams p) {
         }
     }
     __syncthreads();
+    // the warps' factors of each row, over its sum unless partial
     const bool partial = ns > 1;
-    for (int e = tid; e < nrow * D; e += kThreads) {
-        const int r = e / D, dim = e % D;
-        float mm = -1e30f;
+    auto row_at = [&](int r) {  // of row r of the tile: its number among all rows and heads
+        const int rr = r_first + r;
+        return size_t(sq.row0 + (rr >> lgG)) * p.c.Hq + kvh * G + (rr & (G - 1));
+    };
+    if (tid < nrow) {
+        float mm = -1e30f, L = 0.f, c[kWarps];
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, s_ml[w][r][0]);
-        float L = 0.f, O = 0.f;
+        for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, s_ml[w][tid][0]);
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-            const float c = fast_exp2(s_ml[w][r][0] - mm);
-            L += s_ml[w][r][1] * c;
-            O += mo_of(w)[e] * c;
+            c[w] = fast_exp2(s_ml[w][tid][0] - mm);
+            L += s_ml[w][tid][1] * c[w];
         }
-        if (partial) {
-            const int rr = r_first + r;
-            const size_t at = (size_t(sq.row0 + rr / G) * p.c.Hq + kvh * G + rr % G) * p.max_splits + j;
-            p.ws_o[at * D + dim] = O;
-            if (dim == 0) {
-                p.ws_ml[at * 2] = mm;
-                p.ws_ml[at * 2 + 1] = L;
-            }
-        } else {
-            *reinterpret_cast<__nv_bfloat16*>(out_at(e)) = __float2bfloat16_rn(L > 0.f ? O / L : 0.f);
+        const float f = partial ? 1.f : L > 0.f ? 1.f / L : 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) s_ml[w][tid][0] = c[w] * f;
+        if (partial) reinterpret_cast<float2*>(p.ws_ml)[row_at(tid) * p.max_splits + j] = make_float2(mm, L);
+    }
+    __syncthreads();
+    for (int e = tid * 4; e < nrow * D; e += kThreads * 4) {
+        const int r = e / D, dim = e % D;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float4 x = *reinterpret_cast<const float4*>(mo_of(w) + e);
+            const float c = s_ml[w][r][0];
+            o.x += x.x * c; o.y += x.y * c; o.z += x.z * c; o.w += x.w * c;
         }
+        if (partial)
+            *reinterpret_cast<float4*>(p.ws_o + (row_at(r) * p.max_splits + j) * D + dim) = o;
+        else
+            *reinterpret_cast<uint2*>(out_at(e)) = make_uint2(f2_to_bf16x2(o.x, o.y), f2_to_bf16x2(o.z, o.w));
     }
     if (!partial) return;
 
@@ -487,34 +507,38 @@ window_rows_kernel(const __grid_constant__ WindowParams p) {
     __syncthreads();
     if (!s_last) return;
     float* wsm = reinterpret_cast<float*>(stages);  // [rows][ns] weights, over the row's sum
-    for (int r = warp; r < nrow; r += kWarps) {
-        const int rr = r_first + r;
-        const size_t row = size_t(sq.row0 + rr / G) * p.c.Hq + kvh * G + rr % G;
-        const float2* ml = reinterpret_cast<const float2*>(p.ws_ml) + row * p.max_splits;
-        float mm = -1e30f;
-        for (int q = lane; q < ns; q += 32) mm = fmaxf(mm, __ldcg(ml + q).x);
+    static_assert(R * 8 <= kThreads, "eight threads a row");
+    {
+        const int r = tid >> 3, sub = tid & 7;
+        const bool have = r < nrow;
+        const float2* ml = reinterpret_cast<const float2*>(p.ws_ml) + row_at(have ? r : 0) * p.max_splits;
+        float mm = -1e30f, L = 0.f;
+        for (int q = sub; q < ns; q += 8) mm = fmaxf(mm, __ldcg(ml + q).x);
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) mm = fmaxf(mm, __shfl_xor_sync(kFull, mm, off));
-        float L = 0.f;
-        for (int q = lane; q < ns; q += 32) {
+        for (int off = 4; off > 0; off >>= 1) mm = fmaxf(mm, __shfl_xor_sync(kFull, mm, off));
+        for (int q = sub; q < ns; q += 8) {
             const float2 v = __ldcg(ml + q);
             const float c = fast_exp2(v.x - mm);
-            wsm[r * ns + q] = c;
+            if (have) wsm[r * ns + q] = c;
             L += c * v.y;
         }
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(kFull, L, off);
-        if (lane == 0) s_ml[0][r][0] = L > 0.f ? 1.f / L : 0.f;
+        for (int off = 4; off > 0; off >>= 1) L += __shfl_xor_sync(kFull, L, off);
+        if (have && sub == 0) s_ml[0][r][0] = L > 0.f ? 1.f / L : 0.f;
     }
     __syncthreads();
-    for (int e = tid; e < nrow * D; e += kThreads) {
-        const int r = e / D, dim = e % D, rr = r_first + r;
-        const size_t row = size_t(sq.row0 + rr / G) * p.c.Hq + kvh * G + rr % G;
-        const float* o = p.ws_o + row * p.max_splits * D + dim;
-        float acc = 0.f;
-#pragma unroll 8
-        for (int q = 0; q < ns; ++q) acc += wsm[r * ns + q] * __ldcg(o + size_t(q) * D);
-        *reinterpret_cast<__nv_bfloat16*>(out_at(e)) = __float2bfloat16_rn(acc * s_ml[0][r][0]);
+    for (int e = tid * 4; e < nrow * D; e += kThreads * 4) {
+        const int r = e / D, dim = e % D;
+        const float* o = p.ws_o + row_at(r) * p.max_splits * D + dim;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int q = 0; q < ns; ++q) {
+            const float4 x = __ldcg(reinterpret_cast<const float4*>(o + size_t(q) * D));
+            const float c = wsm[r * ns + q];
+            acc.x += x.x * c; acc.y += x.y * c; acc.z += x.z * c; acc.w += x.w * c;
+        }
+        const float f = s_ml[0][r][0];
+        *reinterpret_cast<uint2*>(out_at(e)) = make_uint2(f2_to_bf16x2(acc.x * f, acc.y * f), f2_to_bf16x2(acc.z * f, acc.w * f));
     }
     if (tid == 0) *cnt = 0;  // ready for the next call
 }
