@@ -33,11 +33,12 @@ struct RowsMask {
     int dead_lo, dead_hi;  // tokens in [sinks, dead_lo) and above dead_hi are seen by no row
 };
 
-// One 16-token tile at token tok. any: some of it is there; masked: some row
-// does not see all of it. The other arguments are those of mma_tile.
-template <int D, bool I8, bool SHIFT, bool HALVES, int NT, class Rows>
-__device__ __forceinline__ void rows_tile(const Rows& K, const Rows& V, int tok, bool any, bool masked, float ksc,
-                                          float vmul, float delta, const uint32_t (&qf)[NT][D / 16][2],
+// One 16-token tile at token tok. any: some of it is there. MASKED: some row may
+// not see all of it (two copies of the code: most tiles are seen whole, and as a
+// condition inside the mask's instructions are issued for them too, predicated
+// off). The other arguments are those of mma_tile.
+template <int D, bool I8, bool SHIFT, bool HALVES, int NT, bool MASKED, class Rows>
+__device__ __forceinline__ void rows_tile(const Rows& K, const Rows& V, int tok, bool any, float ksc, float vmul, float delta, const uint32_t (&qf)[NT][D / 16][2],
                                           const float (&hs)[NT][2], const RowsMask<NT>& mk, int g, int t,
                                           RowsState<D, NT>& st) {
     using Gm = Geom<D, I8>;
@@ -77,7 +78,7 @@ __device__ __forceinline__ void rows_tile(const Rows& K, const Rows& V, int tok,
     for (int x = 0; x < NT; ++x) {
         const float f0 = ksc * hs[x][0], f1 = ksc * hs[x][1];
         s[x][0] *= f0; s[x][1] *= f1; s[x][2] *= f0; s[x][3] *= f1;
-        if (masked) {
+        if (MASKED) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int tt = tok + g + (i >> 1) * 8;
@@ -129,7 +130,7 @@ __device__ __forceinline__ void rows_tile(const Rows& K, const Rows& V, int tok,
     load_run<Gm::kVB>(V, 2 * t + 1, vc, v1);
     load_run<Gm::kVB>(V, 2 * t + 8, vc, v2);
     load_run<Gm::kVB>(V, 2 * t + 9, vc, v3);
-    if (masked) {
+    if (MASKED) {
         const auto dead = [&](int i) {
             const int tt = tok + i;
             return !any || tt > mk.dead_hi || (tt < mk.dead_lo && tt >= mk.sinks);
@@ -324,9 +325,9 @@ window_rows_kernel(const __grid_constant__ WindowParams p) {
         if (INT8) {
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                const int k = seg + tid + u * kThreads, id = k < seg_end ? s_id[k - seg] : -1;
-                sc[u] = id < 0 ? make_float2(0.f, 0.f)
-                               : __ldcg(reinterpret_cast<const float2*>(p.c.scales) + size_t(id) * p.c.Hkv + kvh);
+                // (a block that is not there: block 0's, dropped when they are used)
+                const int k = seg + tid + u * kThreads, id = k < seg_end ? max(0, s_id[k - seg]) : 0;
+                sc[u] = __ldcg(reinterpret_cast<const float2*>(p.c.scales) + size_t(id) * p.c.Hkv + kvh);
             }
         }
         if (seg == k0) {
@@ -348,7 +349,7 @@ window_rows_kernel(const __grid_constant__ WindowParams p) {
                     const size_t rbase = (size_t(slot) * p.c.Hkv + kvh) * bs + (tok - nfull);
                     const GmemRows kr{reinterpret_cast<const uint8_t*>(p.c.k_tail + rbase * D), D * 2};
                     const GmemRows vr{reinterpret_cast<const uint8_t*>(p.c.v_tail + rbase * D), D * 2};
-                    rows_tile<D, false, INT8, false, NT>(kr, vr, tok, true, is_masked(tok), 1.f, 1.f, 0.f, qb, hb, mk,
+                    rows_tile<D, false, INT8, false, NT, true>(kr, vr, tok, true, 1.f, 1.f, 0.f, qb, hb, mk,
                                                          g, t, st);
                 }
             }
@@ -369,6 +370,7 @@ window_rows_kernel(const __grid_constant__ WindowParams p) {
             for (int u = 0; u < 2; ++u) {
                 const int k = seg + tid + u * kThreads;
                 if (k < seg_end) {
+                    if (s_id[k - seg] < 0) sc[u] = make_float2(0.f, 0.f);
                     s_sc[k - seg] = sc[u];
                     ev = max(ev, v_exp(sc[u].y));
                 }
@@ -419,10 +421,12 @@ window_rows_kernel(const __grid_constant__ WindowParams p) {
             }
             if constexpr (T::kSwz) {
                 const SwzRows kr{stage_of(s)}, vr{stage_of(s) + T::kTileBytes};
-                rows_tile<D, INT8, INT8, HALVES, NT>(kr, vr, tok, any, masked, ksc, vmul, delta, qf, hs, mk, g, t, st);
+                if (masked) rows_tile<D, INT8, INT8, HALVES, NT, true>(kr, vr, tok, any, ksc, vmul, delta, qf, hs, mk, g, t, st);
+                else rows_tile<D, INT8, INT8, HALVES, NT, false>(kr, vr, tok, any, ksc, vmul, delta, qf, hs, mk, g, t, st);
             } else {
                 const SmemRows kr{stage_of(s), Gm::kRow}, vr{stage_of(s) + T::kTileBytes, Gm::kRow};
-                rows_tile<D, INT8, INT8, false, NT>(kr, vr, tok, any, masked, ksc, vmul, delta, qf, hs, mk, g, t, st);
+                if (masked) rows_tile<D, INT8, INT8, false, NT, true>(kr, vr, tok, any, ksc, vmul, delta, qf, hs, mk, g, t, st);
+                else rows_tile<D, INT8, INT8, false, NT, false>(kr, vr, tok, any, ksc, vmul, delta, qf, hs, mk, g, t, st);
             }
             __syncwarp();
             const int nxt = k + STAGES * kWarps;
