@@ -30,8 +30,9 @@ constexpr int kGatherTokens = 16;
 
 struct GatherRow {
     const uint8_t* src;  // nullptr: left out
-    float scale;         // INT8; 0: a bf16 row of the tail
-    uint32_t pad;
+    float scale;         // of a row of codes
+    uint16_t v;          // to v_out
+    uint16_t codes;      // INT8 codes; otherwise bf16 values (a bf16 pool, or the tail)
     int64_t dst;         // element offset in the outputs
 };
 
@@ -97,6 +98,8 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const __grid_con
             GatherRow r;
             r.src = nullptr;
             r.scale = 0.f;
+            r.v = uint16_t(kv);
+            r.codes = INT8 && id >= 0;
             r.dst = int64_t(sq.row0 + i0 + tl) * p.out_stride + h * D;
             if (id >= 0) {
                 r.src = static_cast<const uint8_t*>(kv ? p.c.v_pool : p.c.k_pool) +
@@ -106,7 +109,6 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const __grid_con
                 r.src = reinterpret_cast<const uint8_t*>((kv ? p.c.v_tail : p.c.k_tail) +
                                                          ((size_t(slot) * Hkv + h) * bs + off) * D);
             }
-            r.pad = uint32_t(kv);
             s_row[tid] = r;
         }
         __syncthreads();
@@ -120,7 +122,7 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const __grid_con
                 if (e >= rows * CH) break;
                 const GatherRow& r = s_row[e / CH];
                 if (!r.src) continue;
-                if (INT8 && r.scale != 0.f) {
+                if (INT8 && r.codes) {
                     const uint2 x = __ldg(reinterpret_cast<const uint2*>(r.src + e % CH * 8));
                     w[u].x = x.x;
                     w[u].y = x.y;
@@ -134,14 +136,14 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const __grid_con
                 if (e >= rows * CH) break;
                 const GatherRow& r = s_row[e / CH];
                 if (!r.src) continue;
-                void* out = r.pad ? p.v_out : p.k_out;
+                void* out = r.v ? p.v_out : p.k_out;
                 const int64_t at = r.dst + e % CH * 8;
-                if (!F32 && (!INT8 || r.scale == 0.f)) {
+                if (!F32 && (!INT8 || !r.codes)) {
                     *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at) = w[u];
                     continue;
                 }
                 float2 x[4];
-                if (INT8 && r.scale != 0.f) {
+                if (INT8 && r.codes) {
                     s8x4_to_f4(w[u].x, x[0], x[1]);
                     s8x4_to_f4(w[u].y, x[2], x[3]);
 #pragma unroll

@@ -381,3 +381,24 @@ def test_empty_calls():
     pkv.pkv_rope_append(s.lc.desc, s.batch, None, None, kv, kv)
     pkv.pkv_gather_kv(s.lc.desc, s.batch, kv, kv)
     assert NAN != NAN and s.error_bits() == 0
+
+
+@pytest.mark.parametrize("heads", [(4, 2, 64), (8, 2, 128)])
+@pytest.mark.parametrize("new", [[1, 2], [60, 130]])
+def test_blocks_whose_scale_is_zero(heads, new):
+    """An INT8 block with scales of zero (one that another program wrote) stands for zeros, whatever its codes."""
+    s = Setup(7, new, [100, 200], heads, 16, True)
+    for b, i in ((0, 0), (0, 5), (1, 3), (1, 11)):
+        s.lc.scales[int(s.table[b, i])] = 0.0
+        for n in "kv":
+            s.values[n][b][i * 16:(i + 1) * 16] = 0.0
+    back = [torch.full((s.T, s.hkv, s.d), 3.0, dtype=torch.float32, device="cuda") for _ in range(2)]
+    pkv.pkv_gather_kv(s.lc.desc, s.batch, *back)
+    for n, got in zip("kv", back):
+        want = np.concatenate([x[c - m:] for x, m, c in zip(s.values[n], s.new, s.ctx)])
+        assert torch.equal(got.cpu(), torch.as_tensor(want).float())
+    for window, sinks in ((0, 0), (40, 4)):
+        ref, mag = attention(s, window, sinks)
+        for split in ("auto", 48):
+            assert_attention(run_window(s, window, sinks, split), ref, mag)
+    assert s.error_bits() == 0
