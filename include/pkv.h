@@ -401,11 +401,13 @@ int pkv_rope_append(const pkv_cache_desc* c, const pkv_batch_desc* batch, const 
  * p (sinks then means nothing). For each of them and query head h
  *   out[row][h] = sum_t softmax_t(sm_scale * q[row][h] . k_t) v_t
  * with K and V read as pkv_decode_attention reads them (INT8 dequantized, the
- * partly filled last block from the slot's tail). q, out: [num_tokens][Hq][d]
- * bf16 with token strides of q_stride, out_stride elements (multiples of 8;
- * both 16-byte aligned); sm_scale is finite and not negative. fp32 accumulation. Rows of a sequence with a bad
- * context length are zero; a token whose block id or slot is bad counts as
- * not visible, and a row that sees nothing is zero.
+ * partly filled last block from the slot's tail; V scales below 2^-60 may
+ * count as zero). q, out: [num_tokens][Hq][d] bf16 with token strides of
+ * q_stride, out_stride elements (multiples of 8; both 16-byte aligned); out may
+ * be q itself with the same stride, otherwise they must not overlap. sm_scale
+ * is finite and not negative, and scores are within +-1e30. fp32 accumulation.
+ * Rows of a sequence with a bad context length are zero; a token whose block id
+ * or slot is bad counts as not visible, and a row that sees nothing is zero.
  *
  * Blocks before the window (and behind the sinks) are neither read nor looked
  * up: their table entries may be -1 and their memory in use elsewhere. Rows
