@@ -134,9 +134,8 @@ window_tc_kernel(const __grid_constant__ WindowParams p) {
     __shared__ __align__(16) uint4 s_next;
     __shared__ uint32_t s_tmem;
     __shared__ int s_last;
-    // by tile % 8: units of a key tile that are not there (bits 0 ..) and, INT8,
-    // whose V is zero (bits 16 ..)
-    __shared__ uint32_t s_bad[8];
+    // units of a key tile that are not there, by tile % 8; INT8, [1]: or whose V is zero
+    __shared__ uint32_t s_bad[1 + INT8][8];
     __shared__ float2 s_sc[INT8 ? 8 : 1][8];   // units' K scale times p.qscale, log2 of the V scale
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -241,7 +240,7 @@ window_tc_kernel(const __grid_constant__ WindowParams p) {
                     tc_fence_after();
                     const int u0 = (k0 + jj) * U;  // first block of the tile in the list
                     const int slot = (tiles + jj) & 7;
-                    const uint32_t bad = s_bad[slot] & 0xFFFFu;
+                    const uint32_t bad = s_bad[0][slot];
                     const int t_first = kt.tile(u0) << lg;
                     const bool masked =
                         bad != 0 || u0 < kt.nsink || t_first + kTcKeys - 1 > pf || t_first < pl - p.window + 1;
@@ -525,7 +524,7 @@ window_tc_kernel(const __grid_constant__ WindowParams p) {
                     if (role == 0) {
                         if (lane < U && u < kt.n && !there) report(p.c.err, kErrBlockId);
                         const uint32_t missing = __ballot_sync(kFull, lane < U && !there);
-                        if (lane == 0) s_bad[(tiles + jj) & 7] = missing;
+                        if (lane == 0) s_bad[0][(tiles + jj) & 7] = missing;
                     } else {
                         const int t0 = kt.tile(u) << lg;
                         fix = __any_sync(kFull, there && (t0 + bs - 1 > p_last || (t0 < dead_lo && t0 + bs > p.sinks)));
@@ -595,7 +594,7 @@ window_tc_kernel(const __grid_constant__ WindowParams p) {
                     const uint32_t raw = raw0 + uint32_t(v) * T::kRawBytes + uint32_t(row0 * D + c * 16);
                     uint4 w[NC];
                     each<NC>([&](auto k) { w[k.value] = lds128_at<k.value * kStep * D>(raw); });
-                    const uint32_t units = s_bad[(it / 2) & 7], bad = (units | (v ? units >> 16 : 0u)) & 0xFFFFu;
+                    const uint32_t bad = s_bad[v][(it / 2) & 7];
                     const int u0 = tile * U, t0 = kt.tile(u0) << lg;
                     // a plain tile: every block is in the pool and (V) some row sees every token
                     const bool plain = bad == 0 && u0 >= kt.nsink && t0 + kTcKeys <= min(nfull, p_last + 1) && t0 >= dead_lo;
@@ -765,18 +764,21 @@ window_tc_kernel(const __grid_constant__ WindowParams p) {
                 const uint32_t total = uint32_t(__popc(__ballot_sync(kFull, id >= 0))) * bytes;
                 float2 sc = make_float2(1.f, 1.f);
                 if (id >= 0) sc = __ldcg(reinterpret_cast<const float2*>(p.c.scales) + size_t(id) * p.c.Hkv + kvh);
-                // V scales below this are taken for zero, by way of zero rows: 2^-40 and
-                // the scale in one exponent leave a weight 26 bits above fp32's smallest
-                // (a block's quantizer gives 1e-6 / 127 at the least)
-                const bool zero = !(sc.y >= 0x1p-60f);
-                const uint32_t zeros = __ballot_sync(kFull, zero);
 #pragma unroll 1
                 for (int v = 0; v < 2; ++v) {
                     if (tiles + jj > 0 && !(ok = wait(&bars.raw_empty[v], tiles + jj - 1))) break;
                     if (v == 0) {
-                        // never 0: a hidden token's score is -infinity, and 0 times that is not a number
+                        // K: never 0: a hidden token's score is -infinity, and 0 times that is not
+                        // a number. V scales below 2^-60 are taken for zero, by way of zero rows:
+                        // 2^-40 and the scale in one exponent leave a weight 26 bits above fp32's
+                        // smallest (a block's quantizer gives 1e-6 / 127 at the least).
+                        const bool zero = !(sc.y >= 0x1p-60f);
+                        const uint32_t zeros = __ballot_sync(kFull, zero);
                         if (lane < U) s_sc[slot][lane] = make_float2(fmaxf(sc.x * p.qscale, 1e-37f), zero ? 0.f : __log2f(sc.y));
-                        if (lane == 0) s_bad[slot] = missing | zeros << 16;
+                        if (lane == 0) {
+                            s_bad[0][slot] = missing;
+                            s_bad[INT8][slot] = missing | zeros;
+                        }
                     }
                     __syncwarp();
                     const uint32_t full = bar(&bars.raw_full[v]);
