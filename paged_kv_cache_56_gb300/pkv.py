@@ -540,7 +540,10 @@ def make_rope(inv_freq: torch.Tensor, *, interleaved: bool = False, scale: float
     token's index in its context). The tensors are kept alive by the descriptor."""
     d = RopeDesc(_dev(inv_freq, "inv_freq", torch.float64), _opt_dev(positions, "positions", torch.int32),
                  2 * inv_freq.numel(), 1 if interleaved else 0, scale)
+    if positions is not None and positions.device != inv_freq.device:
+        raise ValueError("inv_freq and positions must be on one device")
     d.keep, d.num_positions = (inv_freq, positions), None if positions is None else positions.numel()
+    d.device = inv_freq.device
     return d
 
 
@@ -583,8 +586,11 @@ def pkv_rope_append(desc: CacheDesc, batch: BatchDesc, rope, q, k: torch.Tensor,
     op, os_ = (qp, qs) if q is None or q_out is None else _rows(q_out, "q_out", batch, hq, d)
     kp, ks = _rows(k, "k", batch, hkv, d)
     vp, vs = _rows(v, "v", batch, hkv, d)
-    if rope is not None and rope.num_positions is not None and rope.num_positions < batch.num_tokens:
-        raise ValueError(f"positions hold {rope.num_positions} entries, need {batch.num_tokens}")
+    if rope is not None:
+        if rope.device != batch.device:
+            raise ValueError(f"rope must be on {batch.device}")
+        if rope.num_positions is not None and rope.num_positions < batch.num_tokens:
+            raise ValueError(f"positions hold {rope.num_positions} entries, need {batch.num_tokens}")
     _check("pkv_rope_append",
            lib().pkv_rope_append(ctypes.byref(desc), ctypes.byref(batch), None if rope is None else ctypes.byref(rope),
                                  qp, qs, kp, ks, vp, vs, op, os_, _batch_stream(batch, stream)))
@@ -610,6 +616,8 @@ def pkv_window_attention(desc: CacheDesc, batch: BatchDesc, q: torch.Tensor, out
     qp, qs = _rows(q, "q", batch, hq, d)
     op, os_ = _rows(out, "out", batch, hq, d)
     wp, wn = (None, 0) if ws is None else (_dev(ws, "ws", ws.dtype), ws.numel() * ws.element_size())
+    if ws is not None and ws.device != batch.device:
+        raise ValueError(f"ws must be on {batch.device}")
     _check("pkv_window_attention",
            lib().pkv_window_attention(ctypes.byref(desc), ctypes.byref(batch), qp, qs, window, sinks, sm_scale,
                                       split_tokens, wp, wn, op, os_, _batch_stream(batch, stream)))
@@ -626,6 +634,8 @@ def pkv_gather_kv(desc: CacheDesc, batch: BatchDesc, k_out: torch.Tensor, v_out:
     vp, vs = _rows(v_out, "v_out", batch, hkv, d, k_out.dtype)
     if ks != vs:
         raise ValueError("k_out and v_out must have the same token stride")
+    if first is not None and first.device != batch.device:
+        raise ValueError(f"first must be on {batch.device}")
     kind = PKV_OUT_FP32 if k_out.dtype == torch.float32 else PKV_OUT_BF16
     _check("pkv_gather_kv",
            lib().pkv_gather_kv(ctypes.byref(desc), ctypes.byref(batch), _opt_dev(first, "first", torch.int32, batch.B),

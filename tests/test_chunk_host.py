@@ -334,3 +334,16 @@ def test_division_steps_of_the_quantizer():
                 for _ in range(2):
                     q = rn(rn(f - q * scale) * inv + q)
                 assert q == rn(f / scale)
+
+
+def test_everything_of_a_call_is_on_one_device():
+    b = batch()
+    b.device, b.keep = torch.device("cpu"), None
+    q = torch.zeros((8, 4, 128), dtype=torch.bfloat16)
+    r = pkv.RopeDesc()
+    r.device, r.num_positions = torch.device("cuda", 1), None
+    for call in (lambda: pkv.pkv_rope_append(desc(), b, r, None, q[:, :2], q[:, :2]),
+                 lambda: pkv.pkv_gather_kv(desc(), b, q[:, :2], q[:, :2], torch.zeros(2, dtype=torch.int32, device="meta")),
+                 lambda: pkv.pkv_window_attention(desc(), b, q, q, 0, 0, 0.1, 0, torch.zeros(8, device="meta"))):
+        with pytest.raises(ValueError):
+            call()
