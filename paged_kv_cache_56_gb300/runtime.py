@@ -629,12 +629,21 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, stretch: float = 1.
     return f * keep + f / stretch * (1 - keep), 0.1 * math.log(stretch) + 1.0
 
 
+def _on(stream):
+    """Context with `stream` (a torch stream, a handle or None) as the current one."""
+    if stream is not None and not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream))
+    return torch.cuda.stream(stream)  # None: no change
+
+
 class ChunkBuffers:
     """Device-side batch of up to max_batch sequences bringing up to max_tokens
     tokens in all, at most max_new each; pinned mirrors make the uploads async.
     The descriptor stays the same from batch to batch (its arrays are refilled),
     so that a captured graph of the chunk operators can be replayed on it: a
-    batch of fewer sequences leaves the rest without tokens."""
+    batch of fewer sequences leaves the rest without tokens. max_new chooses the
+    attention's kernel: decode steps and drafted tokens want buffers of their
+    own, not a prompt's."""
 
     def __init__(self, cache: PagedKVCache, max_batch: int, max_tokens: int, max_new: int):
         dev = cache.device
@@ -700,11 +709,12 @@ def extend_step(cache: PagedKVCache, bufs: ChunkBuffers, req_ids, counts, q, k, 
     """Host plan + upload + kernels of counts[i] new tokens of each sequence;
     advances the sequences. q, k, v, out: per layer, rows of the sequences one
     after another, bufs.max_tokens rows long (rows behind the batch's are not
-    touched)."""
+    touched). The uploads, too, are on `stream` (default: the current one)."""
     plan = cache.plan_chunk(req_ids, counts)
-    cache.apply_cow(plan, stream)
-    bufs.upload(plan)
-    run_chunk(cache, bufs, q, k, v, out, sm_scale, rope, window, sinks, stream)
+    with _on(stream):
+        cache.apply_cow(plan)
+        bufs.upload(plan)
+        run_chunk(cache, bufs, q, k, v, out, sm_scale, rope, window, sinks)
     cache.commit_chunk(req_ids, counts)
     return plan
 
@@ -712,7 +722,13 @@ def extend_step(cache: PagedKVCache, bufs: ChunkBuffers, req_ids, counts, q, k, 
 def read_back(cache: PagedKVCache, layer: int, req_ids, dtype=torch.bfloat16, stream=None):
     """(k, v, starts): the rows of whole contexts in token order, dequantized --
     [sum of lengths, Hkv, d] each, those of req_ids[i] at starts[i] ..
-    starts[i+1]-1 -- e.g. to move sequences to another cache."""
+    starts[i+1]-1 -- e.g. to move sequences to another cache. They are made on
+    `stream` (default: the current one)."""
+    with _on(stream):
+        return _read_back(cache, layer, req_ids, dtype)
+
+
+def _read_back(cache: PagedKVCache, layer: int, req_ids, dtype):
     lens = [cache.seqs[r].length for r in req_ids]
     starts = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
     T, dev = int(starts[-1]), cache.layers[layer].k_pool.device
@@ -723,5 +739,5 @@ def read_back(cache: PagedKVCache, layer: int, req_ids, dtype=torch.bfloat16, st
         tables = pkv.pkv_build_block_tables(cache.alloc, req_ids, cache.max_blocks)
         slots = up(np.array([cache.seqs[r].slot for r in req_ids])) if cache.layers[layer].int8 else None
         batch = pkv.make_batch(up(starts), up(tables), up(np.array(lens)), slots, num_tokens=T, max_tokens=max(lens))
-        pkv.pkv_gather_kv(cache.layers[layer].desc, batch, k, v, None, stream)
+        pkv.pkv_gather_kv(cache.layers[layer].desc, batch, k, v)
     return k, v, starts
