@@ -149,40 +149,20 @@ int check_window(const pkv_cache_desc* c, const pkv_batch_desc* batch, int windo
 
 // Tensor map of the queries for window_tc_kernel: [tokens][Hkv][G][d] with
 // boxes of 128 rows (128 / G tokens x the group) x 64 elements, 128-byte
-// swizzle. The last maps are kept per thread, as the pools' are.
+// swizzle.
 int q_tensor_map(const pkv_cache_desc* c, int tokens, const void* q, int64_t stride, CUtensorMap* out) {
-    struct Entry {
-        CUtensorMap map;
-        const void* q;
-        int64_t stride;
-        int tokens, hq, hkv, d;
-    };
-    thread_local Entry cache[64] = {};
-    const uint64_t h = (uint64_t(reinterpret_cast<uintptr_t>(q)) >> 4) * 0x9E3779B97F4A7C15ull;
-    Entry& e = cache[h >> 58];
-    if (e.q != q || e.stride != stride || e.tokens != tokens || e.hq != c->num_q_heads || e.hkv != c->num_kv_heads ||
-        e.d != c->head_dim) {
-        const PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
-        if (!enc) return PKV_ERR_CUDA;
-        const cuuint64_t g = cuuint64_t(c->num_q_heads / c->num_kv_heads), d = cuuint64_t(c->head_dim);
-        const cuuint64_t dims[4] = {d, g, cuuint64_t(c->num_kv_heads), cuuint64_t(tokens)};
-        const cuuint64_t strides[3] = {d * 2, g * d * 2, cuuint64_t(stride) * 2};
-        const cuuint32_t box[4] = {64, cuuint32_t(g), 1, cuuint32_t(128 / g)};
-        const cuuint32_t elem[4] = {1, 1, 1, 1};
-        e.q = nullptr;
-        if (enc(&e.map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(q), dims, strides, box, elem,
-                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-            return PKV_ERR_CUDA;
-        e.q = q;
-        e.stride = stride;
-        e.tokens = tokens;
-        e.hq = c->num_q_heads;
-        e.hkv = c->num_kv_heads;
-        e.d = c->head_dim;
-    }
-    *out = e.map;
-    return PKV_OK;
+    const PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (!enc) return PKV_ERR_CUDA;
+    const cuuint64_t g = cuuint64_t(c->num_q_heads / c->num_kv_heads), d = cuuint64_t(c->head_dim);
+    const cuuint64_t dims[4] = {d, g, cuuint64_t(c->num_kv_heads), cuuint64_t(tokens)};
+    const cuuint64_t strides[3] = {d * 2, g * d * 2, cuuint64_t(stride) * 2};
+    const cuuint32_t box[4] = {64, cuuint32_t(g), 1, cuuint32_t(128 / g)};
+    const cuuint32_t elem[4] = {1, 1, 1, 1};
+    return enc(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(q), dims, strides, box, elem,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? PKV_OK
+               : PKV_ERR_CUDA;
 }
 
 bool is_empty(const pkv_batch_desc* b) { return b->B == 0 || b->num_tokens == 0 || b->max_tokens == 0; }
@@ -266,6 +246,9 @@ int pkv_window_attention(const pkv_cache_desc* c, const pkv_batch_desc* batch, c
     Plan pl;
     if ((st = make_plan(c, batch, window, sinks, &pl)) != PKV_OK) return st;
     const int splits = max_splits_of(c, batch, pl, split_tokens);
+    // window_tc_kernel's planner and warps without rows wait for as long as an item
+    // takes, a second at most; 2^25 tokens take about half of that
+    if (pl.tc && (pl.key_tiles + splits - 1) / splits > (1 << 25) / kTile) return PKV_ERR_UNSUPPORTED;
     const Workspace w = workspace_of(c, batch, pl, splits);
     if (w.total > 0 && (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < w.total)) return PKV_ERR_INVALID;
 
@@ -299,8 +282,9 @@ int pkv_window_attention(const pkv_cache_desc* c, const pkv_batch_desc* batch, c
     p.split_tiles = splits > 1 ? split_tokens / kTile : 0;
     p.max_splits = splits;
     p.row_tiles = pl.row_tiles;
-    // never 0: a hidden token's score is -infinity, and 0 times that is not a number
-    p.qscale = std::max(sm_scale * 1.4426950408889634f, 1e-37f);
+    // never 0 or infinite: a hidden token's score is -infinity, and 0 times that is
+    // not a number, nor is an infinite scale times a score of 0
+    p.qscale = std::min(std::max(sm_scale * 1.4426950408889634f, 1e-37f), 3.4e38f);
     // window_tc_kernel: the row tiles of all sequences are one list
     const int64_t g = c->num_q_heads / c->num_kv_heads;
     p.item_tiles = 0;

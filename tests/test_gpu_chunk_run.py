@@ -288,3 +288,61 @@ def test_workspaces_are_checked():
                           positions=torch.zeros(0, dtype=torch.int32, device="cuda"))
         kv = torch.zeros((1, 8, 128), dtype=torch.bfloat16, device="cuda")
         pkv.pkv_rope_append(s.lc.desc, s.batch, r, None, kv, kv)
+
+
+def test_output_in_place_of_the_queries():
+    for new, split in (([1, 3], 48), ([1, 3], 0), ([40, 300], 0), ([40, 300], 128)):
+        s = Setup(6, new, [400, 300], (8, 2, 128), 16, False)
+        ref, mag = attention(s, 100, 4)
+        n = pkv.pkv_window_ws_bytes(s.lc.desc, s.batch, 100, 4, split)
+        ws = torch.zeros(n, dtype=torch.uint8, device="cuda") if n else None
+        q = s.q.cuda()
+        pkv.pkv_window_attention(s.lc.desc, s.batch, q, q, 100, 4, s.d ** -0.5, split, ws)
+        assert_attention(q, ref, mag)
+        assert s.error_bits() == 0
+
+
+@pytest.mark.parametrize("new", [[1], [70]])
+def test_largest_and_smallest_scale(new):
+    """sm_scale 0 weighs every visible token alike; with the largest one the best score takes all, and q = 0 does as 0."""
+    s = Setup(8, new, [100], (4, 2, 64), 16, False)
+    ref, mag = attention(s, 0, 0, 0.0)
+    q, out = s.q.cuda(), torch.empty((s.T, 4, 64), dtype=torch.bfloat16, device="cuda")
+    pkv.pkv_window_attention(s.lc.desc, s.batch, q, out, 0, 0, 0.0)
+    assert_attention(out, ref, mag)
+    pkv.pkv_window_attention(s.lc.desc, s.batch, torch.zeros_like(q), out, 0, 0, 3.0e38)
+    assert_attention(out, ref, mag)
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_a_step_on_another_stream(handle):
+    """Uploads, copies and kernels of a step are ordered on the stream that it is given."""
+    m = Model((8, 2, 128), 16, [False, True], seqs=2, blocks=40)
+    m.cache.add_sequence(1)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    m.step([1], [45], 30, 4, stream=side.cuda_stream if handle else side)
+    m.cache.fork(1, 2)
+    torch.cuda.synchronize()
+    m.step([1, 2], [30, 3], 30, 4, stream=side.cuda_stream if handle else side)
+    want = read_back(m.cache, 0, [1, 2], torch.float32)
+    got = read_back(m.cache, 0, [1, 2], torch.float32, side.cuda_stream if handle else side)
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_too_long_a_split_is_refused():
+    s = Setup(8, [40], [100], (4, 2, 64), 16, False)
+    q, out = s.q.cuda(), torch.empty((40, 4, 64), dtype=torch.bfloat16, device="cuda")
+    table = torch.full((1, (2 ** 25 + 256) // 16), -1, dtype=torch.int32, device="cuda")
+    table[:, :s.width] = s.d_table
+    batch = pkv.make_batch(s.d_starts, table, s.d_ctx, num_tokens=40, max_tokens=40)
+    with pytest.raises(pkv.PkvError) as e:
+        pkv.pkv_window_attention(s.lc.desc, batch, q, out, 0, 0, 0.125)
+    assert e.value.code == pkv.PKV_ERR_UNSUPPORTED
+    ws = torch.zeros(pkv.pkv_window_ws_bytes(s.lc.desc, batch, 0, 0, 2 ** 24), dtype=torch.uint8, device="cuda")
+    for args in ((0, 0, 0.125, 2 ** 24, ws), (4096, 4, 0.125)):
+        pkv.pkv_window_attention(s.lc.desc, batch, q, out, *args)
+        ref, mag = attention(s, 0, 0, 0.125)
+        assert_attention(out, ref, mag)
+    assert s.error_bits() == 0
