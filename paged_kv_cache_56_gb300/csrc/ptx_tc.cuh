@@ -136,8 +136,8 @@ __device__ __forceinline__ void next_cta(uint32_t answer, uint32_t bar) {
                  "r"(bar)
                  : "memory");
 }
-// The answer: false if there was none left, else the CTA's x and y.
-__device__ __forceinline__ bool next_cta_read(uint32_t answer, int& x, int& y) {
+// The answer: false if there was none left, else the CTA's x.
+__device__ __forceinline__ bool next_cta_read(uint32_t answer, int& x) {
     uint32_t got, a = 0, b = 0, c;
     asm volatile(
         "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t"
@@ -150,7 +150,6 @@ __device__ __forceinline__ bool next_cta_read(uint32_t answer, int& x, int& y) {
         : "r"(answer)
         : "memory");
     x = int(a);
-    y = int(b);
     return got != 0;
 }
 

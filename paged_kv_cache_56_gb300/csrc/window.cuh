@@ -24,15 +24,16 @@ struct WindowParams {
     const uint16_t* q;
     uint16_t* out;
     int64_t q_stride, out_stride;
-    float* ws_o;        // [num_tokens * Hq][max_splits][D] partial outputs
-    float* ws_ml;       // [num_tokens * Hq][max_splits][2]
+    float* ws_o;        // [rows][max_splits][D] partial outputs; rows: of q, of all heads
+    float* ws_ml;       // [rows][max_splits][2]     (window_tc_kernel: of the items that are split)
     int32_t* ws_count;  // arrivals at each (sequence, kv head, row tile)
     int32_t window;     // INT32_MAX: none
     int32_t sinks;
     int32_t split_tiles;  // 16-token tiles a split (0: no split)
     int32_t max_splits;
     int32_t row_tiles;  // row tiles of max_tokens tokens
-    int32_t item_tiles;  // window_tc_kernel: row tiles that the batch can have
+    int32_t item_tiles;  // window_tc_kernel: row tiles that the batch can have; the list of them
+    int32_t split_items;  // with each kv head ends in this many that are split
     float qscale;       // sm_scale * log2(e)
 };
 

@@ -34,6 +34,9 @@ struct Plan {
     bool tc;          // window_tc_kernel
     int row_tiles;    // row tiles of max_tokens tokens
     int key_tiles;    // most 16-token tiles that one row tile sees
+    int64_t n;        // tc: items (row tile, kv head), as many as the batch is likely to have
+    int64_t most;     // ... as it can have
+    int64_t split_items;  // ... the last ones, that split_tokens > 0 splits
     int ctas_per_sm;
 };
 
@@ -106,6 +109,16 @@ int make_plan(const pkv_cache_desc* c, const pkv_batch_desc* bt, int window, int
         else
             pl->fn = int8 ? window_tc_fn_d64_int8(&pl->smem, &pl->threads) : window_tc_fn_d64_bf16(&pl->smem, &pl->threads);
         pl->row_tiles = int((rows + 255) / 256);
+        // One CTA a SM walks through the items, so all but the last n % SMs of them
+        // keep every SM busy as they are; those are split. (Ragged batches: the rows of
+        // num_tokens, and half a row tile more a sequence.)
+        int sms = 0;
+        const int st = sm_count(&sms);
+        if (st != PKV_OK) return st;
+        const int64_t tiles = int64_t(pl->row_tiles) * bt->B;
+        pl->n = std::min(tiles, (bt->num_tokens * int64_t(g) + 128 * int64_t(bt->B) + 255) / 256) * c->num_kv_heads;
+        pl->most = std::min(tiles, bt->num_tokens * int64_t(g) / 256 + bt->B) * c->num_kv_heads;
+        pl->split_items = pl->n < sms ? pl->most : pl->n % sms;
         pl->key_tiles = most_key_tiles(c, bt, window, sinks, int(std::min<int64_t>(256 / g, bt->max_tokens)), c->block_size);
         return prepare_kernel(pl->fn, pl->smem, pl->threads, int8 ? kTcLaunchRegsInt8 : kTcLaunchRegsBf16,
                               &pl->ctas_per_sm);
@@ -121,7 +134,9 @@ int make_plan(const pkv_cache_desc* c, const pkv_batch_desc* bt, int window, int
 }
 
 int max_splits_of(const pkv_cache_desc* c, const pkv_batch_desc* bt, const Plan& pl, int split_tokens) {
-    if (split_tokens <= 0 || int64_t(bt->B) * c->num_kv_heads * pl.row_tiles > kCounters) return 1;
+    if (split_tokens <= 0) return 1;
+    const int64_t split = pl.tc ? pl.split_items : int64_t(bt->B) * c->num_kv_heads * pl.row_tiles;
+    if (split == 0 || split > kCounters) return 1;
     const int tiles = split_tokens / kTile;
     return std::min(kMaxSplits, (pl.key_tiles + tiles - 1) / tiles);
 }
@@ -133,8 +148,9 @@ struct Workspace {
 Workspace workspace_of(const pkv_cache_desc* c, const pkv_batch_desc* bt, const Plan& pl, int max_splits) {
     const auto up = [](size_t x) { return (x + 255) / 256 * 256; };
     Workspace w;
-    w.ml = up(size_t(bt->num_tokens) * c->num_q_heads * max_splits * 8);
-    w.o = size_t(bt->num_tokens) * c->num_q_heads * max_splits * c->head_dim * 4;
+    const size_t rows = pl.tc ? size_t(pl.split_items) * 256 : size_t(bt->num_tokens) * c->num_q_heads;
+    w.ml = up(rows * max_splits * 8);
+    w.o = rows * max_splits * c->head_dim * 4;
     w.total = max_splits > 1 ? size_t(kCounters) * 4 + w.ml + w.o : 0;
     return w;
 }
@@ -193,18 +209,13 @@ int pkv_window_split_tokens(const pkv_cache_desc* c, const pkv_batch_desc* batch
     int sms = 0;
     if ((st = make_plan(c, batch, window, sinks, &pl)) != PKV_OK || (st = sm_count(&sms)) != PKV_OK) return st;
     if (pl.tc) {
-        // One CTA a SM walks through the items. n of them in s parts each take
-        // ceil(n s / SMs) rounds of (key tiles / s + o) tiles' time, where o stands for
-        // an item's beginning and end: 2, or 8 with the partial rows written, read back
-        // and merged. The s that makes it least. (Ragged batches: the rows of
-        // num_tokens, half a row tile more a sequence.)
-        const int64_t g = c->num_q_heads / c->num_kv_heads;
-        const int64_t n = std::min<int64_t>(int64_t(pl.row_tiles) * batch->B,
-                                            (batch->num_tokens * g + 128 * int64_t(batch->B) + 255) / 256) * c->num_kv_heads;
-        const int64_t tiles = (pl.key_tiles + 7) / 8;
+        // The last r items in s parts each take ceil(r s / SMs) rounds of (key tiles / s
+        // + o) tiles' time, where o stands for an item's beginning and end: 2, or 8 with
+        // the partial rows written, read back and merged. The s that makes it least.
+        const int64_t r = pl.n < sms ? pl.n : pl.split_items, tiles = (pl.key_tiles + 7) / 8;
         int64_t best = 0, split = 1;
         for (int64_t s = 1; s <= std::min<int64_t>(tiles / 2, kMaxSplits); ++s) {
-            const int64_t cost = (n * s + sms - 1) / sms * ((tiles + s - 1) / s + (s > 1 ? 8 : 2));
+            const int64_t cost = (r * s + sms - 1) / sms * ((tiles + s - 1) / s + (s > 1 ? 8 : 2));
             if (s == 1 || cost < best) {
                 best = cost;
                 split = s;
@@ -248,7 +259,8 @@ int pkv_window_attention(const pkv_cache_desc* c, const pkv_batch_desc* batch, c
     const int splits = max_splits_of(c, batch, pl, split_tokens);
     // window_tc_kernel's planner and warps without rows wait for as long as an item
     // takes, a second at most; 2^25 tokens take about half of that
-    if (pl.tc && (pl.key_tiles + splits - 1) / splits > (1 << 25) / kTile) return PKV_ERR_UNSUPPORTED;
+    const int parts = pl.tc && pl.split_items < pl.most ? 1 : splits;
+    if (pl.tc && (pl.key_tiles + parts - 1) / parts > (1 << 25) / kTile) return PKV_ERR_UNSUPPORTED;
     const Workspace w = workspace_of(c, batch, pl, splits);
     if (w.total > 0 && (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < w.total)) return PKV_ERR_INVALID;
 
@@ -286,13 +298,15 @@ int pkv_window_attention(const pkv_cache_desc* c, const pkv_batch_desc* batch, c
     // not a number, nor is an infinite scale times a score of 0
     p.qscale = std::min(std::max(sm_scale * 1.4426950408889634f, 1e-37f), 3.4e38f);
     // window_tc_kernel: the row tiles of all sequences are one list
-    const int64_t g = c->num_q_heads / c->num_kv_heads;
-    p.item_tiles = 0;
-    if (pl.tc)
-        p.item_tiles = int(std::min<int64_t>(int64_t(pl.row_tiles) * batch->B, batch->num_tokens * g / 256 + batch->B));
-    const int64_t gx = int64_t(pl.tc ? p.item_tiles : pl.row_tiles) * splits;
+    p.item_tiles = p.split_items = 0;
+    int64_t gx = int64_t(pl.row_tiles) * splits;
+    if (pl.tc) {
+        p.split_items = splits > 1 ? int(pl.split_items) : 0;
+        gx = pl.most + int64_t(p.split_items) * (splits - 1);
+        p.item_tiles = int(pl.most / c->num_kv_heads);
+    }
     if (gx > 0x7FFFFFFF) return PKV_ERR_INVALID;
-    const dim3 grid(unsigned(gx), unsigned(c->num_kv_heads), pl.tc ? 1u : unsigned(batch->B));
+    const dim3 grid(unsigned(gx), pl.tc ? 1u : unsigned(c->num_kv_heads), pl.tc ? 1u : unsigned(batch->B));
     return launch(pl.fn, grid, dim3(unsigned(pl.threads)), pl.smem, static_cast<cudaStream_t>(stream), p);
 }
 

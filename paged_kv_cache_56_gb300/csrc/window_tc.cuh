@@ -86,8 +86,9 @@ struct TcBars {
 // A work item, as the planning warp describes it to the others.
 struct TcItem {
     int kind;          // 0: attention; 1: rows of a sequence with a bad length, zero; 2: the end
-    int b, kvh, rt, j;  // sequence, kv head, row tile, split
+    int b, kvh, j;     // sequence, kv head, split
     int ns;            // splits of this row tile
+    int at;            // its place among the row tiles that are split
     int row0, pos0;    // the sequence's first row, and its position
     int r_first, r_end;
     int p_first, p_last;
@@ -357,9 +358,6 @@ window_tc_kernel(const __grid_constant__ WindowParams p) {
             if (!ok) break;
             // ---- write the row
             const float l = l2.x + l2.y;
-            const int64_t tok = im.row0 + (have ? (row >> lgG) : 0);
-            const int head = im.kvh * G + (have ? (row & (G - 1)) : 0);
-            const size_t at = (size_t(tok) * p.c.Hq + head) * S + im.j;
             if (used) {
                 tc_fence_after();
                 const float f = im.ns > 1 ? 1.f : l > 0.f ? 1.f / l : 0.f;
@@ -380,9 +378,10 @@ window_tc_kernel(const __grid_constant__ WindowParams p) {
                     const int rr = first + lane / 8 + 4 * e;
                     const int64_t t = im.row0 + (rr >> lgG);
                     const int h = im.kvh * G + (rr & (G - 1));
-                    to[e] = partial ? ((t * p.c.Hq + h) * S + im.j) * D + ch * 4 : t * p.out_stride + h * D + ch * 8;
+                    to[e] = partial ? (int64_t(im.at * 256 + rr - im.r_first) * S + im.j) * D + ch * 4
+                                    : t * p.out_stride + h * D + ch * 8;
                 }
-                const int64_t ahead = partial ? int64_t(8 >> lgG) * p.c.Hq * S * D : (8 >> lgG) * p.out_stride;
+                const int64_t ahead = partial ? int64_t(8 * S) * D : (8 >> lgG) * p.out_stride;
                 for (int c = 0; c < steps; ++c) {
                     __syncwarp();
                     if (partial) {
@@ -419,15 +418,15 @@ window_tc_kernel(const __grid_constant__ WindowParams p) {
                     }
                 }
                 if (im.ns > 1 && have) {
-                    p.ws_ml[at * 2] = m_ref == -INFINITY ? -1e30f : m_ref;
-                    p.ws_ml[at * 2 + 1] = l;
+                    reinterpret_cast<float2*>(p.ws_ml)[size_t(im.at * 256 + tid) * S + im.j] =
+                        make_float2(m_ref == -INFINITY ? -1e30f : m_ref, l);
                 }
                 tc_fence_before();  // O_i has been read before the next item's P_i is announced
             }
             if (im.ns == 1) continue;
 
             // ---- the last split of the row tile to arrive merges all of them, a warp a row
-            int32_t* cnt = p.ws_count + (size_t(im.b) * p.c.Hkv + im.kvh) * p.row_tiles + im.rt;
+            int32_t* cnt = p.ws_count + im.at;
             if (!(ok = meet(merges++))) break;
             if (tid == 0) s_last = atom_add_acq_rel_gpu(cnt, 1) == im.ns - 1;
             if (!(ok = meet(merges++))) break;
@@ -436,11 +435,9 @@ window_tc_kernel(const __grid_constant__ WindowParams p) {
             // (16 bytes a lane) are in flight at a time.
             const int first = im.r_first + warp * 32, rows = min(32, im.r_end - first), parts = im.ns;
             const int head0 = im.kvh * G, row0 = im.row0;
-            const auto place = [&](int r) {  // of row first + r: its number among all rows and heads
-                return size_t(row0 + ((first + r) >> lgG)) * p.c.Hq + head0 + ((first + r) & (G - 1));
-            };
+            const size_t place0 = size_t(im.at * 256 + warp * 32);  // of row `first` in the workspace
             if (rows <= 0) continue;
-            const float2* ml = reinterpret_cast<const float2*>(p.ws_ml) + place(min(lane, rows - 1)) * S;
+            const float2* ml = reinterpret_cast<const float2*>(p.ws_ml) + (place0 + min(lane, rows - 1)) * S;
             float mm = -1e30f, L = 0.f;
             for (int x = 0; x < parts; ++x) {
                 const float2 v = __ldcg(ml + x);
@@ -461,7 +458,7 @@ window_tc_kernel(const __grid_constant__ WindowParams p) {
                     float v[8][E];
 #pragma unroll
                     for (int r = 0; r < 8; ++r) {
-                        const float* o = p.ws_o + (place(min(g + r, rows - 1)) * S + x) * D + lane * E;
+                        const float* o = p.ws_o + ((place0 + min(g + r, rows - 1)) * S + x) * D + lane * E;
                         if constexpr (E == 4) {
                             const float4 f = __ldcg(reinterpret_cast<const float4*>(o));
                             v[r][0] = f.x; v[r][1] = f.y; v[r][2] = f.z; v[r][3] = f.w;
@@ -803,14 +800,18 @@ window_tc_kernel(const __grid_constant__ WindowParams p) {
         // ================= items and queries =================
         const bool leader = elect_one();
         if (leader) prefetch_tensormap(&p.tm_q);
-        int cx = blockIdx.x, kvh = blockIdx.y;
-        if (cx == 0 && kvh == 0)
+        int cx = blockIdx.x;
+        const int whole = p.item_tiles * p.c.Hkv - p.split_items;
+        if (cx == 0)
             for (int b = lane; b < p.bt.B; b += 32) (void)seq_range(p.bt, b, bs, p.c.err, true);
         int published = 0, loaded = 0;
         for (int round = 0;; ++round) {
-            // row tiles of all sequences in a list, from its end: later rows see more keys
-            const int j = cx % S;
-            const WorkItem wi = locate(p.item_tiles - 1 - cx / S, p.bt.B, [&](int s) {
+            // (row tile, kv head) of all sequences in a list, the row tiles from the last
+            // one on: later rows see more keys. The list's last split_items are split.
+            const bool split = cx >= whole;
+            const int at = split ? (cx - whole) / S : 0, j = split ? (cx - whole) % S : 0;
+            const int item = split ? whole + at : cx, kvh = item % p.c.Hkv;
+            const WorkItem wi = locate(p.item_tiles - 1 - item / p.c.Hkv, p.bt.B, [&](int s) {
                 const SeqRange r = seq_range(p.bt, s, bs, nullptr, false);
                 return int((int64_t(r.n) * G + 2 * kTcRows - 1) / (2 * kTcRows));
             });
@@ -820,7 +821,7 @@ window_tc_kernel(const __grid_constant__ WindowParams p) {
                 x.kind = sq.bad ? 1 : 0;
                 x.b = wi.b;
                 x.kvh = kvh;
-                x.rt = wi.i;
+                x.at = at;
                 x.j = j;
                 x.row0 = sq.row0;
                 x.pos0 = sq.ctx - sq.n;
@@ -831,7 +832,7 @@ window_tc_kernel(const __grid_constant__ WindowParams p) {
                 x.kt = key_tiles(max(0, x.p_first), max(0, x.p_last), p.window, p.sinks, bs);
                 const int all = (x.kt.n + U - 1) / U;
                 int per = all;
-                if (p.split_tiles > 0) per = max(p.split_tiles * kTile / kTcKeys, (all + S - 1) / S);
+                if (split) per = max(p.split_tiles * kTile / kTcKeys, (all + S - 1) / S);
                 x.ns = (all + per - 1) / per;
                 x.k0 = j * per;
                 x.n = min(all, x.k0 + per) - x.k0;
@@ -868,7 +869,7 @@ window_tc_kernel(const __grid_constant__ WindowParams p) {
             }
             __syncwarp();
             if (!(ok = wait(&bars.next, round))) break;
-            const bool more = next_cta_read(smem_addr(&s_next), cx, kvh);
+            const bool more = next_cta_read(smem_addr(&s_next), cx);
             __syncwarp();
             if (!more) break;
         }
