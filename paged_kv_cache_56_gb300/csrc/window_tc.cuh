@@ -431,16 +431,19 @@ window_tc_kernel(const __grid_constant__ WindowParams p) {
             if (tid == 0) s_last = atom_add_acq_rel_gpu(cnt, 1) == im.ns - 1;
             if (!(ok = meet(merges++))) break;
             if (!s_last) continue;
-            // A lane has the weights of one of the warp's 32 rows; eight rows' partials
-            // (16 bytes a lane) are in flight at a time.
+            // Latency counts here: eight rows' partials (16 bytes a lane) of two splits are in
+            // flight at a time, and a lane has those rows' weights of one split in 32.
             const int first = im.r_first + warp * 32, rows = min(32, im.r_end - first), parts = im.ns;
             const int head0 = im.kvh * G, row0 = im.row0;
             const size_t place0 = size_t(im.at * 256 + warp * 32);  // of row `first` in the workspace
             if (rows <= 0) continue;
-            const float2* ml = reinterpret_cast<const float2*>(p.ws_ml) + (place0 + min(lane, rows - 1)) * S;
-            float mm = -1e30f, L = 0.f;
+            const auto ml = [&](int r, int x) {
+                return __ldcg(reinterpret_cast<const float2*>(p.ws_ml) + (place0 + min(r, rows - 1)) * S + x);
+            };
+            float mm = -1e30f, L = 0.f;  // of row `lane`
+#pragma unroll 4
             for (int x = 0; x < parts; ++x) {
-                const float2 v = __ldcg(ml + x);
+                const float2 v = ml(lane, x);
                 const float up = fmaxf(mm, v.x);
                 L = L * fast_exp2(mm - up) + v.y * fast_exp2(v.x - up);
                 mm = up;
@@ -453,25 +456,36 @@ window_tc_kernel(const __grid_constant__ WindowParams p) {
                 for (int r = 0; r < 8; ++r)
 #pragma unroll
                     for (int e = 0; e < E; ++e) acc[r][e] = 0.f;
-                for (int x = 0; x < parts; ++x) {
-                    const float c = fast_exp2(__ldcg(ml + x).x - mm) * inv;
-                    float v[8][E];
+                for (int x0 = 0; x0 < parts; x0 += 32) {
+                    float wr[8];
 #pragma unroll
                     for (int r = 0; r < 8; ++r) {
-                        const float* o = p.ws_o + ((place0 + min(g + r, rows - 1)) * S + x) * D + lane * E;
-                        if constexpr (E == 4) {
-                            const float4 f = __ldcg(reinterpret_cast<const float4*>(o));
-                            v[r][0] = f.x; v[r][1] = f.y; v[r][2] = f.z; v[r][3] = f.w;
-                        } else {
-                            const float2 f = __ldcg(reinterpret_cast<const float2*>(o));
-                            v[r][0] = f.x; v[r][1] = f.y;
-                        }
+                        const float m = __shfl_sync(kFull, mm, g + r), f = __shfl_sync(kFull, inv, g + r);
+                        wr[r] = x0 + lane < parts ? fast_exp2(ml(g + r, x0 + lane).x - m) * f : 0.f;
                     }
+                    for (int x = 0; x < min(32, parts - x0); x += 2) {
+                        float v[2][8][E];
 #pragma unroll
-                    for (int r = 0; r < 8; ++r) {
-                        const float w = __shfl_sync(kFull, c, min(g + r, 31));
+                        for (int h = 0; h < 2; ++h)
 #pragma unroll
-                        for (int e = 0; e < E; ++e) acc[r][e] += w * v[r][e];
+                            for (int r = 0; r < 8; ++r) {
+                                const float* o = p.ws_o + ((place0 + min(g + r, rows - 1)) * S + min(x0 + x + h, parts - 1)) * D + lane * E;
+                                if constexpr (E == 4) {
+                                    const float4 f = __ldcg(reinterpret_cast<const float4*>(o));
+                                    v[h][r][0] = f.x; v[h][r][1] = f.y; v[h][r][2] = f.z; v[h][r][3] = f.w;
+                                } else {
+                                    const float2 f = __ldcg(reinterpret_cast<const float2*>(o));
+                                    v[h][r][0] = f.x; v[h][r][1] = f.y;
+                                }
+                            }
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+#pragma unroll
+                            for (int r = 0; r < 8; ++r) {
+                                const float w = __shfl_sync(kFull, wr[r], x + h);  // (behind the last: 0)
+#pragma unroll
+                                for (int e = 0; e < E; ++e) acc[r][e] += w * v[h][r][e];
+                            }
                     }
                 }
 #pragma unroll
