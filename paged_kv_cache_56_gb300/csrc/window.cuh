@@ -18,7 +18,10 @@ namespace pkv {
 struct WindowParams {
     CUtensorMap tm_k;  // the pools, as in DecodeParams
     CUtensorMap tm_v;
-    CUtensorMap tm_q;  // q as [tokens][Hkv][G][D], boxes of 128 rows x 64 elements (window_tc_kernel)
+    // window_tc_kernel:
+    CUtensorMap tm_q;    // q as [tokens][Hkv][G][D], boxes of 128 rows x 64 elements
+    CUtensorMap tm_out;  // out likewise, boxes of 32 rows
+    CUtensorMap tm_ws;   // ws_o, boxes of 32 rows x one split x 32 elements
     BatchView bt;
     CacheView c;
     const uint16_t* q;

@@ -163,22 +163,34 @@ int check_window(const pkv_cache_desc* c, const pkv_batch_desc* batch, int windo
     return PKV_OK;
 }
 
-// Tensor map of the queries for window_tc_kernel: [tokens][Hkv][G][d] with
-// boxes of 128 rows (128 / G tokens x the group) x 64 elements, 128-byte
-// swizzle.
-int q_tensor_map(const pkv_cache_desc* c, int tokens, const void* q, int64_t stride, CUtensorMap* out) {
+int encode_map(CUtensorMapDataType type, int rank, const void* base, const cuuint64_t* dims, const cuuint64_t* strides,
+               const cuuint32_t* box, CUtensorMap* out) {
     const PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
-    if (!enc) return PKV_ERR_CUDA;
+    const cuuint32_t elem[4] = {1, 1, 1, 1};
+    return enc && enc(out, type, rank, const_cast<void*>(base), dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? PKV_OK
+               : PKV_ERR_CUDA;
+}
+
+// Tensor map of q or out for window_tc_kernel: [tokens][Hkv][G][d] with boxes of
+// `rows` rows (rows / G tokens x the group) x 64 elements, 128-byte swizzle.
+int rows_tensor_map(const pkv_cache_desc* c, int tokens, const void* base, int64_t stride, int rows, CUtensorMap* out) {
     const cuuint64_t g = cuuint64_t(c->num_q_heads / c->num_kv_heads), d = cuuint64_t(c->head_dim);
     const cuuint64_t dims[4] = {d, g, cuuint64_t(c->num_kv_heads), cuuint64_t(tokens)};
     const cuuint64_t strides[3] = {d * 2, g * d * 2, cuuint64_t(stride) * 2};
-    const cuuint32_t box[4] = {64, cuuint32_t(g), 1, cuuint32_t(128 / g)};
-    const cuuint32_t elem[4] = {1, 1, 1, 1};
-    return enc(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(q), dims, strides, box, elem,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
-               ? PKV_OK
-               : PKV_ERR_CUDA;
+    const cuuint32_t box[4] = {64, cuuint32_t(g), 1, cuuint32_t(rows / g)};
+    return encode_map(CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims, strides, box, out);
+}
+
+// ... of the partial outputs: [rows][splits][d] fp32, boxes of 32 rows x 32 elements.
+int partials_tensor_map(const pkv_cache_desc* c, int64_t rows, int splits, const void* base, CUtensorMap* out) {
+    const cuuint64_t d = cuuint64_t(c->head_dim);
+    const cuuint64_t dims[3] = {d, cuuint64_t(splits), cuuint64_t(rows)};
+    const cuuint64_t strides[2] = {d * 4, cuuint64_t(splits) * d * 4};
+    const cuuint32_t box[3] = {32, 1, 32};
+    return encode_map(CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, base, dims, strides, box, out);
 }
 
 bool is_empty(const pkv_batch_desc* b) { return b->B == 0 || b->num_tokens == 0 || b->max_tokens == 0; }
@@ -272,7 +284,8 @@ int pkv_window_attention(const pkv_cache_desc* c, const pkv_batch_desc* batch, c
             if ((st = pool_tensor_map(c->k_pool, c->num_blocks, rows, row_bytes, &p.tm_k, c->block_size)) != PKV_OK) return st;
             if ((st = pool_tensor_map(c->v_pool, c->num_blocks, rows, row_bytes, &p.tm_v, c->block_size)) != PKV_OK) return st;
         }
-        if ((st = q_tensor_map(c, batch->num_tokens, q, q_stride, &p.tm_q)) != PKV_OK) return st;
+        if ((st = rows_tensor_map(c, batch->num_tokens, q, q_stride, 128, &p.tm_q)) != PKV_OK) return st;
+        if ((st = rows_tensor_map(c, batch->num_tokens, out, out_stride, 32, &p.tm_out)) != PKV_OK) return st;
     } else if (row_bytes >= 128) {
         const int32_t rows = c->num_kv_heads * c->block_size;
         if ((st = pool_tensor_map(c->k_pool, c->num_blocks, rows, row_bytes, &p.tm_k)) != PKV_OK) return st;
@@ -302,6 +315,7 @@ int pkv_window_attention(const pkv_cache_desc* c, const pkv_batch_desc* batch, c
     int64_t gx = int64_t(pl.row_tiles) * splits;
     if (pl.tc) {
         p.split_items = splits > 1 ? int(pl.split_items) : 0;
+        if (splits > 1 && (st = partials_tensor_map(c, pl.split_items * 256, splits, p.ws_o, &p.tm_ws)) != PKV_OK) return st;
         gx = pl.most + int64_t(p.split_items) * (splits - 1);
         p.item_tiles = int(pl.most / c->num_kv_heads);
     }
