@@ -27,9 +27,12 @@
 // may be corrected.
 //
 // The running maximum is a reference that follows the true one only when that
-// is more than 2^8 ahead, so O_i is rarely rescaled. Weights are kept in units
-// of 2^-40 (an exponent bias, free), so that neither they times V nor their
-// sums leave fp32 whatever V's size. Weights are rounded to bf16 for the multiply
+// is more than 2^12 ahead, so O_i is rarely rescaled; it begins as the first
+// tile's maximum (a reference of 1, without that tile's second pass, measured 5%
+// slower: more tiles go beyond it later, and a tile that does costs its warp two
+// passes). Weights are kept in units of 2^-40 (an exponent bias, free): 2^12 of
+// them times the largest V and 2^28 tokens stay in fp32, one times a V of 2^-60
+// leaves 26 bits. Weights are rounded to bf16 for the multiply
 // (half a step, 2^-8 of each weight, as the outputs are); their sum is fp32.
 #pragma once
 
@@ -41,7 +44,7 @@ namespace pkv {
 constexpr int kTcRows = 128;   // rows of a row tile
 constexpr int kTcKeys = 128;   // tokens of a key tile
 constexpr float kTcShift = 40.f;
-constexpr float kTcAhead = 8.f;
+constexpr float kTcAhead = 12.f;
 
 template <int D, bool INT8>
 struct TcTraits {
