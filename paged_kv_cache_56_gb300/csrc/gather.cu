@@ -7,7 +7,9 @@
 // the rows, 8 elements a thread and several loads in flight: consecutive
 // threads take consecutive elements of the output, so that writes are whole
 // lines and reads whole rows of a block. Bound by memory: every cached byte is
-// read once and every output byte written once.
+// read once and every output byte written once. Measured: 8 contexts of 30000 to
+// 32768 tokens, 8 kv heads, d = 128, INT8 -> bf16, 1.55 GB in 250 us, 6.2 TB/s (a
+// plain copy: 6.7); with the divisions in the copying loop 401 us.
 #include <algorithm>
 
 #include "batch.cuh"

@@ -66,7 +66,6 @@ constexpr int kTcLaunchRegsInt8 = 128;
 
 using WindowFn = void (*)(WindowParams);
 
-WindowFn window_rows_fn(int d, bool int8, int nt);
 size_t window_rows_smem(int d, bool int8);
 
 }  // namespace pkv

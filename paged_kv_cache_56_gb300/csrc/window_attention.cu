@@ -102,6 +102,12 @@ int make_plan(const pkv_cache_desc* c, const pkv_batch_desc* bt, int window, int
     const int64_t rows = int64_t(bt->max_tokens) * g;
     // The row kernel reads each key once for up to 16 rows and is bound by that;
     // more rows would have it read them again, and the tensor cores take over.
+    // Measured, 16 sequences of 7000 tokens, 8 kv heads, d = 128, bf16 / INT8, us:
+    //   rows              16          32          64
+    //   row kernel      82 /  68   135 / 135   273 / 258
+    //   tensor cores   105 / 133   128 / 156   128 / 156
+    // and 64 sequences of 1000 tokens: 62 / 57 against 64 / 82 with 16 rows, 80 / 85
+    // against 64 / 81 with 32.
     pl->tc = rows > 16;
     if (pl->tc) {
         if (c->head_dim == 128)
@@ -123,6 +129,7 @@ int make_plan(const pkv_cache_desc* c, const pkv_batch_desc* bt, int window, int
         return prepare_kernel(pl->fn, pl->smem, pl->threads, int8 ? kTcLaunchRegsInt8 : kTcLaunchRegsBf16,
                               &pl->ctas_per_sm);
     }
+    // up to 8 rows in tiles of 16 (the first of these): 81 / 66 us against 78 / 50 us
     const int nt = rows <= 8 ? 1 : 2;
     if (c->head_dim == 128) pl->fn = int8 ? window_rows_fn_d128_int8(nt) : window_rows_fn_d128_bf16(nt);
     else pl->fn = int8 ? window_rows_fn_d64_int8(nt) : window_rows_fn_d64_bf16(nt);
