@@ -39,15 +39,17 @@
 // prompts of 7400 to 8000 tokens, 16 query heads, bf16, 1.0 TF in 702 us, 1425
 // TF/s (cuBLAS: 1969); prompts of 5000 to 8192 tokens, window 1024, 32 query
 // heads, 211 GF in 196 us; chunks of 100 to 512 tokens, window 4096, INT8, 161 GF
-// in 192 us. A key tile takes about 3300 cycles of which the multiplies need
-// 2460; the rest is the softmax's chain behind them: the scores' way out of
-// tensor memory and the weights' way in share its ports with the multiplies
-// (without those loads: 644 us). With windows the tiles at both ends, half
-// masked but multiplied whole, and the items' ends come to that (ten tiles an
-// item). INT8: the conversion's stores and the multiplies' reads share the shared
-// memory's bandwidth, and 328 items on 152 SMs fill two rounds and a sixth,
-// whose items are split. Of other forms, two threads a row, exponentials in
-// polynomials, and scores in two buffers of 32 columns were slower or the same.
+// in 192 us. A key tile of an item takes about 3400 cycles, its multiplies 2048
+// of them. They read 192 KB of shared memory for it (Q and K at 128 bytes a cycle,
+// all that it has; V at 64) and the copies write another 64 KB, 2048 cycles too;
+// what is above that is the chain from scores to weights (without the loads from
+// tensor memory: 644 us). Scores in halves of 64 tokens, the first issued before
+// O_i += P_i V so that the softmax starts earlier, read Q twice as often: 823 us.
+// With windows the tiles at both ends, half masked but multiplied whole, and the
+// items' ends come to that (ten tiles an item). INT8: the conversion stores as
+// much to shared memory again, and 328 items on 152 SMs fill two rounds and a
+// sixth, whose items are split. Of other forms, two threads a row, exponentials
+// in polynomials, and scores in two buffers of 32 columns were slower or the same.
 #pragma once
 
 #include "ptx_tc.cuh"
