@@ -1,12 +1,12 @@
 // Rotary turn of a batch's new q and k rows fused with the write of k and v
 // into the paged cache (pkv_rope_append).
 //
-// One CTA per (chunk of CT tokens aligned to the cache's blocks, group of kv
+// One CTA per (chunk of 16 tokens, aligned to the cache's blocks, group of kv
 // heads); a thread has one token and one pair of 16-byte chunks of a row -- the
 // eight pairs of elements that turn by the same angles in every head -- so it
 // works out its eight angles once, keeps their sines and cosines in registers
-// and walks through the heads, four rows in flight. In INT8 mode CT is the
-// block size and a full block is quantized from registers: its bf16 rows
+// and walks through the heads, four rows in flight. In INT8 mode a block
+// of 64 tokens is a cluster of four CTAs, and a full block is quantized from registers: its bf16 rows
 // never go to memory, and the only shared memory is the block's maximum.
 //
 // Angles. The position is an integer p, so only the fraction of p * f / 2 pi
@@ -139,6 +139,17 @@ __device__ __forceinline__ void sincos_turn(uint32_t a, float& sn, float& cn) {
     cn = ((quarter + 1u) & 2u) ? -v : v;
 }
 
+// Two floats to the same place of another CTA of the cluster's shared memory, and
+// the meeting after which what was stored before it is there.
+__device__ __forceinline__ void st_cluster_f2(uint32_t addr, uint32_t cta, float x, float y) {
+    asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\tst.shared::cluster.v2.f32 [a], {%2, %3};\n\t}" ::"r"(addr),
+                 "r"(cta), "f"(x), "f"(y)
+                 : "memory");
+}
+__device__ __forceinline__ void cluster_meet() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 // Largest |x| of eight bf16 values, as bf16 pairs (not-a-numbers do not count).
 __device__ __forceinline__ __nv_bfloat162 absmax8(const uint4& w, __nv_bfloat162 m) {
     const uint32_t x[4] = {w.x, w.y, w.z, w.w};
@@ -178,28 +189,31 @@ __device__ __forceinline__ uint2 codes8(const uint4& w, float scale, float inv) 
     return make_uint2(out[0], out[1]);
 }
 
-template <int D, bool INT8, int CT>
-__global__ void __launch_bounds__(CT * D / 16, CT == 64 ? 2048 / (CT * D / 16) / 2 : (INT8 ? 768 : 896) / (CT * D / 16))
-rope_append_kernel(const __grid_constant__ RopeParams p) {
+constexpr int kRopeTokens = 16;  // of a CTA
+
+// PARTS: CTAs a chunk of kRopeTokens * PARTS tokens, a cluster.
+template <int D, bool INT8, int PARTS>
+__device__ __forceinline__ void rope_append(const RopeParams& p) {
+    constexpr int CT = kRopeTokens * PARTS;
     constexpr int PR = D / 16;               // chunk pairs a row
-    constexpr int THREADS = CT * PR;
-    constexpr int HB = 1;                    // kv heads at a time: their K and V rows are in flight together
+    constexpr int THREADS = kRopeTokens * PR, WARPS = THREADS / 32;
     constexpr int NB = 2;                    // query rows in flight
     __shared__ unsigned long long s_turns[D / 2];
-    __shared__ float s_max[2 * HB][THREADS / 32];
+    __shared__ __align__(16) float s_max[2][PARTS * WARPS][2];  // of every warp of the chunk: K's and V's, of two heads in turn
     pdl_wait();
     pdl_launch_dependents();
 
     const int tid = threadIdx.x, half = p.half;
+    const int bx = int(blockIdx.x) / PARTS, part = int(blockIdx.x) % PARTS;
     const int G = p.c.Hq / p.c.Hkv;
     if (tid < half) s_turns[tid] = turns_of(__ldg(p.inv_freq + tid));
     // one chunk a sequence at most: item x is sequence x; otherwise the x-th of
     // the chunks of all sequences, and one more CTA that checks the lengths
-    const int item = int(blockIdx.x) / p.groups, group = int(blockIdx.x) % p.groups;
+    const int item = bx / p.groups, group = bx % p.groups;
     WorkItem it{item, 0};
     if (p.ragged) {
-        if (blockIdx.x == gridDim.x - 1) {
-            check_lengths(p.bt, p.c.bs, p.c.err);
+        if (bx == int(gridDim.x) / PARTS - 1) {
+            if (part == 0) check_lengths(p.bt, p.c.bs, p.c.err);
             return;
         }
         it = locate(item, p.bt.B, [&](int s) {
@@ -209,7 +223,7 @@ rope_append_kernel(const __grid_constant__ RopeParams p) {
         if (it.b < 0) return;
     }
     const int b = it.b;
-    const SeqRange sq = seq_range(p.bt, b, p.c.bs, p.c.err, !p.ragged && group == 0 && tid == 0);
+    const SeqRange sq = seq_range(p.bt, b, p.c.bs, p.c.err, !p.ragged && group == 0 && part == 0 && tid == 0);
     if (sq.n == 0 || sq.bad) return;
     const int start = sq.ctx - sq.n;                       // first new token
     const int chunk0 = start / CT, last = (sq.ctx - 1) / CT;
@@ -228,7 +242,16 @@ rope_append_kernel(const __grid_constant__ RopeParams p) {
     const int jobs = (from_tail && last_partial && chunk == chunk0 && last > chunk0) ? 2 : 1;
     const bool leave_kv = from_tail && last_partial && chunk == last && last > chunk0;
     const int kvh0 = group * p.heads, kvh1 = min(p.c.Hkv, kvh0 + p.heads);
-    const int tl = tid / PR, pr = tid % PR;                // this thread's token of the chunk, chunk pair of a row
+    const int tl = part * kRopeTokens + tid / PR, pr = tid % PR;  // this thread's token of the chunk, chunk pair of a row
+    if constexpr (PARTS > 1) {
+        // tokens that are neither new nor in a block that fills; the cluster's other
+        // CTAs meet this one's only over a block that does
+        const auto idle = [&](int base) {
+            const int t0 = base + part * kRopeTokens;
+            return base + CT > sq.ctx && (t0 + kRopeTokens <= start || t0 >= sq.ctx);
+        };
+        if (idle(chunk * CT) && (jobs == 1 || idle(last * CT))) return;
+    }
     int lo, hi;
     pair_offsets(pr, half, inter, lo, hi);
     const bool turns = pr < half / 8;
@@ -238,6 +261,7 @@ rope_append_kernel(const __grid_constant__ RopeParams p) {
         else turn_pairs<false>(w, an);
     };
 
+    int turn_no = 0;  // heads whose maximum has been taken
     for (int job = 0; job < jobs; ++job) {
         const int base = (job == 0 ? chunk : last) * CT, tok = base + tl;
         const bool fresh = tok >= start && tok < sq.ctx;   // this thread's token is a new one
@@ -247,21 +271,19 @@ rope_append_kernel(const __grid_constant__ RopeParams p) {
         int id = -1;
         if (do_kv && (!INT8 || full)) id = table[base / p.c.bs];
 
-        Pair16 w[2 * HB], x[NB];  // K, V of kvh, then of kvh + 1; query rows
-        const auto load_kv = [&](int kvh) {
+        Pair16 w[2], x[NB];  // K and V of a head; query rows
+        const auto load_kv = [&](int h) {
 #pragma unroll
-            for (int u = 0; u < 2 * HB; ++u) {
-                const int kv = u & 1, h = kvh + u / 2;
-                w[u].a = w[u].b = make_uint4(0u, 0u, 0u, 0u);
-                if (h >= kvh1) continue;
+            for (int kv = 0; kv < 2; ++kv) {
+                w[kv].a = w[kv].b = make_uint4(0u, 0u, 0u, 0u);
                 if (fresh) {
                     const uint16_t* r = (kv ? p.v + row * p.v_stride : p.k + row * p.k_stride) + h * D;
-                    w[u].a = ldg128(r + lo);
-                    w[u].b = ldg128(r + hi);
+                    w[kv].a = ldg128(r + lo);
+                    w[kv].b = ldg128(r + hi);
                 } else if (full && slot_ok) {  // an earlier token of the block
                     const uint16_t* r = (kv ? p.c.v_tail : p.c.k_tail) + ((size_t(slot) * p.c.Hkv + h) * CT + tl) * D;
-                    w[u].a = ldcg128(r + lo);
-                    w[u].b = ldcg128(r + hi);
+                    w[kv].a = ldcg128(r + lo);
+                    w[kv].b = ldcg128(r + hi);
                 }
             }
         };
@@ -299,66 +321,68 @@ rope_append_kernel(const __grid_constant__ RopeParams p) {
         if (INT8 && do_kv && !slot_ok && (!full || start > base) && tid == 0) report(p.c.err, kErrSlot);
         const bool write = do_kv && (INT8 && !full ? slot_ok : id >= 0 && (slot_ok || start <= base));
 
-        // Neighbouring CTAs take the two parts in opposite order: one's arithmetic
-        // on K and V beside the other's stream of queries
-        for (int part = 0; part < 2; ++part) {
-        // ---- K and V rows of HB heads at a time
-        if (part == int(blockIdx.x & 1) && write) {
-            for (int kvh = kvh0; kvh < kvh1; kvh += HB) {
+        // Neighbouring CTAs (clusters) take the two halves in opposite order: one's
+        // arithmetic on K and V beside the other's stream of queries
+        for (int turn_of = 0; turn_of < 2; ++turn_of) {
+        // ---- K and V rows, a head at a time
+        if (turn_of == (bx & 1) && write) {
+            if (PARTS > 1 && full) cluster_meet();  // every CTA has begun
+            for (int kvh = kvh0; kvh < kvh1; ++kvh) {
                 if (kvh > kvh0) load_kv(kvh);
-                if (fresh) {
+                if (fresh) turn(w[0], an);
+                if (full) {  // (`full` and `write` are the cluster's)
+                    float mx[2];
 #pragma unroll
-                    for (int u = 0; u < 2 * HB; u += 2) turn(w[u], an);
-                }
-                if (full) {
-                    float mx[2 * HB];
-#pragma unroll
-                    for (int u = 0; u < 2 * HB; ++u) {
-                        const __nv_bfloat162 top = absmax8(w[u].b, absmax8(w[u].a, __floats2bfloat162_rn(0.f, 0.f)));
-                        mx[u] = fmaxf(__low2float(top), __high2float(top));
+                    for (int kv = 0; kv < 2; ++kv) {
+                        const __nv_bfloat162 top = absmax8(w[kv].b, absmax8(w[kv].a, __floats2bfloat162_rn(0.f, 0.f)));
+                        mx[kv] = fmaxf(__low2float(top), __high2float(top));
                     }
 #pragma unroll
                     for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
-                        for (int u = 0; u < 2 * HB; ++u) mx[u] = fmaxf(mx[u], __shfl_xor_sync(kFull, mx[u], o));
-                    if (kvh > kvh0) __syncthreads();  // the heads before are done with s_max
-                    if ((tid & 31) == 0) {
-#pragma unroll
-                        for (int u = 0; u < 2 * HB; ++u) s_max[u][tid >> 5] = mx[u];
+                        for (int kv = 0; kv < 2; ++kv) mx[kv] = fmaxf(mx[kv], __shfl_xor_sync(kFull, mx[kv], o));
+                    // two buffers in turn: a CTA is at most one meeting ahead of another
+                    float(*top)[2] = s_max[turn_no++ & 1];
+                    if constexpr (PARTS > 1) {
+                        if ((tid & 31) < PARTS)  // one lane for each CTA of the cluster
+                            st_cluster_f2(smem_addr(top[part * WARPS + (tid >> 5)]), uint32_t(tid & 31), mx[0], mx[1]);
+                        cluster_meet();
+                    } else {
+                        if ((tid & 31) == 0) *reinterpret_cast<float2*>(top[tid >> 5]) = make_float2(mx[0], mx[1]);
+                        __syncthreads();
                     }
-                    __syncthreads();  // `full` and `write` are the CTA's
+                    float m[2] = {0.f, 0.f};
 #pragma unroll
-                    for (int u = 0; u < 2 * HB; ++u) {
-                        const int kv = u & 1, h = kvh + u / 2;
-                        if (h >= kvh1) continue;
-                        float m = 0.f;
+                    for (int k = 0; k < PARTS * WARPS; ++k) {
+                        const float2 v = *reinterpret_cast<const float2*>(top[k]);
+                        m[0] = fmaxf(m[0], v.x);
+                        m[1] = fmaxf(m[1], v.y);
+                    }
 #pragma unroll
-                        for (int k = 0; k < THREADS / 32; ++k) m = fmaxf(m, s_max[u][k]);
-                        const float scale = m < 1e-6f ? 1.0f : __fdiv_rn(m, 127.0f), inv = __fdiv_rn(1.0f, scale);
+                    for (int kv = 0; kv < 2; ++kv) {
+                        const float scale = m[kv] < 1e-6f ? 1.0f : __fdiv_rn(m[kv], 127.0f), inv = __fdiv_rn(1.0f, scale);
                         int8_t* dst = static_cast<int8_t*>(kv ? p.c.v_pool : p.c.k_pool) +
-                                      ((size_t(id) * p.c.Hkv + h) * CT + tl) * D;
-                        *reinterpret_cast<uint2*>(dst + lo) = codes8(w[u].a, scale, inv);
-                        *reinterpret_cast<uint2*>(dst + hi) = codes8(w[u].b, scale, inv);
-                        if (tid == 0) p.c.scales[(size_t(id) * p.c.Hkv + h) * 2 + kv] = scale;
+                                      ((size_t(id) * p.c.Hkv + kvh) * CT + tl) * D;
+                        *reinterpret_cast<uint2*>(dst + lo) = codes8(w[kv].a, scale, inv);
+                        *reinterpret_cast<uint2*>(dst + hi) = codes8(w[kv].b, scale, inv);
+                        if (tid == 0 && part == 0) p.c.scales[(size_t(id) * p.c.Hkv + kvh) * 2 + kv] = scale;
                     }
                 } else if (fresh) {
                     // rows of the pool block, or of the tail
 #pragma unroll
-                    for (int u = 0; u < 2 * HB; ++u) {
-                        const int kv = u & 1, h = kvh + u / 2;
-                        if (h >= kvh1) continue;
-                        uint16_t* dst = INT8 ? (kv ? p.c.v_tail : p.c.k_tail) + ((size_t(slot) * p.c.Hkv + h) * CT + tl) * D
+                    for (int kv = 0; kv < 2; ++kv) {
+                        uint16_t* dst = INT8 ? (kv ? p.c.v_tail : p.c.k_tail) + ((size_t(slot) * p.c.Hkv + kvh) * CT + tl) * D
                                              : static_cast<uint16_t*>(kv ? p.c.v_pool : p.c.k_pool) +
-                                                   ((size_t(id) * p.c.Hkv + h) * p.c.bs + tok % p.c.bs) * D;
-                        *reinterpret_cast<uint4*>(dst + lo) = w[u].a;
-                        *reinterpret_cast<uint4*>(dst + hi) = w[u].b;
+                                                   ((size_t(id) * p.c.Hkv + kvh) * p.c.bs + tok % p.c.bs) * D;
+                        *reinterpret_cast<uint4*>(dst + lo) = w[kv].a;
+                        *reinterpret_cast<uint4*>(dst + hi) = w[kv].b;
                     }
                 }
             }
         }
 
         // ---- the groups' queries, NB rows in flight
-        if (part != int(blockIdx.x & 1) && do_q && fresh) {
+        if (turn_of != (bx & 1) && do_q && fresh) {
             for (int h = kvh0 * G; h < kvh1 * G; h += NB) {
                 if (h > kvh0 * G) load_q(h);
 #pragma unroll
@@ -372,6 +396,21 @@ rope_append_kernel(const __grid_constant__ RopeParams p) {
         }
         }
     }
+}
+
+template <int D, bool INT8>
+__global__ void __launch_bounds__(D, (INT8 ? 768 : 896) / D) rope_append_kernel(const __grid_constant__ RopeParams p) {
+    rope_append<D, INT8, 1>(p);
+}
+
+// INT8 blocks of 64 tokens: a cluster of four CTAs, which exchange their rows'
+// maxima. (One CTA of 4 D threads took 18.6 us for 128 single tokens and 67.5 us
+// for 11200 tokens in chunks of 700: its threads sit idle in a step, and two of
+// them fill an SM.)
+template <int D>
+__global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(D, 768 / D)
+rope_append_cluster_kernel(const __grid_constant__ RopeParams p) {
+    rope_append<D, true, 4>(p);
 }
 
 __global__ void empty_kernel() {}
@@ -421,31 +460,28 @@ extern "C" int pkv_rope_append(const pkv_cache_desc* c, const pkv_batch_desc* ba
     p.v_stride = v_stride;
     p.q_out_stride = q_out_stride;
     const bool int8 = c->dtype == PKV_DTYPE_INT8;
-    const int ct = int8 ? c->block_size : 16;
+    const int ct = int8 ? c->block_size : kRopeTokens, parts = ct / kRopeTokens;
     // the most aligned chunks that max_tokens tokens in a row can touch
     const unsigned chunks = unsigned((batch->max_tokens + ct - 2) / ct + 1);
     // Angles are worked out once a CTA, so it takes as many kv heads as leave
     // CTAs for a wave or two (7 of 128 threads fit on an SM).
     const int64_t real = std::min<int64_t>(int64_t(chunks) * batch->B, batch->num_tokens / ct + 2 * int64_t(batch->B));
     p.heads = 1;
-    while (p.heads * 2 <= c->num_kv_heads && real * c->num_kv_heads / (p.heads * 2) >= 152 * 7 * 2) p.heads *= 2;
+    while (p.heads * 2 <= c->num_kv_heads && real * parts * c->num_kv_heads / (p.heads * 2) >= 152 * 7 * 2) p.heads *= 2;
     // chunks of all sequences: no more than B times the longest's, nor than
     // the tokens fill, two begun ones a sequence
     p.ragged = chunks > 1;
     const int64_t gx = p.ragged ? real : batch->B;
     p.groups = (c->num_kv_heads + p.heads - 1) / p.heads;
-    if (gx * p.groups >= 0x7FFFFFFF) return PKV_ERR_INVALID;
-    const dim3 grid(unsigned(gx * p.groups + p.ragged));
-    const unsigned threads = unsigned(ct * d / 16);
+    if ((gx * p.groups + 1) * parts > 0x7FFFFFFF) return PKV_ERR_INVALID;
+    const dim3 grid(unsigned((gx * p.groups + p.ragged) * parts));
     void (*fn)(RopeParams) = nullptr;
     if (d == 128)
-        fn = !int8 ? rope_append_kernel<128, false, 16>
-                   : ct == 16 ? rope_append_kernel<128, true, 16> : rope_append_kernel<128, true, 64>;
+        fn = !int8 ? rope_append_kernel<128, false> : parts == 1 ? rope_append_kernel<128, true> : rope_append_cluster_kernel<128>;
     else
-        fn = !int8 ? rope_append_kernel<64, false, 16>
-                   : ct == 16 ? rope_append_kernel<64, true, 16> : rope_append_kernel<64, true, 64>;
+        fn = !int8 ? rope_append_kernel<64, false> : parts == 1 ? rope_append_kernel<64, true> : rope_append_cluster_kernel<64>;
     auto s = static_cast<cudaStream_t>(stream);
-    if ((st = launch(fn, grid, dim3(threads), 0, s, p)) != PKV_OK) return st;
+    if ((st = launch(fn, grid, dim3(unsigned(d)), 0, s, p)) != PKV_OK) return st;
     if (g_pdl.load(std::memory_order_relaxed) && batch->max_tokens > 1) {
         empty_kernel<<<1, 1, 0, s>>>();
         return cuda_status(cudaGetLastError());
