@@ -464,10 +464,15 @@ extern "C" int pkv_rope_append(const pkv_cache_desc* c, const pkv_batch_desc* ba
     // the most aligned chunks that max_tokens tokens in a row can touch
     const unsigned chunks = unsigned((batch->max_tokens + ct - 2) / ct + 1);
     // Angles are worked out once a CTA, so it takes as many kv heads as leave
-    // CTAs for a wave or two (7 of 128 threads fit on an SM).
+    // CTAs for a wave or two (7 of 128 threads fit on an SM). Of a chunk with few
+    // tokens most threads are idle and a CTA's time is its loads' latency, so that one
+    // wave is better: 128 single tokens of 32 kv heads, two waves -> one, bf16 13.3 us
+    // -> 7.9 us, INT8 16.5 -> 11.9; but clusters of four, of which three CTAs end at
+    // once, 19.4 -> 35.9.
+    const int64_t enough = batch->max_tokens <= kRopeTokens && parts == 1 ? 152 * 6 : 152 * 7 * 2;
     const int64_t real = std::min<int64_t>(int64_t(chunks) * batch->B, batch->num_tokens / ct + 2 * int64_t(batch->B));
     p.heads = 1;
-    while (p.heads * 2 <= c->num_kv_heads && real * parts * c->num_kv_heads / (p.heads * 2) >= 152 * 7 * 2) p.heads *= 2;
+    while (p.heads * 2 <= c->num_kv_heads && real * parts * c->num_kv_heads / (p.heads * 2) >= enough) p.heads *= 2;
     // chunks of all sequences: no more than B times the longest's, nor than
     // the tokens fill, two begun ones a sequence
     p.ragged = chunks > 1;

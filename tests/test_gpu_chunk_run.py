@@ -346,3 +346,37 @@ def test_too_long_a_split_is_refused():
         ref, mag = attention(s, 0, 0, 0.125)
         assert_attention(out, ref, mag)
     assert s.error_bits() == 0
+
+
+@pytest.mark.parametrize("pdl", [False, True])
+@pytest.mark.parametrize("heads", [(2, 2, 64), (8, 8, 128)])
+def test_blocks_of_64_quantize_as_before(pdl, heads):
+    """Blocks of 64 tokens, whose rows several CTAs hold: the bits of the block quantizer, with not-a-numbers and
+    infinities in each quarter, in one call and token by token."""
+    n, hkv, d = 320, heads[1], heads[2]
+    rows = torch.randn((n, hkv, d), generator=torch.Generator().manual_seed(2)).to(torch.bfloat16)
+    for i, x in ((3, float("nan")), (70, float("inf")), (100, 300.0), (175, -float("inf")), (255, -500.0)):
+        rows[i, i % hkv, i % d] = x
+    s = Setup(1, [n], [n], heads, 64, True, appended=False)
+    dev = rows.cuda()
+    back = dev.flip(0).contiguous()
+    pkv.pkv_set_programmatic_launch(pdl)
+    try:
+        pkv.pkv_rope_append(s.lc.desc, s.batch, None, None, dev, back)
+        got = [x.clone() for x in (s.lc.k_pool, s.lc.v_pool, s.lc.scales)]
+        for x in (s.lc.k_pool, s.lc.v_pool, s.lc.scales):
+            x.zero_()
+        one = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+        ctx = torch.arange(1, n + 1, dtype=torch.int32, device="cuda")
+        batches = [pkv.make_batch(one, s.d_table, ctx[i:i + 1], s.d_slots, num_tokens=1, max_tokens=1) for i in range(n)]
+        for i, b in enumerate(batches):
+            pkv.pkv_rope_append(s.lc.desc, b, None, None, dev[i:i + 1], back[i:i + 1])
+    finally:
+        pkv.pkv_set_programmatic_launch(False)
+    ids = torch.as_tensor(s.table[0, :n // 64].copy()).cuda().long()
+    for a, b in zip(got, (s.lc.k_pool, s.lc.v_pool, s.lc.scales)):
+        assert torch.equal(a[ids].view(torch.int8), b[ids].view(torch.int8))
+    pkv.pkv_quantize_blocks_from(s.lc.desc, dev, back, ids.int())
+    for a, b in zip(got, (s.lc.k_pool, s.lc.v_pool, s.lc.scales)):
+        assert torch.equal(a[ids].view(torch.int8), b[ids].view(torch.int8))
+    assert s.error_bits() == 0
