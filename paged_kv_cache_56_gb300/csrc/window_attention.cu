@@ -117,12 +117,13 @@ int make_plan(const pkv_cache_desc* c, const pkv_batch_desc* bt, int window, int
         pl->row_tiles = int((rows + 255) / 256);
         // One CTA a SM walks through the items, so all but the last n % SMs of them
         // keep every SM busy as they are; those are split. (Ragged batches: the rows of
-        // num_tokens, and half a row tile more a sequence.)
+        // num_tokens, and half a row tile more a sequence, or one a sequence.)
         int sms = 0;
         const int st = sm_count(&sms);
         if (st != PKV_OK) return st;
         const int64_t tiles = int64_t(pl->row_tiles) * bt->B;
-        pl->n = std::min(tiles, (bt->num_tokens * int64_t(g) + 128 * int64_t(bt->B) + 255) / 256) * c->num_kv_heads;
+        pl->n = std::min(tiles, std::max<int64_t>(bt->B, (bt->num_tokens * int64_t(g) + 128 * int64_t(bt->B) + 255) / 256)) *
+                c->num_kv_heads;
         pl->most = std::min(tiles, bt->num_tokens * int64_t(g) / 256 + bt->B) * c->num_kv_heads;
         pl->split_items = pl->n < sms ? pl->most : pl->n % sms;
         pl->key_tiles = most_key_tiles(c, bt, window, sinks, int(std::min<int64_t>(256 / g, bt->max_tokens)), c->block_size);
@@ -229,12 +230,16 @@ int pkv_window_split_tokens(const pkv_cache_desc* c, const pkv_batch_desc* batch
     if ((st = make_plan(c, batch, window, sinks, &pl)) != PKV_OK || (st = sm_count(&sms)) != PKV_OK) return st;
     if (pl.tc) {
         // The last r items in s parts each take ceil(r s / SMs) rounds of (key tiles / s
-        // + o) tiles' time, where o stands for an item's beginning and end: 2, or 8 with
-        // the partial rows written, read back and merged. The s that makes it least.
+        // + o) tiles' time, where o stands for an item's beginning and end: 2.5, or with
+        // the partial rows written, read back and merged 5.5 and as much again for 256
+        // rows as there are parts, measured over items of 8 to 250 tiles and 24 to 256
+        // rows. The s that makes it least. (In quarters of a tile.)
         const int64_t r = pl.n < sms ? pl.n : pl.split_items, tiles = (pl.key_tiles + 7) / 8;
+        const int64_t rows = std::min<int64_t>(256, int64_t(batch->max_tokens) * (c->num_q_heads / c->num_kv_heads));
         int64_t best = 0, split = 1;
         for (int64_t s = 1; s <= std::min<int64_t>(tiles / 2, kMaxSplits); ++s) {
-            const int64_t cost = (r * s + sms - 1) / sms * ((tiles + s - 1) / s + (s > 1 ? 8 : 2));
+            const int64_t o = s > 1 ? 22 + s * std::max<int64_t>(1, rows / 64) : 10;
+            const int64_t cost = (r * s + sms - 1) / sms * (4 * ((tiles + s - 1) / s) + o);
             if (s == 1 || cost < best) {
                 best = cost;
                 split = s;

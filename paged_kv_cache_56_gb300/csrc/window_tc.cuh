@@ -443,33 +443,34 @@ window_tc_kernel(const __grid_constant__ WindowParams p) {
             }
             if (im.ns == 1) continue;
 
-            // ---- the last split of the row tile to arrive merges all of them, a warp a row
+            // ---- the last split of the row tile to arrive merges all of them
             int32_t* cnt = p.ws_count + im.at;
             if (lane == 0) bulk_wait();  // this warp's partials are written
             if (!(ok = meet(merges++))) break;
             if (tid == 0) s_last = atom_add_acq_rel_gpu(cnt, 1) == im.ns - 1;
             if (!(ok = meet(merges++))) break;
             if (!s_last) continue;
-            // Latency counts here: eight rows' partials (16 bytes a lane) of two splits are in
-            // flight at a time, and a lane has those rows' weights of one split in 32.
-            const int first = im.r_first + warp * 32, rows = min(32, im.r_end - first), parts = im.ns;
+            // Latency counts here: a warp takes eight rows at a time, whose partials (16 bytes
+            // a lane) of two splits are in flight, and a lane has those rows' weights of one
+            // split in 32.
+            const int rows = im.r_end - im.r_first, parts = im.ns;
             const int head0 = im.kvh * G, row0 = im.row0;
-            const size_t place0 = size_t(im.at * 256 + warp * 32);  // of row `first` in the workspace
-            if (rows <= 0) continue;
+            const size_t place0 = size_t(im.at) * 256;  // of the item's first row in the workspace
             const auto ml = [&](int r, int x) {
                 return __ldcg(reinterpret_cast<const float2*>(p.ws_ml) + (place0 + min(r, rows - 1)) * S + x);
             };
-            float mm = -1e30f, L = 0.f;  // of row `lane`
+            constexpr int E = D / 32;  // elements a lane
+            // the warp's rows are warp * 8 .. + 7 of every 64; this lane has one's statistics
+            float mm = -1e30f, L = 0.f;
 #pragma unroll 4
             for (int x = 0; x < parts; ++x) {
-                const float2 v = ml(lane, x);
+                const float2 v = ml(lane / 8 * 64 + warp * 8 + lane % 8, x);
                 const float up = fmaxf(mm, v.x);
                 L = L * fast_exp2(mm - up) + v.y * fast_exp2(v.x - up);
                 mm = up;
             }
             const float inv = L > 0.f ? 1.f / L : 0.f;
-            constexpr int E = D / 32;  // elements a lane
-            for (int g = 0; g < rows; g += 8) {
+            for (int g = warp * 8; g < rows; g += 64) {
                 float acc[8][E];
 #pragma unroll
                 for (int r = 0; r < 8; ++r)
@@ -479,7 +480,7 @@ window_tc_kernel(const __grid_constant__ WindowParams p) {
                     float wr[8];
 #pragma unroll
                     for (int r = 0; r < 8; ++r) {
-                        const float m = __shfl_sync(kFull, mm, g + r), f = __shfl_sync(kFull, inv, g + r);
+                        const float m = __shfl_sync(kFull, mm, g / 64 * 8 + r), f = __shfl_sync(kFull, inv, g / 64 * 8 + r);
                         wr[r] = x0 + lane < parts ? fast_exp2(ml(g + r, x0 + lane).x - m) * f : 0.f;
                     }
                     for (int x = 0; x < min(32, parts - x0); x += 2) {
@@ -510,7 +511,7 @@ window_tc_kernel(const __grid_constant__ WindowParams p) {
 #pragma unroll
                 for (int r = 0; r < 8; ++r) {
                     if (g + r >= rows) break;
-                    const int rr = first + g + r;
+                    const int rr = im.r_first + g + r;
                     uint16_t* at = p.out + int64_t(row0 + (rr >> lgG)) * p.out_stride + (head0 + (rr & (G - 1))) * D + lane * E;
 #pragma unroll
                     for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t*>(at + e) = f2_to_bf16x2(acc[r][e], acc[r][e + 1]);
