@@ -23,12 +23,13 @@
 // 30718 tokens of 16 query heads, bf16, 503 MB in 80 us, 6.3 TB/s (a plain copy:
 // 6.7); 12535 tokens of 32 query heads, INT8, 282 MB in 53 us, 5.4 TB/s -- the
 // quantizer's arithmetic and its block maximum (a barrier a head) leave half of
-// the issue slots and a part of the loads idle; 128 single tokens 8.6 us, launch
-// and the chain ids -> rows -> angles.
+// the issue slots and a part of the loads idle; 128 single tokens 8.6 us (bf16 5.7),
+// launch and the chain lengths -> rows -> maximum -> codes.
 //
 // Layout: with a token a thread the angles are worked out once and stay in
 // registers (shared-memory tables: 131 us for the bf16 case), consecutive lanes
-// read whole 256-byte rows, and a block's rows meet in one CTA for its maximum.
+// read whole 256-byte rows, and a block's rows meet in one CTA or cluster for its
+// maximum.
 #include <algorithm>
 
 #include "batch.cuh"

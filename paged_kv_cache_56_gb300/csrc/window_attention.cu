@@ -104,10 +104,10 @@ int make_plan(const pkv_cache_desc* c, const pkv_batch_desc* bt, int window, int
     // more rows would have it read them again, and the tensor cores take over.
     // Measured, 16 sequences of 7000 tokens, 8 kv heads, d = 128, bf16 / INT8, us:
     //   rows              16          32          64
-    //   row kernel      82 /  68   135 / 135   273 / 258
-    //   tensor cores   105 / 133   128 / 156   128 / 156
-    // and 64 sequences of 1000 tokens: 62 / 57 against 64 / 82 with 16 rows, 80 / 85
-    // against 64 / 81 with 32.
+    //   row kernel      82 /  68   136 / 135   278 / 259
+    //   tensor cores    88 / 121    88 / 121    88 / 121
+    // and 64 sequences of 1000 tokens: 62 / 57 against 64 / 80 with 16 rows, 81 / 85
+    // against 64 / 80 with 32.
     pl->tc = rows > 16;
     if (pl->tc) {
         if (c->head_dim == 128)
