@@ -380,3 +380,32 @@ def test_blocks_of_64_quantize_as_before(pdl, heads):
     for a, b in zip(got, (s.lc.k_pool, s.lc.v_pool, s.lc.scales)):
         assert torch.equal(a[ids].view(torch.int8), b[ids].view(torch.int8))
     assert s.error_bits() == 0
+
+
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("bs", [16, 64])
+@pytest.mark.parametrize("heads", [(32, 32, 128), (12, 12, 64), (40, 20, 64)])
+@pytest.mark.parametrize("seqs", [3, 60])
+def test_many_heads(seqs, heads, bs, int8):
+    """More kv heads than one CTA's round of rows: written, attended and read back, few sequences and many."""
+    rng = np.random.default_rng(seqs)
+    ctx = rng.integers(1, 90, size=seqs).tolist()
+    new = [int(rng.integers(0, c + 1)) for c in ctx]
+    s = Setup(12, new, ctx, heads, bs, int8)
+    back = [torch.full((s.T + 1, s.hkv, s.d), 3.0, dtype=torch.float32, device="cuda") for _ in range(2)]
+    pkv.pkv_gather_kv(s.lc.desc, s.batch, *back)
+    for name, b in zip("kv", back):
+        want = np.concatenate([x[c - m:] for x, m, c in zip(s.values[name], new, ctx)])
+        assert torch.equal(b[:-1].cpu(), torch.as_tensor(want).float()) and (b[-1] == 3).all()
+    ref, mag = attention(s, 20, 3)
+    out = torch.zeros((s.T, s.hq, s.d), dtype=torch.bfloat16, device="cuda")
+    pkv.pkv_window_attention(s.lc.desc, s.batch, s.q.cuda(), out, 20, 3, s.d ** -0.5)
+    assert_attention(out, ref, mag)
+    whole = Setup(12, ctx, ctx, heads, bs, int8, appended=False)
+    pkv.pkv_rope_append(whole.lc.desc, whole.batch, None, None, whole.new_rows("k").cuda(), whole.new_rows("v").cuda())
+    both = [torch.empty((whole.T, s.hkv, s.d), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    pkv.pkv_gather_kv(whole.lc.desc, whole.batch, *both)
+    for name, b in zip("kv", both):
+        want = torch.as_tensor(np.concatenate(s.values[name])).float().to(torch.bfloat16)
+        assert torch.equal(b.cpu(), want)
+    assert s.error_bits() == 0 and whole.error_bits() == 0
