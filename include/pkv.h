@@ -482,6 +482,10 @@ int pkv_set_programmatic_launch(int enable);
  * stays usable and later launches are unaffected. The outputs of the
  * affected (sequence, kv head) are then meaningless. -1 (the default) turns
  * it off and selects the regular kernels, which carry no such check.
+ * pkv_window_attention with up to 8 rows a kv head (max_tokens x group) does
+ * the same, its first CTA being the first split of the first row tile; with 9 to
+ * 16 rows it returns PKV_ERR_UNSUPPORTED; with more, whatever the shape, its
+ * first CTA leaves out the copy of the queries of its work item of that index.
  * PKV_ERR_INVALID for tile < -1. Process-wide. */
 int pkv_debug_skip_copy(int32_t tile);
 

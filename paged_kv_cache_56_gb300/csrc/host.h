@@ -20,6 +20,7 @@ int check_desc(const pkv_cache_desc* c);
 inline int cuda_status(cudaError_t e) { return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA; }
 
 extern std::atomic<int> g_pdl;
+extern std::atomic<int> g_skip_copy;  // pkv_debug_skip_copy
 
 // Launches with the programmatic-stream-serialization attribute when enabled
 // (pkv_set_programmatic_launch), plainly otherwise.

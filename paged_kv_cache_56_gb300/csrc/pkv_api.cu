@@ -141,7 +141,7 @@ int check_desc(const pkv_cache_desc* c) {
 }
 
 std::atomic<int> g_pdl{0};
-static std::atomic<int> g_skip_copy{-1};
+std::atomic<int> g_skip_copy{-1};
 
 // Copies whole slabs src[i] -> dst[i] for up to three arrays at once (slab
 // index * slab bytes = offset; arrays may be NULL): a0 and a1 with slabs of

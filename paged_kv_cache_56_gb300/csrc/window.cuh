@@ -38,6 +38,7 @@ struct WindowParams {
     int32_t item_tiles;  // window_tc_kernel: row tiles that the batch can have; the list of them
     int32_t split_items;  // with each kv head ends in this many that are split
     float qscale;       // sm_scale * log2(e)
+    int32_t skip_copy;  // pkv_debug_skip_copy (-1: off)
 };
 
 // The 16-token tiles that rows of positions p_first .. p_last see, as a list.

@@ -9,10 +9,10 @@
 
 namespace pkv {
 
-WindowFn window_rows_fn_d64_bf16(int nt);
-WindowFn window_rows_fn_d64_int8(int nt);
-WindowFn window_rows_fn_d128_bf16(int nt);
-WindowFn window_rows_fn_d128_int8(int nt);
+WindowFn window_rows_fn_d64_bf16(int nt, bool hook);
+WindowFn window_rows_fn_d64_int8(int nt, bool hook);
+WindowFn window_rows_fn_d128_bf16(int nt, bool hook);
+WindowFn window_rows_fn_d128_int8(int nt, bool hook);
 WindowFn window_tc_fn_d64_bf16(size_t* smem, int* threads);
 WindowFn window_tc_fn_d128_bf16(size_t* smem, int* threads);
 WindowFn window_tc_fn_d64_int8(size_t* smem, int* threads);
@@ -96,7 +96,7 @@ int most_key_tiles(const pkv_cache_desc* c, const pkv_batch_desc* bt, int window
     return int(std::min(all, seen * (unit / kTile)));
 }
 
-int make_plan(const pkv_cache_desc* c, const pkv_batch_desc* bt, int window, int sinks, Plan* pl) {
+int make_plan(const pkv_cache_desc* c, const pkv_batch_desc* bt, int window, int sinks, Plan* pl, bool hook = false) {
     const bool int8 = c->dtype == PKV_DTYPE_INT8;
     const int g = c->num_q_heads / c->num_kv_heads;
     const int64_t rows = int64_t(bt->max_tokens) * g;
@@ -132,8 +132,9 @@ int make_plan(const pkv_cache_desc* c, const pkv_batch_desc* bt, int window, int
     }
     // up to 8 rows in tiles of 16 (the first of these): 81 / 66 us against 78 / 50 us
     const int nt = rows <= 8 ? 1 : 2;
-    if (c->head_dim == 128) pl->fn = int8 ? window_rows_fn_d128_int8(nt) : window_rows_fn_d128_bf16(nt);
-    else pl->fn = int8 ? window_rows_fn_d64_int8(nt) : window_rows_fn_d64_bf16(nt);
+    if (c->head_dim == 128) pl->fn = int8 ? window_rows_fn_d128_int8(nt, hook) : window_rows_fn_d128_bf16(nt, hook);
+    else pl->fn = int8 ? window_rows_fn_d64_int8(nt, hook) : window_rows_fn_d64_bf16(nt, hook);
+    if (!pl->fn) return PKV_ERR_UNSUPPORTED;
     pl->smem = window_rows_smem(c->head_dim, int8);
     pl->threads = kThreads;
     pl->row_tiles = int((rows + 8 * nt - 1) / (8 * nt));
@@ -279,7 +280,8 @@ int pkv_window_attention(const pkv_cache_desc* c, const pkv_batch_desc* batch, c
         ((q_stride | out_stride) & 7))
         return PKV_ERR_INVALID;
     Plan pl;
-    if ((st = make_plan(c, batch, window, sinks, &pl)) != PKV_OK) return st;
+    p.skip_copy = g_skip_copy.load(std::memory_order_relaxed);
+    if ((st = make_plan(c, batch, window, sinks, &pl, p.skip_copy >= 0)) != PKV_OK) return st;
     const int splits = max_splits_of(c, batch, pl, split_tokens);
     // window_tc_kernel's planner and warps without rows wait for as long as an item
     // takes, a second at most; 2^25 tokens take about half of that

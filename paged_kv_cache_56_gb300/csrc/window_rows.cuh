@@ -179,7 +179,8 @@ __device__ __forceinline__ void rows_tile(const Rows& K, const Rows& V, int tok,
     }
 }
 
-template <int D, bool INT8, int NT>
+// HOOK: the test build of pkv_debug_skip_copy, which leaves one tile's copies unissued.
+template <int D, bool INT8, int NT, bool HOOK>
 __global__ void __launch_bounds__(kThreads, NT == 1 ? kMinCtas : 3)
 window_rows_kernel(const __grid_constant__ WindowParams p) {
     using T = DecodeTraits<D, INT8>;
@@ -277,6 +278,7 @@ window_rows_kernel(const __grid_constant__ WindowParams p) {
     };
     const uint64_t pol = l2_policy_evict_first();
     auto issue = [&](int k, int seg, int s) {
+        if (HOOK && k - k0 == p.skip_copy && warp == 0 && blockIdx.x + blockIdx.y + blockIdx.z == 0) return;
         const int tok = kt.tile(k) * kTile;
         const int id = s_id[k - seg];
         const uint32_t bar = bar_of(s);
@@ -557,8 +559,12 @@ window_rows_kernel(const __grid_constant__ WindowParams p) {
 }
 
 template <int D, bool INT8>
-WindowFn window_rows_pick(int nt) {
-    return nt == 1 ? window_rows_kernel<D, INT8, 1> : window_rows_kernel<D, INT8, 2>;
+WindowFn window_rows_pick(int nt, bool hook) {
+    if constexpr (D == 64) {
+        if (hook) return nt == 1 ? window_rows_kernel<D, INT8, 1, true> : nullptr;
+    }
+    if (hook) return nullptr;
+    return nt == 1 ? window_rows_kernel<D, INT8, 1, false> : window_rows_kernel<D, INT8, 2, false>;
 }
 
 }  // namespace pkv

@@ -2,5 +2,5 @@
 #include "window_rows.cuh"
 
 namespace pkv {
-WindowFn window_rows_fn_d128_int8(int nt) { return window_rows_pick<128, true>(nt); }
+WindowFn window_rows_fn_d128_int8(int nt, bool hook) { return window_rows_pick<128, true>(nt, hook); }
 }  // namespace pkv

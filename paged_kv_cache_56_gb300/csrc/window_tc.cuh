@@ -154,6 +154,9 @@ window_tc_kernel(const __grid_constant__ WindowParams p) {
     __shared__ __align__(16) uint4 s_next;
     __shared__ uint32_t s_tmem;
     __shared__ int s_last;
+    // Splits that another CTA may wait for (see the end): items up to s_settled have
+    // arrived, those up to s_published were described to the other warps.
+    __shared__ int s_settled, s_published;
     // units of a key tile that are not there, by tile % 8; INT8, [1]: or whose V is zero
     __shared__ uint32_t s_bad[1 + INT8][8];
     __shared__ float2 s_sc[INT8 ? 8 : 1][8];   // units' K scale times p.qscale, log2 of the V scale
@@ -189,6 +192,7 @@ window_tc_kernel(const __grid_constant__ WindowParams p) {
             mbar_init(bar(&bars.item_empty[i]), 8 + T::kLoadWarps + 1 + INT8);
         }
         fence_mbar_init();
+        s_settled = s_published = 0;
     }
     if (warp == T::kMmaWarp) tmem_alloc(smem_addr(&s_tmem), 512);
     tc_fence_before();
@@ -204,6 +208,13 @@ window_tc_kernel(const __grid_constant__ WindowParams p) {
     pdl_wait();
     pdl_launch_dependents();
 
+    // A split of a row tile arrives (one thread): true for the last one, which leaves
+    // the counter ready for the next call.
+    const auto arrive = [&](int at, int ns) {
+        const bool last = atom_add_acq_rel_gpu(p.ws_count + at, 1) == ns - 1;
+        if (last) p.ws_count[at] = 0;
+        return last;
+    };
     bool ok = true;
     // The q-th item of this CTA (every warp but the planner's): false at the end.
     const auto take = [&](int q) {
@@ -444,10 +455,12 @@ window_tc_kernel(const __grid_constant__ WindowParams p) {
             if (im.ns == 1) continue;
 
             // ---- the last split of the row tile to arrive merges all of them
-            int32_t* cnt = p.ws_count + im.at;
             if (lane == 0) bulk_wait();  // this warp's partials are written
             if (!(ok = meet(merges++))) break;
-            if (tid == 0) s_last = atom_add_acq_rel_gpu(cnt, 1) == im.ns - 1;
+            if (tid == 0) {
+                s_last = arrive(im.at, im.ns);
+                s_settled = q + 1;
+            }
             if (!(ok = meet(merges++))) break;
             if (!s_last) continue;
             // Latency counts here: a warp takes eight rows at a time, whose partials (16 bytes
@@ -517,7 +530,6 @@ window_tc_kernel(const __grid_constant__ WindowParams p) {
                     for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t*>(at + e) = f2_to_bf16x2(acc[r][e], acc[r][e + 1]);
                 }
             }
-            if (tid == 0) *cnt = 0;  // ready for the next call
         }
         if (lane == 0) {
             bulk_wait();
@@ -580,7 +592,10 @@ window_tc_kernel(const __grid_constant__ WindowParams p) {
                     }
                     if (fix) {
                         // clear the rows of V that no row of the item sees
-                        if (!(ok = wait(&bars.raw_full[0], raw_phase))) break;
+                        if (!(ok = wait(&bars.raw_full[0], raw_phase))) {
+                            (void)wait(&bars.raw_full[0], raw_phase);  // (this copy is not among `tiles`)
+                            break;
+                        }
                         ++raw_phase;
                         for (int x = 0; x < U && tile * U + x < kt.n; ++x) {
                             const int t0 = kt.tile(tile * U + x) << lg;
@@ -800,7 +815,10 @@ window_tc_kernel(const __grid_constant__ WindowParams p) {
                 if (id >= 0) sc = __ldcg(reinterpret_cast<const float2*>(p.c.scales) + size_t(id) * p.c.Hkv + kvh);
 #pragma unroll 1
                 for (int v = 0; v < 2; ++v) {
-                    if (tiles + jj > 0 && !(ok = wait(&bars.raw_empty[v], tiles + jj - 1))) break;
+                    if (tiles + jj > 0 && !(ok = wait(&bars.raw_empty[v], tiles + jj - 1))) {
+                        if (v) (void)wait(&bars.raw_full[0], tiles + jj);  // (this tile's K is not among `tiles`)
+                        break;
+                    }
                     if (v == 0) {
                         // K: never 0: a hidden token's score is -infinity, and 0 times that is not
                         // a number. V scales below 2^-60 are taken for zero, by way of zero rows:
@@ -841,8 +859,9 @@ window_tc_kernel(const __grid_constant__ WindowParams p) {
         const int whole = p.item_tiles * p.c.Hkv - p.split_items;
         if (cx == 0)
             for (int b = lane; b < p.bt.B; b += 32) (void)seq_range(p.bt, b, bs, p.c.err, true);
-        int published = 0, loaded = 0;
-        for (int round = 0;; ++round) {
+        int published = 0, loaded = 0, round = 0;
+        // The grid's cx-th CTA's item; false: it has none.
+        const auto describe = [&](TcItem& x) {
             // (row tile, kv head) of all sequences in a list, the row tiles from the last
             // one on: later rows see more keys. The list's last split_items are split.
             const bool split = cx >= whole;
@@ -852,50 +871,57 @@ window_tc_kernel(const __grid_constant__ WindowParams p) {
                 const SeqRange r = seq_range(p.bt, s, bs, nullptr, false);
                 return int((int64_t(r.n) * G + 2 * kTcRows - 1) / (2 * kTcRows));
             });
-            if (wi.b >= 0) {
-                const SeqRange sq = seq_range(p.bt, wi.b, bs, nullptr, false);
-                TcItem x;
-                x.kind = sq.bad ? 1 : 0;
-                x.b = wi.b;
-                x.kvh = kvh;
-                x.at = at;
-                x.j = j;
-                x.row0 = sq.row0;
-                x.pos0 = sq.ctx - sq.n;
-                x.r_first = wi.i * 2 * kTcRows;
-                x.r_end = min(sq.n * G, x.r_first + 2 * kTcRows);
-                x.p_first = x.pos0 + (x.r_first >> lgG);
-                x.p_last = x.pos0 + ((x.r_end - 1) >> lgG);
-                x.kt = key_tiles(max(0, x.p_first), max(0, x.p_last), p.window, p.sinks, bs);
-                const int all = (x.kt.n + U - 1) / U;
-                int per = all;
-                if (split) per = max(p.split_tiles * kTile / kTcKeys, (all + S - 1) / S);
-                x.ns = (all + per - 1) / per;
-                x.k0 = j * per;
-                x.n = min(all, x.k0 + per) - x.k0;
-                x.nfull = INT8 ? sq.ctx / bs * bs : sq.ctx;
-                x.slot = INT8 ? p.bt.slots[wi.b] : 0;
-                if (sq.bad ? j == 0 : j < x.ns) {
-                    const int s = published & 1;
-                    if (published >= 2 && !(ok = wait(&bars.item_empty[s], (published >> 1) - 1))) break;
-                    if (lane == 0) {
-                        s_item[s] = x;
-                        mbar_arrive(bar(&bars.item_full[s]));
+            if (wi.b < 0) return false;
+            const SeqRange sq = seq_range(p.bt, wi.b, bs, nullptr, false);
+            x.kind = sq.bad ? 1 : 0;
+            x.b = wi.b;
+            x.kvh = kvh;
+            x.at = at;
+            x.j = j;
+            x.row0 = sq.row0;
+            x.pos0 = sq.ctx - sq.n;
+            x.r_first = wi.i * 2 * kTcRows;
+            x.r_end = min(sq.n * G, x.r_first + 2 * kTcRows);
+            x.p_first = x.pos0 + (x.r_first >> lgG);
+            x.p_last = x.pos0 + ((x.r_end - 1) >> lgG);
+            x.kt = key_tiles(max(0, x.p_first), max(0, x.p_last), p.window, p.sinks, bs);
+            const int all = (x.kt.n + U - 1) / U;
+            int per = all;
+            if (split) per = max(p.split_tiles * kTile / kTcKeys, (all + S - 1) / S);
+            x.ns = (all + per - 1) / per;
+            x.k0 = j * per;
+            x.n = min(all, x.k0 + per) - x.k0;
+            x.nfull = INT8 ? sq.ctx / bs * bs : sq.ctx;
+            x.slot = INT8 ? p.bt.slots[wi.b] : 0;
+            return sq.bad ? j == 0 : j < x.ns;
+        };
+        bool asked = false;  // for the next CTA, without an answer yet
+        TcItem x;
+        for (;; ++round) {
+            if (describe(x)) {
+                const int s = published & 1;
+                if (published >= 2 && !(ok = wait(&bars.item_empty[s], (published >> 1) - 1))) {
+                    if (lane == 0 && x.kind == 0 && x.ns > 1) (void)arrive(x.at, x.ns);
+                    break;
+                }
+                if (lane == 0) {
+                    s_item[s] = x;
+                    mbar_arrive(bar(&bars.item_full[s]));
+                }
+                ++published;
+                if (x.kind == 0) {
+                    if (loaded > 0 && !(ok = wait(&bars.q_empty, loaded - 1))) break;
+                    // (the test hook leaves one item of the first CTA without its queries)
+                    if (leader && !(blockIdx.x == 0 && loaded == p.skip_copy)) {
+                        const int nq = x.r_end - x.r_first > kTcRows ? 2 : 1;
+                        mbar_arrive_expect_tx(bar(&bars.q_full), uint32_t(nq) * T::kTileBytes);
+                        for (int i = 0; i < nq; ++i)
+                            for (int h = 0; h < D / 64; ++h)
+                                tma_load_4d(q_addr + i * T::kTileBytes + h * T::kSlab, &p.tm_q, h * 64, 0, x.kvh,
+                                            x.row0 + ((x.r_first + i * kTcRows) >> lgG), bar(&bars.q_full));
                     }
-                    ++published;
-                    if (!sq.bad) {
-                        if (loaded > 0 && !(ok = wait(&bars.q_empty, loaded - 1))) break;
-                        if (leader) {
-                            const int nq = x.r_end - x.r_first > kTcRows ? 2 : 1;
-                            mbar_arrive_expect_tx(bar(&bars.q_full), uint32_t(nq) * T::kTileBytes);
-                            for (int i = 0; i < nq; ++i)
-                                for (int h = 0; h < D / 64; ++h)
-                                    tma_load_4d(q_addr + i * T::kTileBytes + h * T::kSlab, &p.tm_q, h * 64, 0, kvh,
-                                                x.row0 + ((x.r_first + i * kTcRows) >> lgG), bar(&bars.q_full));
-                        }
-                        __syncwarp();
-                        ++loaded;
-                    }
+                    __syncwarp();
+                    ++loaded;
                 }
             }
             // ask for the CTA that the grid would start next, an item ahead and no more
@@ -905,7 +931,9 @@ window_tc_kernel(const __grid_constant__ WindowParams p) {
                 next_cta(smem_addr(&s_next), bar(&bars.next));
             }
             __syncwarp();
+            asked = true;
             if (!(ok = wait(&bars.next, round))) break;
+            asked = false;
             const bool more = next_cta_read(smem_addr(&s_next), cx);
             __syncwarp();
             if (!more) break;
@@ -921,13 +949,27 @@ window_tc_kernel(const __grid_constant__ WindowParams p) {
         if (!ok) {
             // let the copies in flight land before the CTA ends
             if (loaded > 0) (void)wait(&bars.q_full, loaded - 1);
+            // ... and the answer about the next CTA, whose item nobody else will take
+            if (asked && wait(&bars.next, round) && next_cta_read(smem_addr(&s_next), cx) && describe(x) && lane == 0 &&
+                x.kind == 0 && x.ns > 1)
+                (void)arrive(x.at, x.ns);
             if (lane == 0) report(p.c.err, kErrTimeout);
         }
+        if (lane == 0) s_published = published;
     }
 
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    // After a wait that ran out, the splits that this CTA took and did not finish arrive
+    // all the same, so that the counters are back at zero when the call ends (its outputs
+    // mean nothing, the next call's do). Described ones that have not arrived are the
+    // last two at most: the softmax gives an item back after it has arrived.
+    if (tid == 0)
+        for (int q = max(s_settled, s_published - 2); q < s_published; ++q) {
+            const TcItem& im = s_item[q & 1];
+            if (im.kind == 0 && im.ns > 1) (void)arrive(im.at, im.ns);
+        }
     if (warp == T::kMmaWarp) tmem_dealloc(tmem, 512);
 }
 
