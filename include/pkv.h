@@ -423,7 +423,9 @@ int pkv_rope_append(const pkv_cache_desc* c, const pkv_batch_desc* batch, const 
  * that need no more bytes). Calls sharing a workspace must not overlap. The
  * splits depend on the lengths alone: the same call gives the same bits. Of
  * more than 16 rows a kv head (max_tokens x group), a split that may have more
- * than 2^25 visible tokens is refused (PKV_ERR_UNSUPPORTED). */
+ * than 2^25 visible tokens is refused, and so is a batch that may have more than
+ * 2^27 pieces of work -- 256 rows of a kv head, at least one a sequence, times
+ * the splits (PKV_ERR_UNSUPPORTED). */
 int pkv_window_attention(const pkv_cache_desc* c, const pkv_batch_desc* batch, const void* q, int64_t q_stride,
                          int32_t window, int32_t sinks, float sm_scale, int32_t split_tokens, void* ws,
                          size_t ws_bytes, void* out, int64_t out_stride, void* stream);

@@ -84,6 +84,55 @@ __device__ __forceinline__ WorkItem locate(int item, int B, Count count) {
     return WorkItem{-1, 0};
 }
 
+// The same list for a warp that looks up many items, near each other: it knows how
+// many there are and keeps the 32 sequences around the item before, so that a walk
+// through the list reads each sequence's lengths once or twice, not once an item.
+template <class Count>
+struct ListCursor {
+    Count count;
+    int B, b0;               // the group of sequences b0 .. b0 + 31: a lane has one
+    int mine, upto, sum;     // its items, those up to its end, the group's
+    long long before, total; // items before the group; of all sequences
+    __device__ __forceinline__ void load(int b) {
+        const int lane = int(threadIdx.x) & 31;
+        b0 = b;
+        mine = b + lane < B ? count(b + lane) : 0;
+        upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(kFull, upto, o);
+            if (lane >= o) upto += x;
+        }
+        sum = __shfl_sync(kFull, upto, 31);
+    }
+    __device__ __forceinline__ ListCursor(int B_, Count count_) : count(count_), B(B_) {
+        const int lane = int(threadIdx.x) & 31, end = (B - 1) / 32 * 32;  // begins at the last group
+        before = 0;
+#pragma unroll 4
+        for (int b = 0; b < end; b += 32) before += count(b + lane);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(kFull, before, o);
+        load(end);
+        total = before + sum;
+    }
+    // Item `item` < total; b == -1 if the lengths have changed meanwhile.
+    __device__ __forceinline__ WorkItem find(long long item) {
+        while (item < before && b0 > 0) {
+            load(b0 - 32);
+            before -= sum;
+        }
+        while (item >= before + sum && b0 + 32 < B) {
+            before += sum;
+            load(b0 + 32);
+        }
+        const int at = int(item - before);
+        const uint32_t past = __ballot_sync(kFull, at < upto);
+        if (at < 0 || !past) return WorkItem{-1, 0};
+        const int l = __ffs(past) - 1;
+        return WorkItem{b0 + l, at - __shfl_sync(kFull, upto - mine, l)};
+    }
+};
+
 // Reports what is wrong with the batch's lengths: one CTA a launch.
 __device__ __forceinline__ void check_lengths(const BatchView& bt, int bs, int32_t* err) {
     for (int b = int(threadIdx.x); b < bt.B; b += int(blockDim.x)) (void)seq_range(bt, b, bs, err, true);

@@ -35,8 +35,8 @@ struct WindowParams {
     int32_t split_tiles;  // 16-token tiles a split (0: no split)
     int32_t max_splits;
     int32_t row_tiles;  // row tiles of max_tokens tokens
-    int32_t item_tiles;  // window_tc_kernel: row tiles that the batch can have; the list of them
-    int32_t split_items;  // with each kv head ends in this many that are split
+    int32_t item_tiles;   // window_tc_kernel: row tiles that the batch can have; the list of those it
+    int32_t split_items;  // has, with each kv head, ends in this many that are split
     float qscale;       // sm_scale * log2(e)
     int32_t skip_copy;  // pkv_debug_skip_copy (-1: off)
 };

@@ -334,6 +334,9 @@ int pkv_window_attention(const pkv_cache_desc* c, const pkv_batch_desc* batch, c
         p.item_tiles = int(pl.most / c->num_kv_heads);
     }
     if (gx > 0x7FFFFFFF) return PKV_ERR_INVALID;
+    // A CTA drops items that the batch does not have at 0.4 us each, while its other
+    // warps wait: 2^27 items on 152 SMs are 0.35 s of the second that they do.
+    if (pl.tc && gx > int64_t(1) << 27) return PKV_ERR_UNSUPPORTED;
     const dim3 grid(unsigned(gx), pl.tc ? 1u : unsigned(c->num_kv_heads), pl.tc ? 1u : unsigned(batch->B));
     return launch(pl.fn, grid, dim3(unsigned(pl.threads)), pl.smem, static_cast<cudaStream_t>(stream), p);
 }

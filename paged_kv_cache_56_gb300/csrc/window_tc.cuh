@@ -853,21 +853,27 @@ window_tc_kernel(const __grid_constant__ WindowParams p) {
         const bool leader = elect_one();
         if (leader) prefetch_tensormap(&p.tm_q);
         int cx = blockIdx.x;
-        const int whole = p.item_tiles * p.c.Hkv - p.split_items;
+        // (row tile, kv head) of all sequences in a list, the row tiles from the last one
+        // on: later rows see more keys. The list's last split_items are split. The grid
+        // has a CTA for each item that the host's bounds allow; behind the batch's own
+        // they have none, and are asked for and dropped.
+        const auto row_tiles = [&](int s) {
+            const SeqRange r = seq_range(p.bt, s, bs, nullptr, false);
+            return int((int64_t(r.n) * G + 2 * kTcRows - 1) / (2 * kTcRows));
+        };
+        ListCursor<decltype(row_tiles)> list(p.bt.B, row_tiles);
+        const int list_tiles = int(list.total < p.item_tiles ? list.total : p.item_tiles);
+        const int items = list_tiles * p.c.Hkv, whole = max(0, items - p.split_items);
         if (cx == 0)
             for (int b = lane; b < p.bt.B; b += 32) (void)seq_range(p.bt, b, bs, p.c.err, true);
         int published = 0, loaded = 0, round = 0;
         // The grid's cx-th CTA's item; false: it has none.
         const auto describe = [&](TcItem& x) {
-            // (row tile, kv head) of all sequences in a list, the row tiles from the last
-            // one on: later rows see more keys. The list's last split_items are split.
             const bool split = cx >= whole;
             const int at = split ? (cx - whole) / S : 0, j = split ? (cx - whole) % S : 0;
             const int item = split ? whole + at : cx, kvh = item % p.c.Hkv;
-            const WorkItem wi = locate(p.item_tiles - 1 - item / p.c.Hkv, p.bt.B, [&](int s) {
-                const SeqRange r = seq_range(p.bt, s, bs, nullptr, false);
-                return int((int64_t(r.n) * G + 2 * kTcRows - 1) / (2 * kTcRows));
-            });
+            if (item >= items) return false;
+            const WorkItem wi = list.find(list_tiles - 1 - item / p.c.Hkv);
             if (wi.b < 0) return false;
             const SeqRange sq = seq_range(p.bt, wi.b, bs, nullptr, false);
             x.kind = sq.bad ? 1 : 0;
