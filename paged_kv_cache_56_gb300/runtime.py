@@ -274,26 +274,31 @@ class PagedKVCache:
             raise ValueError("counts needs one number >= 0 per sequence")
         if len(set(req_ids)) != B:
             raise ValueError("a sequence may be in a batch once")
-        start = np.array([self.seqs[r].length for r in req_ids], np.int32)
-        have = [len(self.table(r)) for r in req_ids]
-        need = [max(0, -(-int(s + n) // self.bs) - h) for s, n, h in zip(start, counts, have)]
-        if any(h + n > self.max_blocks for h, n in zip(have, need)):
+        start = [self.seqs[r].length for r in req_ids]
+        held = [self.table(r) for r in req_ids]
+        ends = [-(-(s + n) // self.bs) for s, n in zip(start, counts.tolist())]
+        need = [max(0, e - len(t)) for e, t in zip(ends, held)]
+        if any(len(t) + n > self.max_blocks for t, n in zip(held, need)):
             raise ValueError("a sequence would pass max_blocks_per_seq")
-        shared = [r for r, s, n in zip(req_ids, start, counts) if self.forked and n and s % self.bs and
-                  pkv.pkv_block_refs(self.alloc, self.table(r)[s // self.bs]) > 1]
+        shared = []  # (sequence, index) of held blocks that it will write and a fork left with several holders
+        if self.forked:
+            shared = [(r, i) for r, s, n, e, t in zip(req_ids, start, counts, ends, held) if n
+                      for i in range(s // self.bs, min(e, len(t))) if pkv.pkv_block_refs(self.alloc, t[i]) > 1]
         if sum(need) + len(shared) > pkv.pkv_num_free(self.alloc):
             raise pkv.PkvError("pkv_append_block", pkv.PKV_ERR_OOM)
         cow = []
-        for r in shared:  # the first rows go into a block that a fork left shared
-            pair = pkv.pkv_cow_block(self.alloc, r, self.seqs[r].length // self.bs)
-            if pair is not None:  # (the other holder may just have taken its own copy)
+        for r, i in shared:
+            pair = pkv.pkv_cow_block(self.alloc, r, i)
+            # (None: the other holder has just taken its own); only a begun block has rows
+            if pair is not None and i * self.bs < self.seqs[r].length:
                 cow.append(pair)
         for r, n in zip(req_ids, need):
             for _ in range(n):
                 pkv.pkv_append_block(self.alloc, r)
         tables = pkv.pkv_build_block_tables(self.alloc, req_ids, self.max_blocks)
         return ChunkPlan(counts=counts, starts=np.concatenate([[0], np.cumsum(counts)]).astype(np.int32),
-                         ctx_lens=start + counts, slots=np.array([self.seqs[r].slot for r in req_ids], np.int32),
+                         ctx_lens=(np.array(start) + counts).astype(np.int32),
+                         slots=np.array([self.seqs[r].slot for r in req_ids], np.int32),
                          tables=tables, cow=cow)
 
     def commit_chunk(self, req_ids, counts) -> None:

@@ -1,0 +1,66 @@
+"""Plans of the runtime on the host: which blocks a chunk or a step takes for
+itself after a fork, and which tokens may be committed."""
+
+import pytest
+
+from libpkv import ensure_built
+from paged_kv_cache_56_gb300 import pkv
+from paged_kv_cache_56_gb300.runtime import PagedKVCache
+
+
+@pytest.fixture(scope="module")
+def L():
+    return ensure_built()
+
+
+def make_cache(blocks=16, bs=16, int8=False, layers=1):
+    return PagedKVCache(layers, blocks, 4, 2, 64, bs, int8, max_slots=4, max_blocks_per_seq=8, device="cpu")
+
+
+def grow(c, r, n, blocks=0):
+    c.add_sequence(r, blocks)
+    c.plan_chunk([r], [n])
+    c.commit_chunk([r], [n])
+
+
+def written(c, r, start, n):
+    return c.table(r)[start // c.bs:-(-(start + n) // c.bs)]
+
+
+def test_a_chunk_writes_no_block_that_another_sequence_holds(L):
+    """Blocks that a sequence held before it was forked, the whole of which the chunk writes."""
+    c = make_cache()
+    grow(c, 1, 20, blocks=4)
+    c.fork(1, 2)
+    before = c.table(1)
+    p = c.plan_chunk([1, 2], [30, 30])
+    assert not set(written(c, 1, 20, 30)) & set(written(c, 2, 20, 30))
+    assert c.table(1)[0] == c.table(2)[0] == before[0]                      # full and shared still
+    assert [list(x[:4]) for x in p.tables] == [c.table(1), c.table(2)]
+    # the begun block's rows are copied; those behind it hold none yet
+    assert p.cow == [(before[1], c.table(1)[1])] or p.cow == [(before[1], c.table(2)[1])]
+    c.close()
+
+
+def test_a_chunk_that_follows_an_unwritten_plan(L):
+    c = make_cache()
+    c.add_sequence(1)
+    c.plan_chunk([1], [40])  # three blocks, one token of them kept
+    c.commit_chunk([1], [1])
+    c.fork(1, 2)
+    c.plan_chunk([1, 2], [31, 31])
+    assert not set(written(c, 1, 1, 31)) & set(written(c, 2, 1, 31))
+    c.close()
+
+
+def test_a_sequence_alone_in_its_batch_leaves_the_other_ones_blocks(L):
+    c = make_cache()
+    grow(c, 1, 32, blocks=4)  # at a block's end: no begun block
+    c.fork(1, 2)
+    before = c.table(1)
+    p = c.plan_chunk([2], [20])
+    assert c.table(1) == before and not set(written(c, 2, 32, 20)) & set(before)
+    assert not p.cow  # nothing to copy
+    c.commit_chunk([2], [20])
+    assert not c.plan_chunk([1], [20]).cow and c.table(1) == before  # held by it alone now
+    c.close()
