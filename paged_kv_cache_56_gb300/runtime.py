@@ -222,10 +222,16 @@ class PagedKVCache:
         for i, r in enumerate(req_ids):
             s = self.seqs[r]
             p = s.length
-            if p % self.bs == 0 and len(self.table(r)) <= p // self.bs:
-                pkv.pkv_append_block(self.alloc, r)
-                changed = True
-            elif self.forked and p % self.bs:
+            if p % self.bs == 0:
+                held = self.table(r)
+                if len(held) <= p // self.bs:
+                    pkv.pkv_append_block(self.alloc, r)
+                    changed = True
+                elif self.forked and pkv.pkv_block_refs(self.alloc, held[p // self.bs]) > 1:
+                    # held ahead of its tokens when the sequence was forked: no rows to copy
+                    pkv.pkv_cow_block(self.alloc, r, p // self.bs)
+                    changed = True
+            elif self.forked:
                 # the row goes into a partly filled block: if a fork left it
                 # shared, this request takes a private copy first
                 pair = pkv.pkv_cow_block(self.alloc, r, p // self.bs)

@@ -64,3 +64,19 @@ def test_a_sequence_alone_in_its_batch_leaves_the_other_ones_blocks(L):
     c.commit_chunk([2], [20])
     assert not c.plan_chunk([1], [20]).cow and c.table(1) == before  # held by it alone now
     c.close()
+
+
+@pytest.mark.parametrize("int8", [False, True])
+def test_a_step_writes_no_block_that_another_sequence_holds(L, int8):
+    """A step that begins a block which a fork left shared."""
+    c = make_cache(int8=int8)
+    grow(c, 1, 16, blocks=3)
+    c.fork(1, 2)  # (at a block's end: no tail to copy)
+    before = c.table(1)
+    p = c.plan_step([1, 2])
+    assert p.block_ids[0] != p.block_ids[1] and before[1] in p.block_ids
+    assert [t[1] for t in p.tables] == list(p.block_ids) and p.tables_changed and not p.cow
+    c.commit_step([1, 2])
+    assert not c.plan_step([1, 2]).cow
+    c.close()
+
