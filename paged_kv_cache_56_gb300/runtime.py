@@ -16,6 +16,7 @@ binding. A decode step for B running sequences is:
 from __future__ import annotations
 
 import math
+from collections import Counter
 from dataclasses import dataclass
 
 import numpy as np
@@ -286,14 +287,17 @@ class PagedKVCache:
         need = [max(0, e - len(t)) for e, t in zip(ends, held)]
         if any(len(t) + n > self.max_blocks for t, n in zip(held, need)):
             raise ValueError("a sequence would pass max_blocks_per_seq")
-        shared = []  # (sequence, index) of held blocks that it will write and a fork left with several holders
+        shared = []  # (sequence, index, block): held blocks to be written that a fork left with several holders
         if self.forked:
-            shared = [(r, i) for r, s, n, e, t in zip(req_ids, start, counts, ends, held) if n
+            shared = [(r, i, t[i]) for r, s, n, e, t in zip(req_ids, start, counts, ends, held) if n
                       for i in range(s // self.bs, min(e, len(t))) if pkv.pkv_block_refs(self.alloc, t[i]) > 1]
-        if sum(need) + len(shared) > pkv.pkv_num_free(self.alloc):
+        # each takes a copy, but the last holder of a block in this batch keeps it if nobody else holds it
+        writers = Counter(block for _, _, block in shared)
+        copies = sum(min(k, pkv.pkv_block_refs(self.alloc, block) - 1) for block, k in writers.items())
+        if sum(need) + copies > pkv.pkv_num_free(self.alloc):
             raise pkv.PkvError("pkv_append_block", pkv.PKV_ERR_OOM)
         cow = []
-        for r, i in shared:
+        for r, i, _ in shared:
             pair = pkv.pkv_cow_block(self.alloc, r, i)
             # (None: the other holder has just taken its own); only a begun block has rows
             if pair is not None and i * self.bs < self.seqs[r].length:

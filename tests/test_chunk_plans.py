@@ -80,3 +80,23 @@ def test_a_step_writes_no_block_that_another_sequence_holds(L, int8):
     assert not c.plan_step([1, 2]).cow
     c.close()
 
+
+def test_the_last_holder_of_a_block_needs_no_copy(L):
+    """Holders of one block in one plan take a copy each but the last, if nobody else holds it."""
+    for others, free, ok in ((0, 1, True), (0, 0, False), (1, 1, False), (1, 2, True)):
+        c = make_cache(blocks=2 + free)
+        grow(c, 1, 20)
+        c.fork(1, 2)
+        if others:
+            c.fork(1, 3)
+        before = c.table(1)
+        if ok:
+            p = c.plan_chunk([1, 2], [3, 3])
+            assert len(p.cow) == 1 + others and pkv.pkv_num_free(c.alloc) == 0
+            assert c.table(1)[1] != c.table(2)[1] and (not others or c.table(3) == before)
+        else:
+            with pytest.raises(pkv.PkvError) as e:
+                c.plan_chunk([1, 2], [3, 3])
+            assert e.value.code == pkv.PKV_ERR_OOM
+            assert c.table(1) == c.table(2) == before and pkv.pkv_num_free(c.alloc) == free
+        c.close()
