@@ -384,7 +384,10 @@ typedef struct pkv_rope {
  * block that fills (pkv_append_kv + pkv_quantize_full_blocks) would leave
  * pool, scales and the slot's tail -- a block begun by earlier tokens takes
  * their rows from the tail, the last, partly filled block ends up there --
- * except that tail rows are written only for tokens of that last block.
+ * except that tail rows are written only for tokens of that last block. A
+ * context that is cut back afterwards (rejected drafted tokens) therefore has to
+ * end in that block or at a block's end: of any other block the tail's rows are
+ * gone, and its codes were made with the rejected rows.
  *
  * With programmatic launch on and max_tokens > 1, the call also launches an
  * empty kernel behind itself, so that the early reads of a decode kernel

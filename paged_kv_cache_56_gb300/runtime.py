@@ -97,7 +97,8 @@ def plan_split_tokens(cache: "PagedKVCache", batch: int, max_ctx: int, num_sms: 
 class Seq:
     req_id: int
     slot: int
-    length: int = 0  # tokens already in the cache
+    length: int = 0   # tokens already in the cache
+    planned: int = 0  # tokens of the last plan_chunk that are not committed
 
 
 @dataclass
@@ -267,6 +268,7 @@ class PagedKVCache:
     def commit_step(self, req_ids) -> None:
         for r in req_ids:
             self.seqs[r].length += 1
+            self.seqs[r].planned = 0
 
 
     # -- a chunk of new tokens a sequence ------------------------------------
@@ -305,6 +307,8 @@ class PagedKVCache:
         for r, n in zip(req_ids, need):
             for _ in range(n):
                 pkv.pkv_append_block(self.alloc, r)
+        for r, n in zip(req_ids, counts.tolist()):
+            self.seqs[r].planned = n
         tables = pkv.pkv_build_block_tables(self.alloc, req_ids, self.max_blocks)
         return ChunkPlan(counts=counts, starts=np.concatenate([[0], np.cumsum(counts)]).astype(np.int32),
                          ctx_lens=(np.array(start) + counts).astype(np.int32),
@@ -312,8 +316,29 @@ class PagedKVCache:
                          tables=tables, cow=cow)
 
     def commit_chunk(self, req_ids, counts) -> None:
+        """Keeps the first counts[i] tokens that the last plan_chunk of each
+        sequence wrote: all of them, or fewer where drafted tokens were rejected
+        (later tokens overwrite those). An INT8 cache has one bf16 tail a
+        sequence: a chunk that passes a block's end has put the next block's rows
+        there, and the codes of the block before were made with the rejected
+        rows. So the kept context has to end in the chunk's last block or at a
+        block's end, or ValueError is raised and nothing is kept. To be able to
+        reject any drafted token, draft up to the begun block's end
+        (block_size - length % block_size tokens) or on a fork."""
+        if len(req_ids) != len(counts) or len(set(req_ids)) != len(req_ids):
+            raise ValueError("counts needs one number per sequence, each sequence once")
+        counts = [int(n) for n in counts]
         for r, n in zip(req_ids, counts):
-            self.seqs[r].length += int(n)
+            s = self.seqs[r]
+            if n < 0 or n > s.planned:
+                raise ValueError(f"sequence {r}: {n} tokens of {s.planned} planned")
+            end = s.length + n
+            if self.int8 and end % self.bs and end // self.bs != (s.length + s.planned) // self.bs:
+                raise ValueError(f"sequence {r}: an INT8 context of {end} tokens cannot be kept of a chunk that went on to "
+                                 f"{s.length + s.planned}")
+        for r, n in zip(req_ids, counts):
+            self.seqs[r].length += n
+            self.seqs[r].planned = 0
 
 
 @dataclass

@@ -100,3 +100,44 @@ def test_the_last_holder_of_a_block_needs_no_copy(L):
             assert e.value.code == pkv.PKV_ERR_OOM
             assert c.table(1) == c.table(2) == before and pkv.pkv_num_free(c.alloc) == free
         c.close()
+
+
+@pytest.mark.parametrize("int8", [False, True])
+def test_fewer_tokens_than_planned_may_be_kept_where_the_cache_still_holds_them(L, int8):
+    """Rejected drafts. An INT8 cache has the partly filled block in the slot's one tail, which a chunk that passes the
+    block's end fills with the next block's rows: a context may then end only in that last block, or at a block's end."""
+    bs = 16
+    for start in (0, 5, 14, 15, 16):
+        for n in (1, 2, 5, 18, 33):
+            for keep in range(n + 1):
+                c = make_cache(int8=int8, bs=bs)
+                grow(c, 1, start)
+                c.plan_chunk([1], [n])
+                end = start + keep
+                if not int8 or end % bs == 0 or end // bs == (start + n) // bs:
+                    c.commit_chunk([1], [keep])
+                    assert c.seqs[1].length == end
+                else:
+                    with pytest.raises(ValueError):
+                        c.commit_chunk([1], [keep])
+                    assert c.seqs[1].length == start
+                    c.commit_chunk([1], [n])  # the whole chunk still may
+                    assert c.seqs[1].length == start + n
+                c.close()
+
+
+def test_a_commit_is_all_or_nothing_and_never_of_more_than_planned(L):
+    c = make_cache(int8=True)
+    grow(c, 1, 14)
+    grow(c, 2, 3)
+    c.plan_chunk([1, 2], [5, 5])
+    for counts in ([1, 5], [5, 6], [5, -1], [5]):
+        with pytest.raises(ValueError):
+            c.commit_chunk([1, 2], counts)
+        assert c.seqs[1].length == 14 and c.seqs[2].length == 3
+    c.commit_chunk([2, 1], [2, 5])
+    assert c.seqs[1].length == 19 and c.seqs[2].length == 5
+    with pytest.raises(ValueError):  # nothing is planned any more
+        c.commit_chunk([2], [1])
+    c.commit_chunk([2], [0])
+    c.close()
