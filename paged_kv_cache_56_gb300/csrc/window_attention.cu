@@ -279,6 +279,7 @@ int pkv_window_attention(const pkv_cache_desc* c, const pkv_batch_desc* batch, c
     if (!q || !out || !aligned16(q) || !aligned16(out) || q_stride < row || out_stride < row ||
         ((q_stride | out_stride) & 7))
         return PKV_ERR_INVALID;
+    if (q == out && q_stride != out_stride) return PKV_ERR_INVALID;
     Plan pl;
     p.skip_copy = g_skip_copy.load(std::memory_order_relaxed);
     if ((st = make_plan(c, batch, window, sinks, &pl, p.skip_copy >= 0)) != PKV_OK) return st;

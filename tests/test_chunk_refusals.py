@@ -1,0 +1,20 @@
+"""Calls of the chunk operators that cannot be right are refused before any launch."""
+
+import pytest
+import torch
+
+from libpkv import ensure_built
+from paged_kv_cache_56_gb300 import pkv
+from test_chunk_host import batch, rope, window
+
+
+@pytest.fixture(scope="module")
+def L():
+    return ensure_built()
+
+
+def test_in_place_with_another_stride(L):
+    """The output may be the queries themselves, row for row only."""
+    for qs, os_ in ((512, 1024), (1024, 512)):
+        assert rope(L, q=16, qs=qs, o=16, os_=os_) == pkv.PKV_ERR_INVALID
+        assert window(L, q=16, qs=qs, o=16, os_=os_) == pkv.PKV_ERR_INVALID
