@@ -686,6 +686,8 @@ class ChunkBuffers:
     own, not a prompt's."""
 
     def __init__(self, cache: PagedKVCache, max_batch: int, max_tokens: int, max_new: int):
+        if not (0 <= max_batch <= 65535 and 0 <= max_new <= max_tokens):
+            raise ValueError("needs 0 <= max_batch <= 65535 and 0 <= max_new <= max_tokens")
         dev = cache.device
         self.cache, self.max_batch, self.max_tokens, self.max_new = cache, max_batch, max_tokens, max_new
 

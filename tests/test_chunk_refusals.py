@@ -18,3 +18,13 @@ def test_in_place_with_another_stride(L):
     for qs, os_ in ((512, 1024), (1024, 512)):
         assert rope(L, q=16, qs=qs, o=16, os_=os_) == pkv.PKV_ERR_INVALID
         assert window(L, q=16, qs=qs, o=16, os_=os_) == pkv.PKV_ERR_INVALID
+
+
+def test_buffers_of_more_new_tokens_than_tokens():
+    """The largest sequence of a batch cannot bring more than the batch; the descriptor would fail at the first launch."""
+    from types import SimpleNamespace
+    from paged_kv_cache_56_gb300.runtime import ChunkBuffers
+    cache = SimpleNamespace(device="cpu", max_blocks=4, int8=False)
+    for args in ((2, 8, 9), (2, 8, -1), (-1, 8, 8), (2, 0, 1), (65536, 8, 8)):
+        with pytest.raises(ValueError, match="max_"):
+            ChunkBuffers(cache, *args)
