@@ -559,8 +559,8 @@ def _rows(t: torch.Tensor, name: str, batch: BatchDesc, heads: int, dim: int, dt
         raise ValueError(f"{name} must be [{batch.num_tokens}, {heads}, {dim}], got {tuple(shape)}")
     if (stride[2] != 1 and dim > 1) or (stride[1] != dim and heads > 1):
         raise ValueError(f"{name}: each token's row must be contiguous")
-    # a single row may carry any stride; the C entry wants one that holds a row
-    return t.data_ptr(), stride[0] if shape[0] > 1 else max(stride[0], heads * dim)
+    # of a single row the stride means nothing: that of a row by itself is passed
+    return t.data_ptr(), stride[0] if batch.num_tokens > 1 else heads * dim
 
 
 # the current stream's handle without a Stream object around it, which costs
