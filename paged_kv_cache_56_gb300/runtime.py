@@ -99,6 +99,7 @@ class Seq:
     slot: int
     length: int = 0   # tokens already in the cache
     planned: int = 0  # tokens of the last plan_chunk that are not committed
+    pinned: int = 0   # blocks of a shared prefix in front of its own
 
 
 @dataclass
@@ -160,7 +161,7 @@ class PagedKVCache:
         pkv.pkv_alloc(self.alloc, req_id, n_blocks)
         if len(shared_blocks):
             pkv.pkv_attach_shared(self.alloc, req_id, list(shared_blocks))
-        s = Seq(req_id, self.free_slots.pop(0), 0)
+        s = Seq(req_id, self.free_slots.pop(0), 0, pinned=len(shared_blocks))
         self.seqs[req_id] = s
         return s
 
@@ -175,7 +176,7 @@ class PagedKVCache:
         p = self.seqs[parent]
         pkv.pkv_fork(self.alloc, parent, child)
         self.forked = True
-        s = Seq(child, self.free_slots.pop(0), p.length)
+        s = Seq(child, self.free_slots.pop(0), p.length, pinned=p.pinned)
         self.seqs[child] = s
         if self.int8 and p.length % self.bs:
             dev = self.layers[0].k_pool.device
@@ -284,6 +285,8 @@ class PagedKVCache:
         if len(set(req_ids)) != B:
             raise ValueError("a sequence may be in a batch once")
         start = [self.seqs[r].length for r in req_ids]
+        if any(n and s < self.seqs[r].pinned * self.bs for r, s, n in zip(req_ids, start, counts)):
+            raise ValueError("a sequence would write into its shared prefix (its length starts behind that)")
         held = [self.table(r) for r in req_ids]
         ends = [-(-(s + n) // self.bs) for s, n in zip(start, counts.tolist())]
         need = [max(0, e - len(t)) for e, t in zip(ends, held)]

@@ -141,3 +141,28 @@ def test_a_commit_is_all_or_nothing_and_never_of_more_than_planned(L):
         c.commit_chunk([2], [1])
     c.commit_chunk([2], [0])
     c.close()
+
+
+def test_a_chunk_does_not_write_a_shared_prefix(L):
+    """Blocks attached in front of a sequence are read-only: its length starts behind them."""
+    c = make_cache()
+    grow(c, 1, 32)
+    c.add_sequence(2, shared_blocks=c.table(1))
+    for start, n, ok in ((0, 5, False), (31, 3, False), (32, 3, True), (0, 0, True)):
+        c.seqs[2].length = start
+        before = c.table(2)
+        if ok:
+            c.plan_chunk([2], [n])
+        else:
+            with pytest.raises(ValueError, match="prefix"):
+                c.plan_chunk([2], [n])
+            assert c.table(2) == before
+    c.commit_chunk([2], [0])
+    c.seqs[2].length = 32
+    c.plan_chunk([2], [3])
+    c.commit_chunk([2], [3])
+    c.fork(2, 3)  # the child's prefix is the parent's
+    c.seqs[3].length = 31
+    with pytest.raises(ValueError, match="prefix"):
+        c.plan_chunk([3], [1])
+    c.close()
