@@ -404,11 +404,19 @@ int pkv_rope_append(const pkv_cache_desc* c, const pkv_batch_desc* batch, const 
  * p (sinks then means nothing). For each of them and query head h
  *   out[row][h] = sum_t softmax_t(sm_scale * q[row][h] . k_t) v_t
  * with K and V read as pkv_decode_attention reads them (INT8 dequantized, the
- * partly filled last block from the slot's tail; V scales below 2^-60 may
- * count as zero). q, out: [num_tokens][Hq][d] bf16 with token strides of
+ * partly filled last block from the slot's tail). q, out: [num_tokens][Hq][d] bf16 with token strides of
  * q_stride, out_stride elements (multiples of 8; both 16-byte aligned); out may
  * be q itself with the same stride, otherwise they must not overlap. sm_scale
- * is finite and not negative, and scores are within +-1e30. fp32 accumulation.
+ * is finite and not negative, and scores are within +-1e30.
+ *
+ * Scores, exponentials and all sums are fp32. A weight meets V in 16 bits (two
+ * bf16 parts; INT8: 11, one f16) in a call of up to 16 rows a kv head (max_tokens
+ * x group), in 8 bits (bf16) in one of more: an error of up to 2^-8 of each
+ * weight, beside the output's own rounding of 2^-8. |V| times the number of
+ * visible tokens is below 2^127. V scales below 2^-60 may count as zero; in a
+ * call of more than 16 rows elements of a bf16 V lose bits below 2^-60, all of
+ * them below 2^-109.
+ *
  * Rows of a sequence with a bad context length are zero; a token whose block id
  * or slot is bad counts as not visible, and a row that sees nothing is zero.
  *

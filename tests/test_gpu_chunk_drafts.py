@@ -70,3 +70,17 @@ def test_rejected_tokens_leave_no_trace(start, n, keep, int8, bs):
         r = rows(m)
         assert torch.equal(drafted.step(r), plain.step(r))
     assert pkv.pkv_sync_status([drafted.cache.layers[0].desc, plain.cache.layers[0].desc]) == 0
+
+
+@pytest.mark.parametrize("bs", [16, 64])
+def test_forked_sequences_with_blocks_ahead_of_their_tokens(bs):
+    """Blocks that a sequence held before it was forked are each holder's own once it writes them, by chunk or by step."""
+    from test_gpu_chunk_run import Model
+    m = Model((8, 2, 64), bs, [False, True], seqs=3, blocks=40)
+    m.cache.add_sequence(1, 5)
+    m.step([1], [20], 0, 0)
+    m.cache.fork(1, 2)
+    m.step([1, 2], [70, 50], 0, 0)  # checks what each holds afterwards against the rows that it brought
+    m.step([2, 1], [1, 1], 0, 0)
+    m.cache.fork(2, 3)
+    m.step([1, 2, 3], [9, 70, 3], 30, 4)
