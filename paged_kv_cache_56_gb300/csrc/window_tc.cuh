@@ -898,7 +898,6 @@ window_tc_kernel(const __grid_constant__ WindowParams p) {
             x.slot = INT8 ? p.bt.slots[wi.b] : 0;
             return sq.bad ? j == 0 : j < x.ns;
         };
-        bool asked = false;  // for the next CTA, without an answer yet
         TcItem x;
         for (;; ++round) {
             if (describe(x)) {
@@ -934,9 +933,8 @@ window_tc_kernel(const __grid_constant__ WindowParams p) {
                 next_cta(smem_addr(&s_next), bar(&bars.next));
             }
             __syncwarp();
-            asked = true;
-            if (!(ok = wait(&bars.next, round))) break;
-            asked = false;
+            // (nobody else will take that CTA's item: its answer is waited for twice as long)
+            if (!(ok = wait(&bars.next, round) || wait(&bars.next, round))) break;
             const bool more = next_cta_read(smem_addr(&s_next), cx);
             __syncwarp();
             if (!more) break;
@@ -952,10 +950,6 @@ window_tc_kernel(const __grid_constant__ WindowParams p) {
         if (!ok) {
             // let the copies in flight land before the CTA ends
             if (loaded > 0) (void)wait(&bars.q_full, loaded - 1);
-            // ... and the answer about the next CTA, whose item nobody else will take
-            if (asked && wait(&bars.next, round) && next_cta_read(smem_addr(&s_next), cx) && describe(x) && lane == 0 &&
-                x.kind == 0 && x.ns > 1)
-                (void)arrive(x.at, x.ns);
             if (lane == 0) report(p.c.err, kErrTimeout);
         }
         if (lane == 0) s_published = published;
