@@ -1,6 +1,8 @@
 """Plans of the runtime on the host: which blocks a chunk or a step takes for
 itself after a fork, and which tokens may be committed."""
 
+import random
+
 import pytest
 
 from libpkv import ensure_built
@@ -165,4 +167,70 @@ def test_a_chunk_does_not_write_a_shared_prefix(L):
     c.seqs[3].length = 31
     with pytest.raises(ValueError, match="prefix"):
         c.plan_chunk([3], [1])
+    c.close()
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_random_walks_never_write_a_block_of_two_sequences(L, seed):
+    """Chunks, steps, forks, rejected drafts and blocks ahead of their tokens, in a pool that runs out now and then."""
+    rng = random.Random(seed)
+    int8 = seed % 2 == 1
+    c = make_cache(blocks=rng.choice([9, 20]), int8=int8)
+    alive, nxt = [], 0
+
+    def writes_alone(reqs, spans):
+        """spans: tokens (from, to) that each request writes."""
+        for r, (a, b) in zip(reqs, spans):
+            mine = c.table(r)[a // c.bs:-(-b // c.bs)] if b > a else []
+            assert len(mine) == (-(-b // c.bs) - a // c.bs if b > a else 0)
+            for other in alive:
+                if other != r:
+                    assert not set(mine) & set(c.table(other)), (seed, r, other)
+
+    for _ in range(60):
+        kind = rng.random()
+        try:
+            if kind < 0.2 and len(alive) < 4:
+                c.add_sequence(nxt, rng.choice([0, 0, 1, 3]))
+                alive.append(nxt)
+                nxt += 1
+            elif kind < 0.35 and alive and len(alive) < 4:
+                p = rng.choice(alive)
+                if int8 and c.seqs[p].length % c.bs:
+                    continue  # (its tail's copy needs a GPU)
+                c.fork(p, nxt)
+                alive.append(nxt)
+                nxt += 1
+            elif kind < 0.45 and alive:
+                c.remove_sequence(alive.pop(rng.randrange(len(alive))))
+            elif kind < 0.65 and alive:
+                reqs = [r for r in rng.sample(alive, rng.randint(1, len(alive))) if c.seqs[r].length < 8 * c.bs]
+                p = c.plan_step(reqs)
+                writes_alone(reqs, [(n, n + 1) for n in p.positions.tolist()])
+                assert len({b for _, b in p.cow}) == len(p.cow)
+                c.commit_step(reqs)
+            elif alive:
+                reqs = rng.sample(alive, rng.randint(1, len(alive)))
+                counts = [rng.choice([0, 1, 5, 16, 40]) for _ in reqs]
+                before = {r: c.table(r) for r in reqs}
+                free = pkv.pkv_num_free(c.alloc)
+                try:
+                    p = c.plan_chunk(reqs, counts)
+                except (pkv.PkvError, ValueError):
+                    assert {r: c.table(r) for r in reqs} == before and pkv.pkv_num_free(c.alloc) == free
+                    continue
+                start = [c.seqs[r].length for r in reqs]
+                writes_alone(reqs, [(s, s + n) for s, n in zip(start, counts)])
+                for r, s in zip(reqs, start):  # rows written before are kept: the same block, or a copy of it
+                    for i in range(-(-s // c.bs)):
+                        now = c.table(r)[i]
+                        assert now == before[r][i] or ((before[r][i], now) in p.cow and i == s // c.bs and s % c.bs)
+                keep = [rng.randint(0, n) for n in counts]
+                try:
+                    c.commit_chunk(reqs, keep)
+                except ValueError:
+                    assert int8
+                    c.commit_chunk(reqs, counts)
+        except pkv.PkvError as e:
+            assert e.code == pkv.PKV_ERR_OOM
     c.close()

@@ -278,3 +278,21 @@ def test_two_calls_at_once():
         assert torch.equal(out, want)
         check(s, out, 0, 0)
         assert s.error_bits() == 0
+
+
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("new", [[1, 3], [40, 300]])
+def test_rows_that_see_nothing_are_zero(new, int8):
+    """A sequence none of whose blocks is there (nor its slot), beside one that is whole; with splits, and with a window."""
+    s = Setup(24, new, [500, 900], (8, 2, 64), 16, int8)
+    s.d_table[0, :] = -1
+    if int8:
+        s.d_slots[0] = -1
+    for window, sinks in ((0, 0), (100, 20)):
+        rows, ref, mag = some_rows(s, window, sinks)
+        mine = rows >= s.starts[1]
+        for split in (0, 128):
+            out = run(s, s.batch, window, sinks, split)
+            assert (out[:s.starts[1]] == 0).all()
+            assert_attention(out[rows[mine]], ref[mine], mag[mine])
+    assert s.error_bits() == pkv.PKV_DEVERR_BLOCK_ID | (pkv.PKV_DEVERR_SLOT if int8 else 0)
