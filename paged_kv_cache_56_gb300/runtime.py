@@ -210,6 +210,11 @@ class PagedKVCache:
         return dict(blocks_total=total, blocks_free=free, blocks_used=total - free, blocks_referenced=len(held),
                     sequences=len(self.seqs), tail_waste_tokens=waste)
 
+    def _copies(self, blocks) -> int:
+        """Free blocks that writing these takes, one entry for each sequence that
+        writes: each takes a copy, but the last of a block's holders keeps it."""
+        return sum(max(0, min(k, pkv.pkv_block_refs(self.alloc, b) - 1)) for b, k in Counter(blocks).items())
+
     # -- one decode step -----------------------------------------------------
     def plan_step(self, req_ids, tables_out: np.ndarray | None = None) -> StepPlan:
         """Host part of one decode step: grows block lists where a new block
@@ -222,6 +227,11 @@ class PagedKVCache:
         slots = np.empty(B, np.int32)
         changed = False
         cow = []
+        if self.forked:  # a copy must not be taken by a plan that then runs out of blocks: the caller would not make it
+            at = [(self.table(r), self.seqs[r].length // self.bs) for r in req_ids]
+            need = sum(len(t) <= j for t, j in at)
+            if need + self._copies([t[j] for t, j in at if j < len(t)]) > pkv.pkv_num_free(self.alloc):
+                raise pkv.PkvError("pkv_append_block", pkv.PKV_ERR_OOM)
         for i, r in enumerate(req_ids):
             s = self.seqs[r]
             p = s.length
@@ -296,10 +306,7 @@ class PagedKVCache:
         if self.forked:
             shared = [(r, i, t[i]) for r, s, n, e, t in zip(req_ids, start, counts, ends, held) if n
                       for i in range(s // self.bs, min(e, len(t))) if pkv.pkv_block_refs(self.alloc, t[i]) > 1]
-        # each takes a copy, but the last holder of a block in this batch keeps it if nobody else holds it
-        writers = Counter(block for _, _, block in shared)
-        copies = sum(min(k, pkv.pkv_block_refs(self.alloc, block) - 1) for block, k in writers.items())
-        if sum(need) + copies > pkv.pkv_num_free(self.alloc):
+        if sum(need) + self._copies([block for _, _, block in shared]) > pkv.pkv_num_free(self.alloc):
             raise pkv.PkvError("pkv_append_block", pkv.PKV_ERR_OOM)
         cow = []
         for r, i, _ in shared:

@@ -234,3 +234,23 @@ def test_random_walks_never_write_a_block_of_two_sequences(L, seed):
         except pkv.PkvError as e:
             assert e.code == pkv.PKV_ERR_OOM
     c.close()
+
+
+def test_a_step_without_room_takes_no_copies(L):
+    """plan_step that runs out of blocks after a fork: nothing has changed, so no copy is lost."""
+    c = make_cache(blocks=4)
+    grow(c, 1, 5)
+    c.fork(1, 2)
+    grow(c, 3, 16)
+    c.add_sequence(4, 1)
+    before = [c.table(r) for r in (1, 2, 3)]
+    with pytest.raises(pkv.PkvError) as e:
+        c.plan_step([1, 3])  # a copy and a new block, one is free
+    assert e.value.code == pkv.PKV_ERR_OOM
+    assert [c.table(r) for r in (1, 2, 3)] == before and pkv.pkv_num_free(c.alloc) == 1
+    c.remove_sequence(4)
+    p = c.plan_step([1, 3])
+    assert len(p.cow) == 1 and p.cow[0][0] == before[0][0]
+    c.commit_step([1, 3])
+    assert not c.plan_step([2]).cow  # the last holder keeps the block
+    c.close()
