@@ -20,7 +20,7 @@
 //
 // Bound by memory: 2 * (Hq + Hkv + Hkv) * d bytes read a token, and as much
 // written (the INT8 cache half of its part). Measured, d = 128, 8 kv heads:
-// 30718 tokens of 16 query heads, bf16, 503 MB in 80 us, 6.3 TB/s (a plain copy:
+// 30718 tokens of 16 query heads, bf16, 503 MB in 82 us, 6.1 TB/s (a plain copy:
 // 6.7); 12535 tokens of 32 query heads, INT8, 282 MB in 53 us, 5.4 TB/s -- the
 // quantizer's arithmetic and its block maximum (a barrier a head) leave half of
 // the issue slots and a part of the loads idle; 128 single tokens 8.6 us (bf16 5.7),

@@ -19,6 +19,8 @@
 // tiles, each load waiting for the one before, about 7 us -- before the stream
 // and the merge behind it, and the SMs with three CTAs wait for those with four.
 // Splits that even this out cost more in merging than they gain (58 us).
+// With 16 rows a tile over INT8 (d = 128) 49 words spill under the 168 registers of
+// three CTAs an SM, and issue bounds it: 16 sequences of 7000 tokens 68 us, 34 by bytes.
 #pragma once
 
 #include "window.cuh"

@@ -36,10 +36,11 @@
 // (half a step, 2^-8 of each weight, as the outputs are); their sum is fp32.
 //
 // Measured, d = 128, 8 kv heads (4 d flops a visible pair and head): causal
-// prompts of 7400 to 8000 tokens, 16 query heads, bf16, 1.0 TF in 702 us, 1425
-// TF/s (cuBLAS: 1969); prompts of 5000 to 8192 tokens, window 1024, 32 query
-// heads, 211 GF in 196 us; chunks of 100 to 512 tokens, window 4096, INT8, 161 GF
-// in 192 us. A key tile of an item takes about 3400 cycles, its multiplies 2048
+// prompts of 7400 to 8000 tokens, 16 query heads, bf16, 1.0 TF in 707 us, 1415
+// TF/s (cuBLAS: 1969), 745 to 755 us at the clocks that a long run settles at;
+// prompts of 5000 to 8192 tokens, window 1024, 32 query heads, 211 GF in 197 to
+// 201 us; chunks of 100 to 512 tokens, window 4096, INT8, 161 GF in 193 us. The
+// INT8 kernel of d = 128 spills 17 words. A key tile of an item takes about 3400 cycles, its multiplies 2048
 // of them. They read 192 KB of shared memory for it (Q and K at 128 bytes a cycle,
 // all that it has; V at 64) and the copies write another 64 KB, 2048 cycles too;
 // what is above that is the chain from scores to weights (without the loads from
@@ -50,6 +51,11 @@
 // much to shared memory again, and 328 items on 152 SMs fill two rounds and a
 // sixth, whose items are split. Of other forms, two threads a row, exponentials
 // in polynomials, and scores in two buffers of 32 columns were slower or the same.
+//
+// Work list: a CTA counts the batch's row tiles once and walks along the list (3 of
+// 65535 sequences with tokens: 1.75 ms a call, of which 0.4 us for each item of the
+// grid that the batch does not have; searched from the front for every item, 3 of
+// 16000 took 142 ms).
 #pragma once
 
 #include "ptx_tc.cuh"
