@@ -404,10 +404,11 @@ int pkv_rope_append(const pkv_cache_desc* c, const pkv_batch_desc* batch, const 
  * p (sinks then means nothing). For each of them and query head h
  *   out[row][h] = sum_t softmax_t(sm_scale * q[row][h] . k_t) v_t
  * with K and V read as pkv_decode_attention reads them (INT8 dequantized, the
- * partly filled last block from the slot's tail). q, out: [num_tokens][Hq][d] bf16 with token strides of
- * q_stride, out_stride elements (multiples of 8; both 16-byte aligned); out may
- * be q itself with the same stride, otherwise they must not overlap. sm_scale
- * is finite and not negative, and scores are within +-1e30.
+ * partly filled last block from the slot's tail). q, out: [num_tokens][Hq][d]
+ * bf16 with token strides of q_stride, out_stride elements (multiples of 8; both
+ * 16-byte aligned); out may be q itself with the same stride, otherwise they
+ * must not overlap. sm_scale is finite and not negative, and scores are within
+ * +-1e30.
  *
  * Scores, exponentials and all sums are fp32. A weight meets V in 16 bits (two
  * bf16 parts; INT8: 11, one f16) in a call of up to 16 rows a kv head (max_tokens

@@ -227,7 +227,8 @@ class PagedKVCache:
         slots = np.empty(B, np.int32)
         changed = False
         cow = []
-        if self.forked:  # a copy must not be taken by a plan that then runs out of blocks: the caller would not make it
+        if self.forked and pkv.pkv_num_free(self.alloc) < B:
+            # a copy must not be taken by a plan that then runs out of blocks: the caller would not make it
             at = [(self.table(r), self.seqs[r].length // self.bs) for r in req_ids]
             need = sum(len(t) <= j for t, j in at)
             if need + self._copies([t[j] for t, j in at if j < len(t)]) > pkv.pkv_num_free(self.alloc):
@@ -331,10 +332,11 @@ class PagedKVCache:
         (later tokens overwrite those). An INT8 cache has one bf16 tail a
         sequence: a chunk that passes a block's end has put the next block's rows
         there, and the codes of the block before were made with the rejected
-        rows. So the kept context has to end in the chunk's last block or at a
-        block's end, or ValueError is raised and nothing is kept. To be able to
-        reject any drafted token, draft up to the begun block's end
-        (block_size - length % block_size tokens) or on a fork."""
+        rows. So the kept context has to end in the block that the chunk ends in
+        or at a block's end, or ValueError is raised and nothing is kept. Where
+        the first token stays, p = length + 1, any of block_size - 1 - p %
+        block_size tokens behind it can be rejected; of longer drafts, on a fork.
+        A chunk that has run is committed, with 0 if nothing of it stays."""
         if len(req_ids) != len(counts) or len(set(req_ids)) != len(req_ids):
             raise ValueError("counts needs one number per sequence, each sequence once")
         counts = [int(n) for n in counts]

@@ -254,3 +254,18 @@ def test_a_step_without_room_takes_no_copies(L):
     c.commit_step([1, 3])
     assert not c.plan_step([2]).cow  # the last holder keeps the block
     c.close()
+
+
+@pytest.mark.parametrize("bs", [16, 64])
+def test_drafts_that_can_always_be_rejected(L, bs):
+    """Behind a token that stays, as many drafted ones as commit_chunk says: any number of them may be kept."""
+    for start in list(range(2 * bs)):
+        p = start + 1
+        drafts = bs - 1 - p % bs
+        for keep in {1, 1 + drafts // 2, 1 + drafts}:
+            c = make_cache(int8=True, bs=bs)
+            grow(c, 1, start)
+            c.plan_chunk([1], [1 + drafts])
+            c.commit_chunk([1], [keep])
+            assert c.seqs[1].length == start + keep
+            c.close()
