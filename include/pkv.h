@@ -62,6 +62,8 @@ extern "C" {
 #define PKV_DEVERR_OFFSET      8  /* in-block offset < 0 or >= block_size */
 #define PKV_DEVERR_TIMEOUT    16  /* a bounded wait on an asynchronous copy expired */
 #define PKV_DEVERR_BATCH      32  /* token_starts descend, pass num_tokens or give a sequence more than max_tokens */
+#define PKV_DEVERR_OOM        64  /* pkv_plan_batch: the ring holds fewer free blocks than the batch needs */
+#define PKV_DEVERR_SEGMENT   128  /* pkv_axis_positions: a segment or a number of segments that cannot be */
 
 #define PKV_DTYPE_BF16 0
 #define PKV_DTYPE_INT8 1
@@ -459,6 +461,167 @@ size_t pkv_window_ws_bytes(const pkv_cache_desc* c, const pkv_batch_desc* batch,
 #define PKV_OUT_FP32 1
 int pkv_gather_kv(const pkv_cache_desc* c, const pkv_batch_desc* batch, const int32_t* first,
                   void* k_out, void* v_out, int64_t out_stride, int32_t out_dtype, void* stream);
+
+/* ======================================================================== */
+/* Batches planned on the GPU                                               */
+/* ======================================================================== */
+
+/* Block lists, lengths and free blocks of the sequence slots, in device
+ * memory: what the host allocator and a runtime keep on the host, for steps
+ * that are planned, run and replayed without it. Blocks have one holder each
+ * (no forks, no shared prefixes). Free ids are a FIFO ring as the host
+ * allocator's list is: taken from the front, given back at the end.
+ *   tables [max_slots][max_blocks]  the blocks that a slot holds, in order
+ *   lens   [max_slots]              its tokens in the cache
+ *   held   [max_slots]              its blocks (blocks ahead of its tokens are fine)
+ *   ring   [num_blocks]             free ids from place state[0] on, wrapping around
+ *   state  [4]                      that place, the number of free ids, 0, 0
+ * A free slot has lens = held = 0. max_slots <= 65536; max_blocks * block_size
+ * < 2^31 - 2^16. int8: some layer keeps INT8 blocks (pkv_commit_batch). Calls
+ * on one pool must not overlap, and nothing else may read or write it meanwhile. */
+typedef struct pkv_seq_pool {
+    int32_t* tables;
+    int32_t* lens;
+    int32_t* held;
+    int32_t* ring;
+    int32_t* state;
+    int32_t* err_word;      /* nullable */
+    int32_t  max_slots;
+    int32_t  max_blocks;
+    int32_t  num_blocks;
+    int32_t  block_size;    /* 16 or 64 */
+    int32_t  int8;
+} pkv_seq_pool;
+
+/* Where pkv_plan_batch puts a batch of B entries (device memory; the first
+ * three make a pkv_batch_desc together with the slots, the others may be NULL):
+ *   token_starts [B + 1]             first row of each entry's new tokens
+ *   block_tables [B][max_blocks]     the entry's blocks, -1 behind them
+ *   ctx_lens     [B]                 its tokens, the new ones included
+ *   fill_blocks  [B]                 the block that its last new token fills, or -1
+ *   block_ids, offsets, token_slots, positions [num_tokens]: of each row the block
+ *                and the offset in it, the slot, and the token's index in its
+ *                sequence; rows behind the batch's are -1, 0, -1, 0. */
+typedef struct pkv_plan {
+    int32_t* token_starts;
+    int32_t* block_tables;
+    int32_t* ctx_lens;
+    int32_t* fill_blocks;
+    int32_t* block_ids;
+    int32_t* offsets;
+    int32_t* token_slots;
+    int32_t* positions;
+    int32_t  num_tokens;
+    int32_t  max_tokens;
+} pkv_plan;
+
+/* Plans counts[b] >= 0 new tokens (NULL: one each) of the sequences in slots[b]
+ * (both device int32 [B]; slot -1: an entry without a sequence, without tokens).
+ * Each sequence takes the blocks that its list lacks from the ring, in the
+ * batch's order, as pkv_append_block would one by one; lens stay (see
+ * pkv_commit_batch), so a plan that is made again finds its blocks held.
+ *
+ * All or nothing: a slot outside [0, max_slots) or twice in the batch
+ * (PKV_DEVERR_SLOT), a count outside [0, max_tokens] or more than num_tokens in
+ * all (PKV_DEVERR_BATCH), a sequence that would pass max_blocks or whose length
+ * and blocks do not hold together (PKV_DEVERR_CTX_LEN), or too few free
+ * blocks (PKV_DEVERR_OOM) leaves the pool as it was and makes an empty plan: no
+ * rows, lengths of 0, ids of -1, on which every operator and pkv_commit_batch
+ * do nothing. B == 0 is a no-op. B <= 65535, max_tokens <= num_tokens < 2^31 - 2^16.
+ *
+ * With programmatic launch on, the call also launches an empty kernel behind
+ * itself, as pkv_rope_append does. */
+int pkv_plan_batch(const pkv_seq_pool* pool, const int32_t* slots, const int32_t* counts, int32_t B,
+                   const pkv_plan* plan, void* stream);
+
+/* Keeps the first accepted[b] tokens (NULL: all; device int32 [B]) that each
+ * entry of a plan brought: lens[slots[b]] = ctx_lens[b] - n_b + accepted[b].
+ * An entry without new tokens keeps its length. accepted outside [0, n_b], or
+ * an INT8 context that would end in another block than the chunk without ending at
+ * a block's end (its rows are gone: see pkv_rope_append), leaves the length as it
+ * was (PKV_DEVERR_CTX_LEN); so does a length that is not ctx_lens[b] - n_b: a
+ * plan is committed once. A slot twice among entries with tokens is not found. */
+int pkv_commit_batch(const pkv_seq_pool* pool, const int32_t* slots, const int32_t* accepted, int32_t B,
+                     const pkv_plan* plan, void* stream);
+
+/* Gives all blocks of the sequences in slots[b] (-1: none) back, in the batch's
+ * order and each list's, and frees the slots. A slot out of range or
+ * twice in the batch (PKV_DEVERR_SLOT), or lists that hold more than the ring has
+ * room for (PKV_DEVERR_CTX_LEN): nothing is given back. A free slot has nothing to
+ * give. */
+int pkv_release_batch(const pkv_seq_pool* pool, const int32_t* slots, int32_t B, void* stream);
+
+/* ======================================================================== */
+/* Prompts with images and video                                            */
+/* ======================================================================== */
+
+/* Rotary positions on three axes (time, height, width) of a batch's tokens. A
+ * sequence is a list of segments {t, h, w, step}, its tokens in order:
+ *   h = w = 0: t tokens of text, token i at base + i on every axis;
+ *   else     : a grid of t frames of h rows of w tokens, token (i, j, k) at
+ *              (base + i * step, base + j, base + k), `step` positions a frame;
+ * the first base is 0, the next one 1 + the largest position of the segment on
+ * any axis. Tokens behind the last segment are text. segments
+ * [num_rows][max_segments][4] and num_segments [num_rows] (device int32, 16- and
+ * 4-byte aligned) are looked up at row rows[b] (device [B]; NULL: row b -- pass the
+ * batch's slots to keep a list for each slot). positions: device int32, axis a at
+ * positions + a * axis_stride, [num_tokens] each; rows of the batch are
+ * written, others left. Positions stop at 2^31 - 1.
+ *
+ * Of the batch, token_starts, ctx_lens (below 2^31 - 2^16) and the bounds are used. A segment with
+ * negative numbers, with only one of h and w 0, of more than 2^31 - 1 tokens or
+ * positions counts as empty (PKV_DEVERR_SEGMENT); a number of segments outside
+ * [0, max_segments], too, leaves the sequence's rows as they were, and so does a
+ * row outside [0, num_rows) (PKV_DEVERR_SLOT). err_word may be NULL. */
+int pkv_axis_positions(const pkv_batch_desc* batch, const int32_t* segments, const int32_t* num_segments,
+                       int32_t num_rows, int32_t max_segments, const int32_t* rows, int32_t* positions,
+                       int64_t axis_stride, int32_t* err_word, void* stream);
+
+/* Rotary positions on several axes: as pkv_rope, but pair j turns by the
+ * position on axis pair_axis[j] (0 .. num_axes - 1, num_axes 1 .. 4). positions:
+ * device int32, axis a's [num_tokens] at positions + a * axis_stride; NULL: the
+ * token's index in the context, on every axis. */
+typedef struct pkv_rope_axes {
+    const double*  inv_freq;
+    const int32_t* positions;
+    int64_t axis_stride;
+    int32_t num_axes;
+    int32_t rotary_dim;
+    int32_t interleaved;
+    float   scale;
+    uint8_t pair_axis[64];
+} pkv_rope_axes;
+
+/* pkv_rope_append with positions on several axes. k_out (nullable)
+ * [num_tokens][Hkv][d], token stride k_out_stride: the turned k, rounded to bf16
+ * as it goes into the cache, also as rows (pkv_prompt_attention reads them);
+ * rows whose block or slot is bad are there too. k_out may be k itself with the
+ * same stride; otherwise the outputs overlap neither the inputs nor each other. */
+int pkv_rope_append_axes(const pkv_cache_desc* c, const pkv_batch_desc* batch, const pkv_rope_axes* rope,
+                         const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                         const void* v, int64_t v_stride, void* q_out, int64_t q_out_stride,
+                         void* k_out, int64_t k_out_stride, void* stream);
+
+/* Attention of whole prompts from their rows: row i of sequence b sees its rows
+ *   t <= i  and  (i - t < window  or  t < sinks)
+ * (window 0: every row up to i), and for query head h
+ *   out[row i][h] = sum_t softmax_t(sm_scale * q[row i][h] . k[row t]) v[row t].
+ * q, out [num_tokens][Hq][d], k, v [num_tokens][Hkv][d] bf16 with token strides
+ * of q_stride, ... elements (multiples of 8, all pointers 16-byte aligned), q and k
+ * already turned. The cache is not read: with an INT8 cache the prompt's attention
+ * meets K and V before they are quantized. out may be q itself with the
+ * same stride; otherwise it overlaps no input. sm_scale is finite and not
+ * negative, scores are within +-1e30.
+ *
+ * Of the descriptors, the heads, head_dim and err_word, token_starts, ctx_lens
+ * and the bounds are used. ctx_lens[b] == n_b says that the sequence has no
+ * earlier tokens: the rows of one that has are zero (PKV_DEVERR_CTX_LEN).
+ * Precision is that of pkv_window_attention with more than 16 rows. The K and V
+ * of a sequence's rows must be finite; those of other sequences, and rows behind the
+ * batch, may hold anything. */
+int pkv_prompt_attention(const pkv_cache_desc* c, const pkv_batch_desc* batch, const void* q, int64_t q_stride,
+                         const void* k, int64_t k_stride, const void* v, int64_t v_stride, int32_t window,
+                         int32_t sinks, float sm_scale, void* out, int64_t out_stride, void* stream);
 
 /* Reads, clears and reports the error words of n descriptors once the work
  * queued on `stream` has finished: synchronises the stream, copies each

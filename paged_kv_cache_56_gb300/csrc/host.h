@@ -54,4 +54,21 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 int pool_tensor_map(const void* pool, int32_t num_blocks, int32_t rows, int32_t row_bytes, CUtensorMap* out,
                     int32_t box_rows = 16);
 
+int encode_map(CUtensorMapDataType type, int rank, const void* base, const cuuint64_t* dims, const cuuint64_t* strides,
+               const cuuint32_t* box, CUtensorMap* out);
+
+// Tensor map of token rows [tokens][kv_heads][group][head_dim], bf16, `stride`
+// elements a token, for boxes of `rows` rows (rows / group tokens x the group) x
+// 64 elements with the 128-byte swizzle.
+int rows_tensor_map(int group, int kv_heads, int head_dim, int tokens, const void* base, int64_t stride, int rows,
+                    CUtensorMap* out);
+
+// Raises a kernel's dynamic shared-memory limit once per kernel and device and
+// returns how many of its CTAs fit on an SM; launch_regs > 0: fails unless
+// the kernel has just that many registers a thread.
+int prepare_kernel(const void* kernel, size_t smem, int threads, int launch_regs, int* ctas);
+
+// SMs of the current device.
+int sm_count(int* out);
+
 }  // namespace pkv

@@ -1,0 +1,561 @@
+// Attention of whole prompts from their rows (pkv_prompt_attention), on the tensor
+// cores of sm_103a (tcgen05, accumulators in tensor memory).
+//
+// A work item is (256 rows, kv head, sequence): two tiles of 128 rows, a row a
+// (token, query head of the group), so that a kv head's whole group shares each
+// K and V tile that the CTA loads. Keys come in tiles of 128 tokens, a tensor
+// copy of 128 rows x 64 elements at a time. There is one CTA a SM; it walks from
+// item to item, taking the grid's next one from the hardware (launch
+// cancellation) while it works. Long items are first in the grid.
+//
+//   warps 0-3, 4-7: softmax of row tile 0 and 1, one row a thread; scores from
+//                   tensor memory, weights back to it
+//   warp 8          the loader of K and V
+//   warp 9          items, and their queries
+//   warp 10         issues the multiplies
+//
+//   S_i = Q_i K^T   128 x 128 x D, operands in shared memory
+//   O_i += P_i V    128 x D x 128, P_i in tensor memory over the scores it came from
+//
+// The running maximum is a reference that follows the true one only when that
+// is more than 2^12 ahead, so O_i is rarely rescaled. Weights are kept in units of
+// 2^-40 and rounded to bf16 for the multiply (2^-8 of each weight, as
+// the outputs are); their sum is fp32.
+#pragma once
+
+#include "ptx_tc.cuh"
+#include "window.cuh"
+
+namespace pkv {
+
+constexpr int kPrRows = 128;  // rows of a row tile
+constexpr int kPrKeys = 128;  // tokens of a key tile
+constexpr float kPrShift = 40.f;
+constexpr float kPrAhead = 12.f;
+constexpr int kPrThreads = 384;
+constexpr int kPrLaunchRegs = 168;
+
+struct PromptParams {
+    CUtensorMap tm_q;    // q as [tokens][Hkv][G][D], boxes of 128 rows x 64 elements
+    CUtensorMap tm_k;    // k, v as [tokens][Hkv][1][D], boxes of 128 rows x 64 elements
+    CUtensorMap tm_v;
+    CUtensorMap tm_out;  // out as q, boxes of 32 rows
+    BatchView bt;
+    uint16_t* out;
+    int64_t out_stride;
+    int32_t* err;
+    int32_t Hq, Hkv;
+    int32_t window;      // INT32_MAX: none
+    int32_t sinks;
+    int32_t item_rows;   // 128 or 256
+    int32_t item_tiles;  // row tiles that the batch can have
+    float qscale;        // sm_scale * log2(e)
+};
+
+template <int D>
+struct PromptTraits {
+    static constexpr int kTileBytes = kPrKeys * D * 2;  // one K or V tile = one row tile of Q
+    static constexpr int kStages = D == 64 ? 6 : 4;
+    static constexpr int kSmem = 1024 + (2 + kStages) * kTileBytes + 8 * 4096;
+    static constexpr int kSlab = kPrKeys * 128;         // 64 of a tile's D columns
+    static constexpr int kSoftmaxRegs = 200, kRestRegs = 104;
+    static_assert(256 * kSoftmaxRegs + 128 * kRestRegs == kPrThreads * kPrLaunchRegs, "register split");
+};
+
+template <int STAGES>
+struct PromptBars {
+    uint64_t q_full, q_empty;
+    uint64_t kv_full[STAGES];
+    uint64_t kv_empty[STAGES];
+    uint64_t fix;            // a V tile whose dead rows have to be cleared first
+    uint64_t s_full[2];      // S_i is there and O_i += P_i V of the tile before is done
+    uint64_t p_full[2];      // P_i is there, O_i corrected
+    uint64_t o_full[2];      // O_i is complete
+    uint64_t item_full[2];   // an item's description is there
+    uint64_t item_empty[2];  // every warp has taken it
+    uint64_t next;           // the answer about the next item is there
+    uint64_t drain;
+};
+
+struct PromptItem {
+    int kind;  // 0: attention; 1: rows of a sequence with earlier tokens, zero; 2: the end
+    int kvh, row0, n;    // kv head; the sequence's first row, its rows (tokens)
+    int r_first, r_end;
+    KeyTiles kt;
+};
+
+template <bool V>
+struct PromptConst {
+    static constexpr bool value = V;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_constant__ PromptParams p) {
+    using T = PromptTraits<D>;
+    constexpr int STAGES = T::kStages, kMmaWarp = 10, kPlanWarp = 9, kLoadWarp = 8;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ PromptBars<STAGES> bars;
+    __shared__ PromptItem s_item[2];
+    __shared__ __align__(16) uint4 s_next;
+    __shared__ uint32_t s_tmem;
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int G = p.Hq / p.Hkv, lgG = 31 - __clz(G);
+    uint8_t* q_smem = smem + ((1024u - (smem_addr(smem) & 1023u)) & 1023u);
+    const uint32_t q_addr = smem_addr(q_smem), kv_addr = q_addr + 2 * T::kTileBytes;
+    const uint32_t stage0 = kv_addr + STAGES * T::kTileBytes;  // 4 KB a softmax warp, for its output rows
+    const uint32_t bar0 = smem_addr(&bars);
+    const auto bar = [&](const uint64_t* x) {
+        return bar0 + uint32_t(reinterpret_cast<const uint8_t*>(x) - reinterpret_cast<const uint8_t*>(&bars));
+    };
+    if (tid == 0) {
+        mbar_init(bar(&bars.q_full), 1);
+        mbar_init(bar(&bars.q_empty), 1);
+        mbar_init(bar(&bars.fix), 1);
+        mbar_init(bar(&bars.next), 1);
+        mbar_init(bar(&bars.drain), 1);
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(bar(&bars.kv_full[s]), 1);
+            mbar_init(bar(&bars.kv_empty[s]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(&bars.s_full[i]), 1);
+            mbar_init(bar(&bars.p_full[i]), kPrRows);
+            mbar_init(bar(&bars.o_full[i]), 1);
+            mbar_init(bar(&bars.item_full[i]), 1);
+            mbar_init(bar(&bars.item_empty[i]), 8 + 2);
+        }
+        fence_mbar_init();
+    }
+    if (warp == kMmaWarp) tmem_alloc(smem_addr(&s_tmem), 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    // Waits for a phase, a whole warp, which it leaves converged. After about a
+    // second without it a role gives up, and so, one after the other, do those
+    // that wait for it.
+    const auto wait = [&](const uint64_t* x, uint32_t parity) {
+        return __all_sync(kFull, wait_phase(bar(x), parity & 1u)) != 0;
+    };
+    pdl_wait();
+    pdl_launch_dependents();
+
+    bool ok = true;
+    // The q-th item of this CTA (every warp but the planner's): false at the end.
+    const auto take = [&](int q) {
+        ok = wait(&bars.item_full[q & 1], q >> 1);
+        return ok && s_item[q & 1].kind != 2;
+    };
+    // Its description is no longer needed.
+    const auto release = [&](int q) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(&bars.item_empty[q & 1]));
+    };
+
+    if (warp < 8) reg_inc<T::kSoftmaxRegs>();
+    else reg_dec<T::kRestRegs>();
+
+    if (warp < 8) {
+        // ================= softmax of row tile i, a row a thread =================
+        const int i = warp >> 2;
+        const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
+        const uint32_t s_addr = tmem + uint32_t(i) * 128u + lane_base, o_addr = tmem + 256u + uint32_t(i) * 128u + lane_base;
+        const float scale = p.qscale;
+        int mine = 0, done = 0;  // key tiles and items of this row tile
+        for (int q = 0; take(q); release(q++)) {
+            const PromptItem& im = s_item[q & 1];
+            const int row = im.r_first + tid;  // tid < 256: rows of the item in order
+            const bool have = row < im.r_end;
+            if (im.kind == 1) {
+                for (int e = tid; e < (im.r_end - im.r_first) * D; e += 256) {
+                    const int r = im.r_first + e / D;
+                    p.out[int64_t(im.row0 + (r >> lgG)) * p.out_stride + (im.kvh * G + (r & (G - 1))) * D + e % D] = 0;
+                }
+                continue;
+            }
+            if (im.r_first + i * kPrRows >= im.r_end) continue;
+            const KeyTiles kt = im.kt;
+            const int n = kt.n;
+            float m_ref = -INFINITY;  // reference of the exponent (base 2)
+            float2 l2 = make_float2(0.f, 0.f);
+            const int hi = have ? row >> lgG : -1, lo = max(0, hi - p.window + 1);
+            // the row tile's first and last position
+            const int pf = (im.r_first + i * kPrRows) >> lgG, pl = (min(im.r_end, im.r_first + (i + 1) * kPrRows) - 1) >> lgG;
+            for (int jj = 0; jj < n; ++jj) {
+                if (!(ok = wait(&bars.s_full[i], mine + jj))) break;
+                tc_fence_after();
+                const int t0 = kt.tile(jj) * kPrKeys;
+                const bool masked = jj < kt.nsink || t0 + kPrKeys - 1 > pf || t0 < pl - p.window + 1;
+                // One pass: weights against the reference as it stands, and the true
+                // maximum beside them. Where a row's maximum is too far ahead (its
+                // first tile, and rarely later) the reference follows, the sums and
+                // O_i are rescaled, and the pass is made again: the weights wait in
+                // registers (w), so the scores are still there. 16 columns at a time,
+                // one chunk's load in flight while the other is worked on.
+                uint32_t w[8][8];
+                float2 sum;
+                for (;;) {
+                    const float neg = (m_ref == -INFINITY ? 0.f : -m_ref) - kPrShift;
+                    float mx = -INFINITY;
+                    sum = make_float2(0.f, 0.f);
+                    const auto chunk = [&](auto hide, uint32_t (&r)[16], int c) {
+                        if constexpr (hide.value) {
+                            const int tc = t0 + c * 16;
+                            // bit e: this row sees token tc + e
+                            const auto below = [](int x) { return (1u << min(16, max(0, x))) - 1u; };
+                            const uint32_t see = below(hi - tc + 1) & (below(p.sinks - tc) | ~below(lo - tc));
+                            if (__all_sync(kFull, (see & 0xFFFFu) == 0u)) {  // nothing for the whole warp
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) w[c][e] = 0u;
+                                return;
+                            }
+                            if (!__all_sync(kFull, (see & 0xFFFFu) == 0xFFFFu)) {
+#pragma unroll
+                                for (int e = 0; e < 16; ++e)
+                                    if (!((see >> e) & 1u)) r[e] = 0xFF800000u;
+                            }
+                        }
+                        const float2 a2 = make_float2(scale, scale), b2 = make_float2(neg, neg);
+                        float mc = -INFINITY, md = -INFINITY;
+                        float2 part = make_float2(0.f, 0.f);
+#pragma unroll
+                        for (int e = 0; e < 16; e += 4) {
+                            float2 x0 = make_float2(__uint_as_float(r[e]), __uint_as_float(r[e + 1]));
+                            float2 x1 = make_float2(__uint_as_float(r[e + 2]), __uint_as_float(r[e + 3]));
+                            mc = fmaxf(fmaxf(mc, x0.x), x1.x);
+                            md = fmaxf(fmaxf(md, x0.y), x1.y);
+                            x0 = __ffma2_rn(x0, a2, b2);
+                            x1 = __ffma2_rn(x1, a2, b2);
+                            x0 = make_float2(fast_exp2(x0.x), fast_exp2(x0.y));
+                            x1 = make_float2(fast_exp2(x1.x), fast_exp2(x1.y));
+                            part = __fadd2_rn(part, __fadd2_rn(x0, x1));
+                            w[c][e / 2] = f2_to_bf16x2(x0.x, x0.y);
+                            w[c][e / 2 + 1] = f2_to_bf16x2(x1.x, x1.y);
+                        }
+                        mx = fmaxf(mx, fmaxf(mc, md) * scale);
+                        sum = __fadd2_rn(sum, part);
+                    };
+                    const auto pass = [&](auto hide) {
+                        uint32_t ra[16], rb[16];
+                        tmem_ld_start(ra, s_addr);
+#pragma unroll
+                        for (int c = 0; c < 8; c += 2) {
+                            tmem_ld_wait(ra);
+                            tmem_ld_start(rb, s_addr + c * 16 + 16);
+                            chunk(hide, ra, c);
+                            tmem_ld_wait(rb);
+                            if (c < 6) tmem_ld_start(ra, s_addr + c * 16 + 32);
+                            chunk(hide, rb, c + 1);
+                        }
+                    };
+                    if (masked) pass(PromptConst<true>{});
+                    else pass(PromptConst<false>{});
+                    const bool up = mx - m_ref > kPrAhead;  // false while nothing has been seen
+                    if (!__any_sync(kFull, up)) break;
+                    const float f = up ? fast_exp2(m_ref - mx) : 1.f;
+                    if (up) m_ref = mx;
+                    l2.x *= f;
+                    l2.y *= f;
+                    if (jj > 0) {
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 32) {
+                            uint32_t o[32];
+                            tmem_ld(o, o_addr + c);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            tmem_st(o_addr + c, o);
+                        }
+                    }
+                }
+                l2 = __fadd2_rn(l2, sum);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) tmem_st(s_addr + c * 8, w[c]);
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(bar(&bars.p_full[i]));
+            }
+            if (ok) ok = wait(&bars.o_full[i], done);
+            mine += n;
+            ++done;
+            if (!ok) break;
+            // ---- write the row: the warp's 32 rows pass through shared memory, 128 bytes of
+            // each at a time, chunks swizzled by row, and leave as a tensor copy, which
+            // nobody waits for. A sequence's last rows share their box with the next
+            // one's, and leave as stores of whole lines.
+            tc_fence_after();
+            const float l = l2.x + l2.y, f = l > 0.f ? 1.f / l : 0.f;
+            const uint32_t st = stage0 + uint32_t(warp) * 4096u;
+            const uint32_t mine_at = st + uint32_t(lane) * 128u, mine_sw = uint32_t(lane & 7);
+            const int first = im.r_first + warp * 32, rows = min(32, im.r_end - first);
+            for (int c = 0; c < D / 64; ++c) {
+                if (lane == 0) bulk_wait_read();
+                __syncwarp();
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t o[32];
+                    tmem_ld(o, o_addr + c * 64 + h * 32);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        uint32_t x[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            x[k] = f2_to_bf16x2(__uint_as_float(o[8 * e + 2 * k]) * f, __uint_as_float(o[8 * e + 2 * k + 1]) * f);
+                        sts128(mine_at + ((uint32_t(h * 4 + e) ^ mine_sw) << 4), make_uint4(x[0], x[1], x[2], x[3]));
+                    }
+                }
+                if (rows == 32) {
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tma_store_4d(&p.tm_out, st, c * 64, 0, im.kvh, im.row0 + (first >> lgG));
+                        bulk_commit();
+                    }
+                } else {
+                    __syncwarp();
+#pragma unroll 1
+                    for (int r = lane / 8; r < rows; r += 4) {  // four rows at a time
+                        const int rr = first + r, ch = lane % 8;
+                        const uint4 v = lds128(st + uint32_t(r) * 128u + ((uint32_t(ch) ^ uint32_t(r & 7)) << 4));
+                        *reinterpret_cast<uint4*>(p.out + int64_t(im.row0 + (rr >> lgG)) * p.out_stride +
+                                                  (im.kvh * G + (rr & (G - 1))) * D + c * 64 + ch * 8) = v;
+                    }
+                }
+            }
+            tc_fence_before();  // O_i has been read before the next item's P_i is announced
+        }
+        if (lane == 0) {
+            bulk_wait();
+            if (!ok) report(p.err, kErrTimeout);
+        }
+    } else if (warp == kLoadWarp) {
+        // ================= K and V tiles =================
+        const bool leader = elect_one();
+        if (leader) {
+            prefetch_tensormap(&p.tm_k);
+            prefetch_tensormap(&p.tm_v);
+        }
+        __syncwarp();
+        int tiles = 0, fixed = 0, jj = 0, v = 0;  // tiles: of the items before
+        bool fixing = false;
+        for (int q = 0; ok && take(q); release(q++)) {
+            const PromptItem& im = s_item[q & 1];
+            if (im.kind == 1) continue;
+            const KeyTiles kt = im.kt;
+            const int kvh = im.kvh, row0 = im.row0, n = im.n;
+            for (jj = 0; jj < kt.n && ok; ++jj) {
+                const int t0 = kt.tile(jj) * kPrKeys;
+                for (v = 0; v < 2; ++v) {
+                    const int it = 2 * (tiles + jj) + v, s = it % STAGES;
+                    if (it >= STAGES && !(ok = wait(&bars.kv_empty[s], it / STAGES - 1))) break;
+                    // V: rows behind the sequence's end are another's, or nobody's: cleared,
+                    // since their weight of zero would not hide a not-a-number
+                    fixing = v && t0 + kPrKeys > n;
+                    const uint32_t full = fixing ? bar(&bars.fix) : bar(&bars.kv_full[s]);
+                    const uint32_t dst = kv_addr + uint32_t(s) * T::kTileBytes;
+                    if (leader) {
+                        mbar_arrive_expect_tx(full, T::kTileBytes);
+#pragma unroll
+                        for (int h = 0; h < D / 64; ++h)
+                            tma_load_4d(dst + uint32_t(h * T::kSlab), v ? &p.tm_v : &p.tm_k, h * 64, 0, kvh, row0 + t0, full);
+                    }
+                    __syncwarp();
+                    if (fixing) {
+                        if (!(ok = wait(&bars.fix, fixed))) break;
+                        ++fixed;
+                        fixing = false;
+                        for (int e = (n - t0) * (D / 8) + lane; e < kPrKeys * (D / 8); e += 32) {
+                            const int rr = e / (D / 8), ch = e % (D / 8);
+                            sts128(dst + uint32_t((ch / 8) * T::kSlab + rr * 128 + (ch % 8) * 16), make_uint4(0u, 0u, 0u, 0u));
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (leader) mbar_arrive(bar(&bars.kv_full[s]));
+                    }
+                }
+                if (!ok) break;
+            }
+            if (ok) {
+                tiles += kt.n;
+                jj = v = 0;
+            }
+        }
+        if (!ok) {
+            // let the copies in flight land before the CTA ends
+            const int upto = 2 * (tiles + jj) + v;
+            for (int it = max(0, upto - STAGES); it < upto; ++it) (void)wait(&bars.kv_full[it % STAGES], it / STAGES);
+            if (fixing) (void)wait(&bars.fix, fixed);
+            if (lane == 0) report(p.err, kErrTimeout);
+        }
+    } else if (warp == kMmaWarp) {
+        // ================= the multiplies =================
+        // The whole warp walks through the loop, so that addresses and descriptors
+        // stay warp-uniform; one thread issues. A step along K is an addition to a
+        // descriptor's address field (16-byte units).
+        constexpr uint32_t kDescS = mma_desc_bf16(kPrKeys, false), kDescO = mma_desc_bf16(D, true);
+        constexpr uint64_t kTile16 = T::kTileBytes / 16;
+        const bool leader = elect_one();
+        const uint32_t tm = __shfl_sync(kFull, tmem, 0);
+        const uint64_t dq = smem_desc(q_addr, 16), dk = smem_desc(kv_addr, 16), dv = smem_desc(kv_addr, T::kSlab);
+        const auto issue_s = [&](int i, int stage) {
+            if (leader) {
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks) {
+                    constexpr uint64_t kSlab16 = T::kSlab / 16;
+                    const uint64_t off = uint64_t(ks / 4) * kSlab16 + uint64_t(ks % 4) * 2u;
+                    mma_ss(tm + uint32_t(i) * 128u, dq + uint64_t(i) * kTile16 + off, dk + uint64_t(stage) * kTile16 + off,
+                           kDescS, ks > 0);
+                }
+            }
+        };
+        const auto commit = [&](const uint64_t* x) {
+            if (leader) mma_commit(bar(x));
+        };
+        int tiles = 0, mine[2] = {0, 0}, items = 0;
+        for (int q = 0; ok && take(q); release(q++)) {
+            const PromptItem& im = s_item[q & 1];
+            if (im.kind == 1) continue;
+            const int n = im.kt.n;
+            const int nq = im.r_end - im.r_first > kPrRows ? 2 : 1;
+            const int first = 2 * tiles, sf = first % STAGES;
+            ok = wait(&bars.q_full, items) && wait(&bars.kv_full[sf], first / STAGES);
+            if (!ok) break;
+            tc_fence_after();
+            for (int i = 0; i < nq; ++i) {
+                issue_s(i, sf);
+                commit(&bars.s_full[i]);
+            }
+            commit(&bars.kv_empty[sf]);
+            if (n == 1) commit(&bars.q_empty);
+            for (int jj = 0; jj < n && ok; ++jj) {
+                const int iv = 2 * (tiles + jj) + 1, ik = iv + 1, sv = iv % STAGES, sk = ik % STAGES;
+                ok = wait(&bars.kv_full[sv], iv / STAGES);
+                for (int i = 0; i < nq && ok; ++i) {
+                    if (!(ok = wait(&bars.p_full[i], mine[i] + jj))) break;
+                    tc_fence_after();
+                    if (leader) {
+#pragma unroll
+                        for (int ks = 0; ks < kPrKeys / 16; ++ks)
+                            mma_ts(tm + 256u + uint32_t(i) * 128u, tm + uint32_t(i) * 128u + uint32_t(ks) * 8u,
+                                   dv + uint64_t(sv) * kTile16 + uint64_t(ks) * 128u, kDescO, jj > 0 || ks > 0);
+                    }
+                    if (i == nq - 1) commit(&bars.kv_empty[sv]);
+                    if (jj + 1 < n) {
+                        if (i == 0 && !(ok = wait(&bars.kv_full[sk], ik / STAGES))) break;
+                        tc_fence_after();
+                        issue_s(i, sk);
+                        commit(&bars.s_full[i]);
+                        if (i == nq - 1) {
+                            commit(&bars.kv_empty[sk]);
+                            if (jj + 2 == n) commit(&bars.q_empty);  // the last use of Q
+                        }
+                    } else {
+                        commit(&bars.o_full[i]);
+                    }
+                }
+            }
+            tiles += n;
+            mine[0] += n;
+            if (nq == 2) mine[1] += n;
+            ++items;
+        }
+        if (!ok) {
+            commit(&bars.drain);
+            (void)wait(&bars.drain, 0);
+            if (lane == 0) report(p.err, kErrTimeout);
+        }
+    } else if (warp == kPlanWarp) {
+        // ================= items and queries =================
+        const bool leader = elect_one();
+        if (leader) prefetch_tensormap(&p.tm_q);
+        int cx = blockIdx.x;
+        // (row tile, kv head) of all sequences in a list, the row tiles from the last one
+        // on: later rows see more keys. The grid has a CTA for each item that the
+        // host's bounds allow; behind the batch's own they have none, and are asked for
+        // and dropped.
+        const auto range = [&](int s, int32_t* err) {
+            return seq_range(p.bt, s, 1 << 16, err, err != nullptr);
+        };
+        const auto row_tiles = [&](int s) { return int((int64_t(range(s, nullptr).n) * G + p.item_rows - 1) / p.item_rows); };
+        ListCursor<decltype(row_tiles)> list(p.bt.B, row_tiles);
+        const int list_tiles = int(list.total < p.item_tiles ? list.total : p.item_tiles);
+        const int items = list_tiles * p.Hkv;
+        if (cx == 0)
+            for (int b = lane; b < p.bt.B; b += 32) {
+                const SeqRange r = range(b, p.err);
+                if (r.n > 0 && r.ctx != r.n) report(p.err, kErrCtxLen);
+            }
+        int published = 0, loaded = 0, round = 0;
+        // The grid's cx-th CTA's item; false: it has none.
+        const auto describe = [&](PromptItem& x) {
+            if (cx >= items) return false;
+            const WorkItem wi = list.find(list_tiles - 1 - cx / p.Hkv);
+            if (wi.b < 0) return false;
+            const SeqRange sq = range(wi.b, nullptr);
+            x.kind = sq.ctx != sq.n ? 1 : 0;
+            x.kvh = cx % p.Hkv;
+            x.row0 = sq.row0;
+            x.n = sq.n;
+            x.r_first = wi.i * p.item_rows;
+            x.r_end = min(sq.n * G, x.r_first + p.item_rows);
+            x.kt = key_tiles(x.r_first >> lgG, (x.r_end - 1) >> lgG, p.window, p.sinks, kPrKeys);
+            return true;
+        };
+        PromptItem x;
+        for (;; ++round) {
+            if (describe(x)) {
+                const int s = published & 1;
+                if (published >= 2 && !(ok = wait(&bars.item_empty[s], (published >> 1) - 1))) break;
+                if (lane == 0) {
+                    s_item[s] = x;
+                    mbar_arrive(bar(&bars.item_full[s]));
+                }
+                ++published;
+                if (x.kind == 0) {
+                    if (loaded > 0 && !(ok = wait(&bars.q_empty, loaded - 1))) break;
+                    if (leader) {
+                        const int nq = x.r_end - x.r_first > kPrRows ? 2 : 1;
+                        mbar_arrive_expect_tx(bar(&bars.q_full), uint32_t(nq) * T::kTileBytes);
+                        for (int i = 0; i < nq; ++i)
+                            for (int h = 0; h < D / 64; ++h)
+                                tma_load_4d(q_addr + i * T::kTileBytes + h * T::kSlab, &p.tm_q, h * 64, 0, x.kvh,
+                                            x.row0 + ((x.r_first + i * kPrRows) >> lgG), bar(&bars.q_full));
+                    }
+                    __syncwarp();
+                    ++loaded;
+                }
+            }
+            // ask for the CTA that the grid would start next, an item ahead and no more
+            if (leader) {
+                fence_proxy_async_smem();  // the answer before has been read
+                mbar_arrive_expect_tx(bar(&bars.next), 16);
+                next_cta(smem_addr(&s_next), bar(&bars.next));
+            }
+            __syncwarp();
+            // (nobody else will take that CTA's item: its answer is waited for twice as long)
+            if (!(ok = wait(&bars.next, round) || wait(&bars.next, round))) break;
+            const bool more = next_cta_read(smem_addr(&s_next), cx);
+            __syncwarp();
+            if (!more) break;
+        }
+        if (ok) {
+            const int s = published & 1;
+            if (published >= 2) ok = wait(&bars.item_empty[s], (published >> 1) - 1);
+            if (ok && lane == 0) {
+                s_item[s].kind = 2;
+                mbar_arrive(bar(&bars.item_full[s]));
+            }
+        }
+        if (!ok) {
+            // let the copies in flight land before the CTA ends
+            if (loaded > 0) (void)wait(&bars.q_full, loaded - 1);
+            if (lane == 0) report(p.err, kErrTimeout);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+}
+
+}  // namespace pkv

@@ -31,6 +31,7 @@
 // read whole 256-byte rows, and a block's rows meet in one CTA or cluster for its
 // maximum.
 #include <algorithm>
+#include <type_traits>
 
 #include "batch.cuh"
 #include "host.h"
@@ -53,6 +54,15 @@ struct RopeParams {
     int32_t groups;  // CTAs a chunk: neighbours in the grid, as their rows are in memory
     int32_t ragged;
     float scale;
+};
+
+// Positions on several axes (pkv_rope_append_axes): a pair's axis chooses its
+// position, and the turned k can leave as rows too.
+struct RopeAxesParams : RopeParams {
+    int64_t axis_stride, k_out_stride;
+    uint16_t* k_out;
+    int32_t num_axes;
+    uint16_t axes[8];  // two bits for each of a thread's eight pairs, by its place in the row
 };
 
 // 16 elements of a row: two 16-byte chunks, at element offsets lo and hi.
@@ -193,8 +203,9 @@ __device__ __forceinline__ uint2 codes8(const uint4& w, float scale, float inv) 
 constexpr int kRopeTokens = 16;  // of a CTA
 
 // PARTS: CTAs a chunk of kRopeTokens * PARTS tokens, a cluster.
-template <int D, bool INT8, int PARTS>
-__device__ __forceinline__ void rope_append(const RopeParams& p) {
+template <int D, bool INT8, int PARTS, class Params>
+__device__ __forceinline__ void rope_append(const Params& p) {
+    constexpr bool AXES = std::is_same_v<Params, RopeAxesParams>;
     constexpr int CT = kRopeTokens * PARTS;
     constexpr int PR = D / 16;               // chunk pairs a row
     constexpr int THREADS = kRopeTokens * PR, WARPS = THREADS / 32;
@@ -279,8 +290,8 @@ __device__ __forceinline__ void rope_append(const RopeParams& p) {
                 w[kv].a = w[kv].b = make_uint4(0u, 0u, 0u, 0u);
                 if (fresh) {
                     const uint16_t* r = (kv ? p.v + row * p.v_stride : p.k + row * p.k_stride) + h * D;
-                    w[kv].a = ldg128(r + lo);
-                    w[kv].b = ldg128(r + hi);
+                    w[kv].a = AXES && !kv ? ldcg128(r + lo) : ldg128(r + lo);  // (k may be turned in place, too)
+                    w[kv].b = AXES && !kv ? ldcg128(r + hi) : ldg128(r + hi);
                 } else if (full && slot_ok) {  // an earlier token of the block
                     const uint16_t* r = (kv ? p.c.v_tail : p.c.k_tail) + ((size_t(slot) * p.c.Hkv + h) * CT + tl) * D;
                     w[kv].a = ldcg128(r + lo);
@@ -305,12 +316,27 @@ __device__ __forceinline__ void rope_append(const RopeParams& p) {
 
         Angles an;
         if (turns && fresh) {
-            const int pos = p.positions ? p.positions[row] : tok;
+            int pos[AXES ? 4 : 1];
+            uint32_t axes = 0;
+            if constexpr (AXES) {
+                axes = p.axes[pr];
+#pragma unroll
+                for (int a = 0; a < 4; ++a) pos[a] = !p.positions ? tok : a < p.num_axes ? p.positions[a * p.axis_stride + row] : 0;
+            } else {
+                pos[0] = p.positions ? p.positions[row] : tok;
+            }
+            const auto at = [&](int i) {  // position of the thread's pair i
+                int x = pos[0];
+                if constexpr (AXES) {
+                    const uint32_t a = (axes >> (2 * i)) & 3u;
+                    x = a & 2u ? (a & 1u ? pos[3] : pos[2]) : (a & 1u ? pos[1] : pos[0]);
+                }
+                return static_cast<unsigned long long>(static_cast<long long>(x));
+            };
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const unsigned long long at = static_cast<unsigned long long>(static_cast<long long>(pos));
-                sincos_turn(uint32_t(at * s_turns[pr * 8 + 2 * e] >> 32), an.s[e].x, an.c[e].x);
-                sincos_turn(uint32_t(at * s_turns[pr * 8 + 2 * e + 1] >> 32), an.s[e].y, an.c[e].y);
+                sincos_turn(uint32_t(at(2 * e) * s_turns[pr * 8 + 2 * e] >> 32), an.s[e].x, an.c[e].x);
+                sincos_turn(uint32_t(at(2 * e + 1) * s_turns[pr * 8 + 2 * e + 1] >> 32), an.s[e].y, an.c[e].y);
                 an.s[e] = __fmul2_rn(an.s[e], make_float2(p.scale, p.scale));
                 an.c[e] = __fmul2_rn(an.c[e], make_float2(p.scale, p.scale));
             }
@@ -321,16 +347,26 @@ __device__ __forceinline__ void rope_append(const RopeParams& p) {
         }
         if (INT8 && do_kv && !slot_ok && (!full || start > base) && tid == 0) report(p.c.err, kErrSlot);
         const bool write = do_kv && (INT8 && !full ? slot_ok : id >= 0 && (slot_ok || start <= base));
+        bool k_rows = false;  // the turned k leaves as rows, whether it can be cached or not
+        if constexpr (AXES) k_rows = do_kv && p.k_out;
 
         // Neighbouring CTAs (clusters) take the two halves in opposite order: one's
         // arithmetic on K and V beside the other's stream of queries
         for (int turn_of = 0; turn_of < 2; ++turn_of) {
         // ---- K and V rows, a head at a time
-        if (turn_of == (bx & 1) && write) {
-            if (PARTS > 1 && full) cluster_meet();  // every CTA has begun
+        if (turn_of == (bx & 1) && (write || k_rows)) {
+            if (PARTS > 1 && full && write) cluster_meet();  // every CTA has begun
             for (int kvh = kvh0; kvh < kvh1; ++kvh) {
                 if (kvh > kvh0) load_kv(kvh);
                 if (fresh) turn(w[0], an);
+                if constexpr (AXES) {
+                    if (k_rows && fresh) {
+                        uint16_t* to = p.k_out + row * p.k_out_stride + kvh * D;
+                        *reinterpret_cast<uint4*>(to + lo) = w[0].a;
+                        *reinterpret_cast<uint4*>(to + hi) = w[0].b;
+                    }
+                    if (!write) continue;
+                }
                 if (full) {  // (`full` and `write` are the cluster's)
                     float mx[2];
 #pragma unroll
@@ -403,6 +439,10 @@ template <int D, bool INT8>
 __global__ void __launch_bounds__(D, (INT8 ? 768 : 896) / D) rope_append_kernel(const __grid_constant__ RopeParams p) {
     rope_append<D, INT8, 1>(p);
 }
+template <int D, bool INT8>
+__global__ void __launch_bounds__(D, (INT8 ? 768 : 896) / D) rope_axes_kernel(const __grid_constant__ RopeAxesParams p) {
+    rope_append<D, INT8, 1>(p);
+}
 
 // INT8 blocks of 64 tokens: a cluster of four CTAs, which exchange their rows'
 // maxima. (One CTA of 4 D threads took 18.6 us for 128 single tokens and 67.5 us
@@ -413,18 +453,23 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(D, 768 / D)
 rope_append_cluster_kernel(const __grid_constant__ RopeParams p) {
     rope_append<D, true, 4>(p);
 }
+template <int D>
+__global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(D, 768 / D)
+rope_axes_cluster_kernel(const __grid_constant__ RopeAxesParams p) {
+    rope_append<D, true, 4>(p);
+}
 
 __global__ void empty_kernel() {}
 
-}  // namespace pkv
+namespace {
 
-using namespace pkv;
-
-extern "C" int pkv_rope_append(const pkv_cache_desc* c, const pkv_batch_desc* batch, const pkv_rope* rope, const void* q,
-                               int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
-                               void* q_out, int64_t q_out_stride, void* stream) {
-    RopeParams p;
-    int st = check_batch(c, batch, &p.bt, &p.c);
+// Checks a call and fills what the kernels' parameters share, all but the positions
+// on several axes. Without a descriptor nothing turns.
+template <class Desc>
+int rope_params(const pkv_cache_desc* c, const pkv_batch_desc* batch, const Desc* rope, const void* q, int64_t q_stride,
+                const void* k, int64_t k_stride, const void* v, int64_t v_stride, void* q_out, int64_t q_out_stride,
+                RopeParams& p, bool* empty) {
+    const int st = check_batch(c, batch, &p.bt, &p.c);
     if (st != PKV_OK) return st;
     const int d = c->head_dim;
     p.half = 0;
@@ -445,7 +490,8 @@ extern "C" int pkv_rope_append(const pkv_cache_desc* c, const pkv_batch_desc* ba
         p.inv_freq = rope->inv_freq;
         p.positions = rope->positions;
     }
-    if (batch->B == 0 || batch->num_tokens == 0 || batch->max_tokens == 0) return PKV_OK;
+    *empty = batch->B == 0 || batch->num_tokens == 0 || batch->max_tokens == 0;
+    if (*empty) return PKV_OK;
     if (!k || !v || !aligned16(k) || !aligned16(v) || (q && (!q_out || !aligned16(q) || !aligned16(q_out))))
         return PKV_ERR_INVALID;
     const int64_t kv_row = int64_t(c->num_kv_heads) * d, q_row = int64_t(c->num_q_heads) * d;
@@ -460,6 +506,14 @@ extern "C" int pkv_rope_append(const pkv_cache_desc* c, const pkv_batch_desc* ba
     p.k_stride = k_stride;
     p.v_stride = v_stride;
     p.q_out_stride = q_out_stride;
+    return PKV_OK;
+}
+
+// The grid, and how a CTA's kv heads are grouped (see there). The kernels are
+// those of D = 64 and 128: bf16, INT8 with blocks of 16, INT8 with blocks of 64.
+template <class Params>
+int rope_launch(const pkv_cache_desc* c, const pkv_batch_desc* batch, Params& p, void (*const (&fns)[2][3])(Params), void* stream) {
+    const int d = c->head_dim;
     const bool int8 = c->dtype == PKV_DTYPE_INT8;
     const int ct = int8 ? c->block_size : kRopeTokens, parts = ct / kRopeTokens;
     // the most aligned chunks that max_tokens tokens in a row can touch
@@ -481,16 +535,62 @@ extern "C" int pkv_rope_append(const pkv_cache_desc* c, const pkv_batch_desc* ba
     p.groups = (c->num_kv_heads + p.heads - 1) / p.heads;
     if ((gx * p.groups + 1) * parts > 0x7FFFFFFF) return PKV_ERR_INVALID;
     const dim3 grid(unsigned((gx * p.groups + p.ragged) * parts));
-    void (*fn)(RopeParams) = nullptr;
-    if (d == 128)
-        fn = !int8 ? rope_append_kernel<128, false> : parts == 1 ? rope_append_kernel<128, true> : rope_append_cluster_kernel<128>;
-    else
-        fn = !int8 ? rope_append_kernel<64, false> : parts == 1 ? rope_append_kernel<64, true> : rope_append_cluster_kernel<64>;
     auto s = static_cast<cudaStream_t>(stream);
-    if ((st = launch(fn, grid, dim3(unsigned(d)), 0, s, p)) != PKV_OK) return st;
+    const int st = launch(fns[d == 128][!int8 ? 0 : parts == 1 ? 1 : 2], grid, dim3(unsigned(d)), 0, s, p);
+    if (st != PKV_OK) return st;
     if (g_pdl.load(std::memory_order_relaxed) && batch->max_tokens > 1) {
         empty_kernel<<<1, 1, 0, s>>>();
         return cuda_status(cudaGetLastError());
     }
     return PKV_OK;
+}
+
+}  // namespace
+}  // namespace pkv
+
+using namespace pkv;
+
+extern "C" int pkv_rope_append(const pkv_cache_desc* c, const pkv_batch_desc* batch, const pkv_rope* rope, const void* q,
+                               int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                               void* q_out, int64_t q_out_stride, void* stream) {
+    static void (*const fns[2][3])(RopeParams) = {
+        {rope_append_kernel<64, false>, rope_append_kernel<64, true>, rope_append_cluster_kernel<64>},
+        {rope_append_kernel<128, false>, rope_append_kernel<128, true>, rope_append_cluster_kernel<128>}};
+    RopeParams p;
+    bool empty = false;
+    const int st = rope_params(c, batch, rope, q, q_stride, k, k_stride, v, v_stride, q_out, q_out_stride, p, &empty);
+    return st != PKV_OK || empty ? st : rope_launch(c, batch, p, fns, stream);
+}
+
+extern "C" int pkv_rope_append_axes(const pkv_cache_desc* c, const pkv_batch_desc* batch, const pkv_rope_axes* rope,
+                                    const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                                    int64_t v_stride, void* q_out, int64_t q_out_stride, void* k_out,
+                                    int64_t k_out_stride, void* stream) {
+    static void (*const fns[2][3])(RopeAxesParams) = {
+        {rope_axes_kernel<64, false>, rope_axes_kernel<64, true>, rope_axes_cluster_kernel<64>},
+        {rope_axes_kernel<128, false>, rope_axes_kernel<128, true>, rope_axes_cluster_kernel<128>}};
+    RopeAxesParams p;
+    bool empty = false;
+    const int st = rope_params(c, batch, rope, q, q_stride, k, k_stride, v, v_stride, q_out, q_out_stride, p, &empty);
+    if (st != PKV_OK) return st;
+    p.num_axes = 1;
+    p.axis_stride = 0;
+    for (auto& a : p.axes) a = 0;
+    if (rope) {
+        if (rope->num_axes < 1 || rope->num_axes > 4) return PKV_ERR_INVALID;
+        p.num_axes = rope->num_axes;
+        p.axis_stride = rope->axis_stride;
+        for (int j = 0; j < p.half; ++j) {
+            if (rope->pair_axis[j] >= rope->num_axes) return PKV_ERR_INVALID;
+            p.axes[j / 8] = uint16_t(p.axes[j / 8] | (rope->pair_axis[j] << (2 * (j % 8))));
+        }
+        if (rope->positions && rope->num_axes > 1 && rope->axis_stride < batch->num_tokens) return PKV_ERR_INVALID;
+    }
+    if (empty) return PKV_OK;
+    if (k_out && (!aligned16(k_out) || k_out_stride < int64_t(c->num_kv_heads) * c->head_dim || (k_out_stride & 7) ||
+                  (k == k_out && k_stride != k_out_stride)))
+        return PKV_ERR_INVALID;
+    p.k_out = static_cast<uint16_t*>(k_out);
+    p.k_out_stride = k_out_stride;
+    return rope_launch(c, batch, p, fns, stream);
 }

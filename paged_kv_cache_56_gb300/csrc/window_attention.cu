@@ -18,6 +18,73 @@ WindowFn window_tc_fn_d128_bf16(size_t* smem, int* threads);
 WindowFn window_tc_fn_d64_int8(size_t* smem, int* threads);
 WindowFn window_tc_fn_d128_int8(size_t* smem, int* threads);
 
+// Raises a kernel's dynamic shared-memory limit once per kernel and device
+// and returns how many of its CTAs fit on an SM.
+int prepare_kernel(const void* f, size_t smem, int threads, int launch_regs, int* ctas) {
+    struct Entry {
+        const void* fn;
+        int dev;
+        int ctas;
+    };
+    static std::mutex mu;
+    static Entry seen[256];
+    static int n = 0;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return PKV_ERR_CUDA;
+    std::lock_guard<std::mutex> lock(mu);
+    for (int i = 0; i < n; ++i)
+        if (seen[i].fn == f && seen[i].dev == dev) {
+            *ctas = seen[i].ctas;
+            return PKV_OK;
+        }
+    if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) != cudaSuccess ||
+        cudaFuncSetAttribute(f, cudaFuncAttributePreferredSharedMemoryCarveout, int(cudaSharedmemCarveoutMaxShared)) !=
+            cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(ctas, f, threads, smem) != cudaSuccess)
+        return PKV_ERR_CUDA;
+    // the warpgroups of window_tc_kernel and prompt_kernel share out the registers that the block was
+    // launched with, and would wait forever for more than that
+    cudaFuncAttributes at;
+    if (launch_regs > 0 && (cudaFuncGetAttributes(&at, f) != cudaSuccess || at.numRegs != launch_regs))
+        return PKV_ERR_CUDA;
+    if (n < 256) seen[n++] = Entry{f, dev, *ctas};
+    return PKV_OK;
+}
+
+int sm_count(int* out) {
+    static std::atomic<int> known[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return PKV_ERR_CUDA;
+    int n = known[dev].load(std::memory_order_relaxed);
+    if (n == 0) {
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return PKV_ERR_CUDA;
+        known[dev].store(n, std::memory_order_relaxed);
+    }
+    *out = n;
+    return PKV_OK;
+}
+
+int encode_map(CUtensorMapDataType type, int rank, const void* base, const cuuint64_t* dims, const cuuint64_t* strides,
+               const cuuint32_t* box, CUtensorMap* out) {
+    const PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    const cuuint32_t elem[4] = {1, 1, 1, 1};
+    return enc && enc(out, type, rank, const_cast<void*>(base), dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? PKV_OK
+               : PKV_ERR_CUDA;
+}
+
+// Tensor map of q or out for window_tc_kernel and prompt_kernel: [tokens][Hkv][G][d] with boxes of
+// `rows` rows (rows / G tokens x the group) x 64 elements, 128-byte swizzle.
+int rows_tensor_map(int group, int kv_heads, int head_dim, int tokens, const void* base, int64_t stride, int rows, CUtensorMap* out) {
+    const cuuint64_t g = cuuint64_t(group), d = cuuint64_t(head_dim);
+    const cuuint64_t dims[4] = {d, g, cuuint64_t(kv_heads), cuuint64_t(tokens)};
+    const cuuint64_t strides[3] = {d * 2, g * d * 2, cuuint64_t(stride) * 2};
+    const cuuint32_t box[4] = {64, cuuint32_t(g), 1, cuuint32_t(rows / g)};
+    return encode_map(CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims, strides, box, out);
+}
+
 namespace {
 
 constexpr int kMaxSplits = 128;  // the merge holds 16 rows' weights of every split in a CTA's rings
@@ -39,53 +106,6 @@ struct Plan {
     int64_t split_items;  // ... the last ones, that split_tokens > 0 splits
     int ctas_per_sm;
 };
-
-// Raises a kernel's dynamic shared-memory limit once per kernel and device
-// and returns how many of its CTAs fit on an SM.
-int prepare_kernel(WindowFn fn, size_t smem, int threads, int launch_regs, int* ctas) {
-    struct Entry {
-        WindowFn fn;
-        int dev;
-        int ctas;
-    };
-    static std::mutex mu;
-    static Entry seen[256];
-    static int n = 0;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return PKV_ERR_CUDA;
-    std::lock_guard<std::mutex> lock(mu);
-    for (int i = 0; i < n; ++i)
-        if (seen[i].fn == fn && seen[i].dev == dev) {
-            *ctas = seen[i].ctas;
-            return PKV_OK;
-        }
-    const void* f = reinterpret_cast<const void*>(fn);
-    if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) != cudaSuccess ||
-        cudaFuncSetAttribute(f, cudaFuncAttributePreferredSharedMemoryCarveout, int(cudaSharedmemCarveoutMaxShared)) !=
-            cudaSuccess ||
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(ctas, fn, threads, smem) != cudaSuccess)
-        return PKV_ERR_CUDA;
-    // window_tc_kernel's warpgroups share out the registers that the block was
-    // launched with, and would wait forever for more than that
-    cudaFuncAttributes at;
-    if (launch_regs > 0 && (cudaFuncGetAttributes(&at, f) != cudaSuccess || at.numRegs != launch_regs))
-        return PKV_ERR_CUDA;
-    if (n < 256) seen[n++] = Entry{fn, dev, *ctas};
-    return PKV_OK;
-}
-
-int sm_count(int* out) {
-    static std::atomic<int> known[64] = {};
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return PKV_ERR_CUDA;
-    int n = known[dev].load(std::memory_order_relaxed);
-    if (n == 0) {
-        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return PKV_ERR_CUDA;
-        known[dev].store(n, std::memory_order_relaxed);
-    }
-    *out = n;
-    return PKV_OK;
-}
 
 // Most 16-token tiles in the list of keys (in units of `unit` tokens) that
 // `span` tokens in a row see.
@@ -127,7 +147,7 @@ int make_plan(const pkv_cache_desc* c, const pkv_batch_desc* bt, int window, int
         pl->most = std::min(tiles, bt->num_tokens * int64_t(g) / 256 + bt->B) * c->num_kv_heads;
         pl->split_items = pl->n < sms ? pl->most : pl->n % sms;
         pl->key_tiles = most_key_tiles(c, bt, window, sinks, int(std::min<int64_t>(256 / g, bt->max_tokens)), c->block_size);
-        return prepare_kernel(pl->fn, pl->smem, pl->threads, int8 ? kTcLaunchRegsInt8 : kTcLaunchRegsBf16,
+        return prepare_kernel(reinterpret_cast<const void*>(pl->fn), pl->smem, pl->threads, int8 ? kTcLaunchRegsInt8 : kTcLaunchRegsBf16,
                               &pl->ctas_per_sm);
     }
     // up to 8 rows in tiles of 16 (the first of these): 81 / 66 us against 78 / 50 us
@@ -139,7 +159,7 @@ int make_plan(const pkv_cache_desc* c, const pkv_batch_desc* bt, int window, int
     pl->threads = kThreads;
     pl->row_tiles = int((rows + 8 * nt - 1) / (8 * nt));
     pl->key_tiles = most_key_tiles(c, bt, window, sinks, std::max(1, 8 * nt / g), kTile);
-    return prepare_kernel(pl->fn, pl->smem, pl->threads, 0, &pl->ctas_per_sm);
+    return prepare_kernel(reinterpret_cast<const void*>(pl->fn), pl->smem, pl->threads, 0, &pl->ctas_per_sm);
 }
 
 int max_splits_of(const pkv_cache_desc* c, const pkv_batch_desc* bt, const Plan& pl, int split_tokens) {
@@ -170,27 +190,6 @@ int check_window(const pkv_cache_desc* c, const pkv_batch_desc* batch, int windo
     if (st != PKV_OK) return st;
     if (window < 0 || sinks < 0 || split_tokens < 0 || split_tokens % kTile) return PKV_ERR_INVALID;
     return PKV_OK;
-}
-
-int encode_map(CUtensorMapDataType type, int rank, const void* base, const cuuint64_t* dims, const cuuint64_t* strides,
-               const cuuint32_t* box, CUtensorMap* out) {
-    const PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
-    const cuuint32_t elem[4] = {1, 1, 1, 1};
-    return enc && enc(out, type, rank, const_cast<void*>(base), dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
-               ? PKV_OK
-               : PKV_ERR_CUDA;
-}
-
-// Tensor map of q or out for window_tc_kernel: [tokens][Hkv][G][d] with boxes of
-// `rows` rows (rows / G tokens x the group) x 64 elements, 128-byte swizzle.
-int rows_tensor_map(const pkv_cache_desc* c, int tokens, const void* base, int64_t stride, int rows, CUtensorMap* out) {
-    const cuuint64_t g = cuuint64_t(c->num_q_heads / c->num_kv_heads), d = cuuint64_t(c->head_dim);
-    const cuuint64_t dims[4] = {d, g, cuuint64_t(c->num_kv_heads), cuuint64_t(tokens)};
-    const cuuint64_t strides[3] = {d * 2, g * d * 2, cuuint64_t(stride) * 2};
-    const cuuint32_t box[4] = {64, cuuint32_t(g), 1, cuuint32_t(rows / g)};
-    return encode_map(CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims, strides, box, out);
 }
 
 // ... of the partial outputs: [rows][splits][d] fp32, boxes of 32 rows x 32 elements.
@@ -299,8 +298,8 @@ int pkv_window_attention(const pkv_cache_desc* c, const pkv_batch_desc* batch, c
             if ((st = pool_tensor_map(c->k_pool, c->num_blocks, rows, row_bytes, &p.tm_k, c->block_size)) != PKV_OK) return st;
             if ((st = pool_tensor_map(c->v_pool, c->num_blocks, rows, row_bytes, &p.tm_v, c->block_size)) != PKV_OK) return st;
         }
-        if ((st = rows_tensor_map(c, batch->num_tokens, q, q_stride, 128, &p.tm_q)) != PKV_OK) return st;
-        if ((st = rows_tensor_map(c, batch->num_tokens, out, out_stride, 32, &p.tm_out)) != PKV_OK) return st;
+        if ((st = rows_tensor_map(c->num_q_heads / c->num_kv_heads, c->num_kv_heads, c->head_dim, batch->num_tokens, q, q_stride, 128, &p.tm_q)) != PKV_OK) return st;
+        if ((st = rows_tensor_map(c->num_q_heads / c->num_kv_heads, c->num_kv_heads, c->head_dim, batch->num_tokens, out, out_stride, 32, &p.tm_out)) != PKV_OK) return st;
     } else if (row_bytes >= 128) {
         const int32_t rows = c->num_kv_heads * c->block_size;
         if ((st = pool_tensor_map(c->k_pool, c->num_blocks, rows, row_bytes, &p.tm_k)) != PKV_OK) return st;

@@ -36,6 +36,8 @@ PKV_DEVERR_CTX_LEN = 4
 PKV_DEVERR_OFFSET = 8
 PKV_DEVERR_TIMEOUT = 16
 PKV_DEVERR_BATCH = 32
+PKV_DEVERR_OOM = 64
+PKV_DEVERR_SEGMENT = 128
 
 PKV_OUT_BF16 = 0
 PKV_OUT_FP32 = 1
@@ -57,7 +59,8 @@ EXPORTED = (
     "pkv_decode_attention_static_ws", "pkv_set_programmatic_launch", "pkv_decode_step", "pkv_decode_layers",
     "pkv_fork", "pkv_cow_block", "pkv_block_refs", "pkv_copy_blocks", "pkv_copy_slots",
     "pkv_debug_skip_copy", "pkv_sync_status", "pkv_rope_append", "pkv_window_attention",
-    "pkv_window_split_tokens", "pkv_window_ws_bytes", "pkv_gather_kv",
+    "pkv_window_split_tokens", "pkv_window_ws_bytes", "pkv_gather_kv", "pkv_plan_batch", "pkv_commit_batch",
+    "pkv_release_batch", "pkv_axis_positions", "pkv_rope_append_axes", "pkv_prompt_attention",
 )
 
 
@@ -93,6 +96,35 @@ class RopeDesc(ctypes.Structure):
     _fields_ = [
         ("inv_freq", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("rotary_dim", ctypes.c_int32),
         ("interleaved", ctypes.c_int32), ("scale", ctypes.c_float),
+    ]
+
+
+class SeqPool(ctypes.Structure):
+    """Mirror of ``pkv_seq_pool``; ``make_seq_pool`` fills one from checked tensors."""
+    _fields_ = [
+        ("tables", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("held", ctypes.c_void_p), ("ring", ctypes.c_void_p),
+        ("state", ctypes.c_void_p), ("err_word", ctypes.c_void_p), ("max_slots", ctypes.c_int32),
+        ("max_blocks", ctypes.c_int32), ("num_blocks", ctypes.c_int32), ("block_size", ctypes.c_int32),
+        ("int8", ctypes.c_int32),
+    ]
+
+
+class PlanDesc(ctypes.Structure):
+    """Mirror of ``pkv_plan``; ``make_plan`` fills one from checked tensors."""
+    _fields_ = [
+        ("token_starts", ctypes.c_void_p), ("block_tables", ctypes.c_void_p), ("ctx_lens", ctypes.c_void_p),
+        ("fill_blocks", ctypes.c_void_p), ("block_ids", ctypes.c_void_p), ("offsets", ctypes.c_void_p),
+        ("token_slots", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("num_tokens", ctypes.c_int32),
+        ("max_tokens", ctypes.c_int32),
+    ]
+
+
+class RopeAxesDesc(ctypes.Structure):
+    """Mirror of ``pkv_rope_axes``; ``make_rope_axes`` fills one from checked tensors."""
+    _fields_ = [
+        ("inv_freq", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("axis_stride", ctypes.c_int64),
+        ("num_axes", ctypes.c_int32), ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+        ("scale", ctypes.c_float), ("pair_axis", ctypes.c_uint8 * 64),
     ]
 
 
@@ -150,6 +182,14 @@ def lib() -> ctypes.CDLL:
             "pkv_window_split_tokens": (ctypes.c_int, [_VP, _VP, _I32, _I32]),
             "pkv_window_ws_bytes": (ctypes.c_size_t, [_VP, _VP, _I32, _I32, _I32]),
             "pkv_gather_kv": (ctypes.c_int, [_VP, _VP, _VP, _VP, _VP, _I64, _I32, _VP]),
+            "pkv_plan_batch": (ctypes.c_int, [_VP, _VP, _VP, _I32, _VP, _VP]),
+            "pkv_commit_batch": (ctypes.c_int, [_VP, _VP, _VP, _I32, _VP, _VP]),
+            "pkv_release_batch": (ctypes.c_int, [_VP, _VP, _I32, _VP]),
+            "pkv_axis_positions": (ctypes.c_int, [_VP, _VP, _VP, _I32, _I32, _VP, _VP, _I64, _VP, _VP]),
+            "pkv_rope_append_axes": (ctypes.c_int, [_VP, _VP, _VP, _VP, _I64, _VP, _I64, _VP, _I64, _VP, _I64, _VP, _I64,
+                                                    _VP]),
+            "pkv_prompt_attention": (ctypes.c_int, [_VP, _VP, _VP, _I64, _VP, _I64, _VP, _I64, _I32, _I32, ctypes.c_float,
+                                                    _VP, _I64, _VP]),
             "pkv_splitk_ws_o_bytes": (ctypes.c_size_t, [_I32, _I32, _I32, _I32]),
             "pkv_splitk_ws_ml_bytes": (ctypes.c_size_t, [_I32, _I32, _I32]),
         }
@@ -640,6 +680,176 @@ def pkv_gather_kv(desc: CacheDesc, batch: BatchDesc, k_out: torch.Tensor, v_out:
     _check("pkv_gather_kv",
            lib().pkv_gather_kv(ctypes.byref(desc), ctypes.byref(batch), _opt_dev(first, "first", torch.int32, batch.B),
                                kp, vp, ks, kind, _batch_stream(batch, stream)))
+
+
+# ---------------------------------------------------------------------------
+# Batches planned on the GPU
+# ---------------------------------------------------------------------------
+
+def make_seq_pool(tables: torch.Tensor, lens: torch.Tensor, held: torch.Tensor, ring: torch.Tensor, state: torch.Tensor, *,
+                  block_size: int, int8: bool = False, err=None) -> SeqPool:
+    """Sequence slots' block lists and free blocks on the GPU (``pkv_seq_pool``):
+    tables [max_slots, max_blocks], lens and held [max_slots], ring
+    [num_blocks] and state [4] (place of the first free id in the ring, free ids, 0, 0)
+    are int32 CUDA tensors, kept alive by the descriptor; err an int32 error word."""
+    if tables.dim() != 2:
+        raise ValueError(f"tables must be [max_slots, max_blocks], got {tuple(tables.shape)}")
+    keep = [tables, lens, held, ring, state, err]
+    if len({t.device for t in keep if t is not None}) != 1:
+        raise ValueError("the pool's tensors must be on one device")
+    slots, width = tables.shape
+    d = SeqPool(_dev(tables, "tables", torch.int32), _dev(lens, "lens", torch.int32, slots),
+                _dev(held, "held", torch.int32, slots), _dev(ring, "ring", torch.int32),
+                _dev(state, "state", torch.int32, 4), _opt_dev(err, "err", torch.int32, 1), slots, width, ring.numel(),
+                block_size, 1 if int8 else 0)
+    d.keep, d.device = keep, tables.device
+    return d
+
+
+def make_plan(token_starts: torch.Tensor, block_tables: torch.Tensor, ctx_lens: torch.Tensor, *, num_tokens: int,
+              max_tokens: int, fill_blocks=None, block_ids=None, offsets=None, token_slots=None, positions=None) -> PlanDesc:
+    """Where ``pkv_plan_batch`` puts a batch of B = ctx_lens.numel() entries
+    (``pkv_plan``): token_starts [B+1], block_tables [B, max_blocks], ctx_lens
+    [B], and where wanted fill_blocks [B] and block_ids, offsets, token_slots, positions
+    [num_tokens]; int32 CUDA tensors, kept alive by the descriptor."""
+    B = ctx_lens.numel()
+    if block_tables.dim() != 2 or block_tables.shape[0] < B:
+        raise ValueError(f"block_tables must be [{B}, max_blocks], got {tuple(block_tables.shape)}")
+    keep = [token_starts, block_tables, ctx_lens, fill_blocks, block_ids, offsets, token_slots, positions]
+    if len({t.device for t in keep if t is not None}) != 1:
+        raise ValueError("the plan's tensors must be on one device")
+    i32 = torch.int32
+    d = PlanDesc(_dev(token_starts, "token_starts", i32, B + 1), _dev(block_tables, "block_tables", i32),
+                 _dev(ctx_lens, "ctx_lens", i32, B), _opt_dev(fill_blocks, "fill_blocks", i32, B),
+                 _opt_dev(block_ids, "block_ids", i32, num_tokens), _opt_dev(offsets, "offsets", i32, num_tokens),
+                 _opt_dev(token_slots, "token_slots", i32, num_tokens), _opt_dev(positions, "positions", i32, num_tokens),
+                 num_tokens, max_tokens)
+    d.keep, d.device, d.B, d.width = keep, ctx_lens.device, B, block_tables.shape[1]
+    return d
+
+
+def _pool_ids(pool: SeqPool, t, name: str, n: int, plan=None):
+    """Pointer of an int32 [n] tensor on the pool's device (None: NULL)."""
+    if t is None:
+        return None
+    if t.device != pool.device or (plan is not None and plan.device != pool.device):
+        raise ValueError(f"{name} and the plan must be on {pool.device}")
+    return _dev(t, name, torch.int32, n)
+
+
+def pkv_plan_batch(pool: SeqPool, slots: torch.Tensor, plan: PlanDesc, counts=None, stream=None) -> None:
+    """Plans counts[b] new tokens (None: one each) of the sequences in slots[b]
+    (-1: none): blocks off the pool's ring, tables, lengths and slot maps into ``plan``."""
+    B = slots.numel()
+    if B != plan.B or (plan.width != pool.max_blocks and B):
+        raise ValueError(f"the plan is for {plan.B} entries of {plan.width} blocks, not {B} of {pool.max_blocks}")
+    _check("pkv_plan_batch",
+           lib().pkv_plan_batch(ctypes.byref(pool), _pool_ids(pool, slots, "slots", B, plan),
+                                _pool_ids(pool, counts, "counts", B), B, ctypes.byref(plan), _batch_stream(pool, stream)))
+
+
+def pkv_commit_batch(pool: SeqPool, slots: torch.Tensor, plan: PlanDesc, accepted=None, stream=None) -> None:
+    """Keeps the first accepted[b] (None: all) of the tokens that the plan's entries brought."""
+    B = slots.numel()
+    if B != plan.B:
+        raise ValueError(f"the plan is for {plan.B} entries, not {B}")
+    _check("pkv_commit_batch",
+           lib().pkv_commit_batch(ctypes.byref(pool), _pool_ids(pool, slots, "slots", B, plan),
+                                  _pool_ids(pool, accepted, "accepted", B), B, ctypes.byref(plan),
+                                  _batch_stream(pool, stream)))
+
+
+def pkv_release_batch(pool: SeqPool, slots: torch.Tensor, stream=None) -> None:
+    """Gives the blocks of the sequences in slots[b] (-1: none) back to the ring and frees the slots."""
+    B = slots.numel()
+    _check("pkv_release_batch", lib().pkv_release_batch(ctypes.byref(pool), _pool_ids(pool, slots, "slots", B), B,
+                                                        _batch_stream(pool, stream)))
+
+
+# ---------------------------------------------------------------------------
+# Prompts with images and video
+# ---------------------------------------------------------------------------
+
+def pkv_axis_positions(batch: BatchDesc, segments: torch.Tensor, num_segments: torch.Tensor, positions: torch.Tensor,
+                       rows=None, err=None, stream=None) -> None:
+    """Rotary positions (time, height, width) of the batch's tokens into positions
+    [3, >= num_tokens] (int32). segments [R, S, 4]: {t, h, w, step} of each segment
+    of a sequence, h = w = 0 for t tokens of text; num_segments [R]; rows [B]: the
+    sequences' rows of both (None: in the batch's order)."""
+    if segments.dim() != 3 or segments.shape[2] != 4:
+        raise ValueError(f"segments must be [rows, max_segments, 4], got {tuple(segments.shape)}")
+    if any(t is not None and t.device != batch.device for t in (segments, num_segments, positions, rows, err)):
+        raise ValueError(f"all tensors must be on {batch.device}")
+    if positions.dim() != 2 or positions.shape[0] != 3 or positions.dtype != torch.int32 or (
+            positions.stride(1) != 1 and positions.shape[1] > 1) or positions.shape[1] < batch.num_tokens:
+        raise ValueError(f"positions must be int32 [3, {batch.num_tokens}] with contiguous rows")
+    R, S = segments.shape[:2]
+    _check("pkv_axis_positions",
+           lib().pkv_axis_positions(ctypes.byref(batch), _dev(segments, "segments", torch.int32),
+                                    _dev(num_segments, "num_segments", torch.int32, R), R, S,
+                                    _opt_dev(rows, "rows", torch.int32, batch.B), positions.data_ptr(), positions.stride(0),
+                                    _opt_dev(err, "err", torch.int32, 1), _batch_stream(batch, stream)))
+
+
+def make_rope_axes(inv_freq: torch.Tensor, pair_axis, *, positions=None, interleaved: bool = False,
+                   scale: float = 1.0) -> RopeAxesDesc:
+    """Rotary descriptor with several axes (``pkv_rope_axes``): inv_freq fp64 CUDA
+    tensor [rotary_dim / 2]; pair_axis: each pair's axis; positions: int32 CUDA tensor
+    [axes, num_tokens] with contiguous rows, or None (each token's index in its
+    context, on every axis)."""
+    pair_axis = [int(a) for a in pair_axis]
+    if len(pair_axis) != inv_freq.numel() or len(pair_axis) > 64 or any(a < 0 for a in pair_axis):
+        raise ValueError("pair_axis needs one axis for each of inv_freq's pairs, 64 at most")
+    axes = max(pair_axis, default=0) + 1
+    ptr, stride = None, 0
+    if positions is not None:
+        if positions.device != inv_freq.device or positions.device.type != "cuda":
+            raise ValueError("inv_freq and positions must be on one CUDA device")
+        if positions.dim() != 2 or positions.dtype != torch.int32 or (positions.stride(1) != 1 and positions.shape[1] > 1):
+            raise ValueError("positions must be int32 [axes, num_tokens] with contiguous rows")
+        if positions.shape[0] < axes:
+            raise ValueError(f"pair_axis names {axes} axes, positions have {positions.shape[0]}")
+        ptr, stride = positions.data_ptr(), positions.stride(0)
+    d = RopeAxesDesc(_dev(inv_freq, "inv_freq", torch.float64), ptr, stride, axes, 2 * inv_freq.numel(),
+                     1 if interleaved else 0, scale, (ctypes.c_uint8 * 64)(*pair_axis))
+    d.keep, d.num_positions = (inv_freq, positions), None if positions is None else positions.shape[1]
+    d.device = inv_freq.device
+    return d
+
+
+def pkv_rope_append_axes(desc: CacheDesc, batch: BatchDesc, rope, q, k: torch.Tensor, v: torch.Tensor, q_out=None,
+                         k_out=None, stream=None) -> None:
+    """``pkv_rope_append`` with a rotary descriptor from make_rope_axes (or None).
+    k_out [T, Hkv, d]: the turned k as rows, too (k itself: in place)."""
+    hq, hkv, d = desc.num_q_heads, desc.num_kv_heads, desc.head_dim
+    qp, qs = (None, 0) if q is None else _rows(q, "q", batch, hq, d)
+    op, os_ = (qp, qs) if q is None or q_out is None else _rows(q_out, "q_out", batch, hq, d)
+    kp, ks = _rows(k, "k", batch, hkv, d)
+    vp, vs = _rows(v, "v", batch, hkv, d)
+    kop, kos = (None, 0) if k_out is None else _rows(k_out, "k_out", batch, hkv, d)
+    if rope is not None:
+        if rope.device != batch.device:
+            raise ValueError(f"rope must be on {batch.device}")
+        if rope.num_positions is not None and rope.num_positions < batch.num_tokens:
+            raise ValueError(f"positions hold {rope.num_positions} entries, need {batch.num_tokens}")
+    _check("pkv_rope_append_axes",
+           lib().pkv_rope_append_axes(ctypes.byref(desc), ctypes.byref(batch), None if rope is None else ctypes.byref(rope),
+                                      qp, qs, kp, ks, vp, vs, op, os_, kop, kos, _batch_stream(batch, stream)))
+
+
+def pkv_prompt_attention(desc: CacheDesc, batch: BatchDesc, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                         out: torch.Tensor, window: int, sinks: int, sm_scale: float, stream=None) -> None:
+    """Causal attention of whole prompts (ctx_lens[b] == the rows of sequence b) from
+    their rows q [T, Hq, d], k and v [T, Hkv, d] into out, each row seeing the last
+    `window` rows of its sequence (0: all) and the first `sinks`."""
+    hq, hkv, d = desc.num_q_heads, desc.num_kv_heads, desc.head_dim
+    qp, qs = _rows(q, "q", batch, hq, d)
+    kp, ks = _rows(k, "k", batch, hkv, d)
+    vp, vs = _rows(v, "v", batch, hkv, d)
+    op, os_ = _rows(out, "out", batch, hq, d)
+    _check("pkv_prompt_attention",
+           lib().pkv_prompt_attention(ctypes.byref(desc), ctypes.byref(batch), qp, qs, kp, ks, vp, vs, window, sinks,
+                                      sm_scale, op, os_, _batch_stream(batch, stream)))
 
 
 def pkv_sync_status(descs, stream=None, raise_on_error: bool = True) -> int:
