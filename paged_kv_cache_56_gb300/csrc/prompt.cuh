@@ -48,7 +48,7 @@ struct PromptParams {
     CUtensorMap tm_q;    // q as [tokens][Hkv][G][D], boxes of 128 rows x 64 elements
     CUtensorMap tm_k;    // k as [tokens][Hkv][1][D], boxes of 64 rows x 64 elements
     CUtensorMap tm_v;    // v likewise, boxes of 128 rows x D / 2 elements
-    CUtensorMap tm_out;  // out as q, boxes of 32 rows x D / 2 elements
+    CUtensorMap tm_out;  // out as q, boxes of 32 rows x 64 elements
     BatchView bt;
     uint16_t* out;
     int64_t out_stride;
@@ -85,8 +85,10 @@ struct PromptBars {
     uint64_t o_full;                 // O is complete
     uint64_t item_full[2];           // an item's description is there
     uint64_t item_empty[2];          // 0: every warp of both CTAs has taken it
-    uint64_t pair[4];                // warps w and w + 4 meet
-    uint64_t settled[4][2];          // their tiles' references are settled (tiles in turn)
+    uint64_t settled[4][4];          // warps w, w + 4: a tile's references are settled (tiles in turn)
+    uint64_t sum_there[4];           // ... the sums of the one are there for the other
+    uint64_t o_read[4];              // ... O has been read
+    uint64_t mail[2];                // (second CTA) an item's description has come
     uint64_t next;                   // 0: the answer about the next item is there
     uint64_t drain[2];
 };
@@ -103,24 +105,11 @@ struct alignas(16) PromptShared {
     PromptBars<STAGES> bars;
     PromptItem item[2];
     uint4 next;
-    float ref[kPrRows];     // the rows' references, as the last tile that raised them left them
-    float sum[2][kPrRows];  // the rows' sums of either warp's tiles
-    int raised[4];          // that tile, of each 32 rows
+    float ref[2][kPrRows];  // the rows' references, as the last tile that raised them left them (items in turn)
+    int raised[2][4];       // that tile, of each 32 rows
+    float2 sum[kPrRows];    // the rows' sums over the tiles of the warp that has not the item's last one, and their reference
     uint32_t tmem;
 };
-
-// f(0), f(1), ... f(N - 1) with the argument a constant.
-template <int V>
-struct PromptIndex {
-    static constexpr int value = V;
-};
-template <int N, int I = 0, class F>
-__device__ __forceinline__ void prompt_each(const F& f) {
-    if constexpr (I < N) {
-        f(PromptIndex<I>{});
-        prompt_each<N, I + 1>(f);
-    }
-}
 
 template <bool V>
 struct PromptConst {
@@ -169,6 +158,7 @@ prompt_kernel(const __grid_constant__ PromptParams p) {
             mbar_init(bar(&bars.item_full[i]), 1);
             mbar_init(bar(&bars.item_empty[i]), 2 * (8 + 1) + 2);
             mbar_init(bar(&bars.drain[i]), 1);
+            mbar_init(bar(&bars.mail[i]), 1);
         }
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(bar(&bars.k_full[s]), 2);
@@ -182,9 +172,10 @@ prompt_kernel(const __grid_constant__ PromptParams p) {
             mbar_init(bar(&bars.p_full[i]), 8);
         }
         for (int i = 0; i < 4; ++i) {
-            mbar_init(bar(&bars.pair[i]), 2);
-            sh.raised[i] = -1;
-            for (int t = 0; t < 2; ++t) mbar_init(bar(&bars.settled[i][t]), 1);
+            for (int t = 0; t < 4; ++t) mbar_init(bar(&bars.settled[i][t]), 1);
+            mbar_init(bar(&bars.sum_there[i]), 1);
+            mbar_init(bar(&bars.o_read[i]), 1);
+            sh.raised[0][i] = sh.raised[1][i] = -1;
         }
         mbar_init(bar(&bars.fix), 1);
         mbar_init(bar(&bars.o_full), 1);
@@ -204,16 +195,13 @@ prompt_kernel(const __grid_constant__ PromptParams p) {
     const auto wait = [&](const uint64_t* x, uint32_t parity) {
         return __all_sync(kFull, wait_phase(bar(x), parity & 1u)) != 0;
     };
-    const auto wait_both = [&](const uint64_t* x, uint32_t parity) {  // arrivals from both CTAs
-        return __all_sync(kFull, wait_phase_cluster(bar(x), parity & 1u)) != 0;
-    };
     pdl_wait();
     pdl_launch_dependents();
 
     bool ok = true;
     // The q-th item of this pair (every warp but the planner's): false at the end.
     const auto take = [&](int q) {
-        ok = wait_both(&bars.item_full[q & 1], q >> 1);
+        ok = wait(&bars.item_full[q & 1], q >> 1);
         return ok && sh.item[q & 1].kind != 2;
     };
     // Its description is no longer needed.
@@ -230,12 +218,8 @@ prompt_kernel(const __grid_constant__ PromptParams p) {
         const int quad = warp & 3, team = warp >> 2, mine = quad * 32 + lane;
         const uint32_t lane_base = uint32_t(quad * 32) << 16, o_addr = tmem + lane_base;
         const float scale = p.qscale;
-        int g = 0, items = 0, meets = 0;  // tiles and items so far; meetings of the two warps
-        const auto meet = [&]() {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(&bars.pair[quad]));
-            return wait(&bars.pair[quad], meets++);
-        };
+        int g = 0, items = 0, full = 0;  // tiles and items so far; items that have rows of this warp
+        bool unread = false;             // the other warp may still be reading O of the last one
         for (int q = 0; take(q); release(q++)) {
             const PromptItem& im = sh.item[q & 1];
             const int first = im.r_first + int(rank) * kPrRows + quad * 32;  // of this warp
@@ -255,16 +239,18 @@ prompt_kernel(const __grid_constant__ PromptParams p) {
             const int pf = first >> lgG, pl = (first + rows - 1) >> lgG;  // the warp's first and last position
             float m_ref = have ? -INFINITY : INFINITY;  // reference of the exponent (base 2); no row: weights of 0
             float2 l2 = make_float2(0.f, 0.f);          // sum of this thread's tiles
+            float* const ref = sh.ref[items & 1];
+            volatile int* const raised = &sh.raised[items & 1][quad];
             // Tile g's reference is settled: the other warp's next tile may be weighed against it.
             const auto settle = [&](int tile) {
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(&bars.settled[quad][tile & 1]));
+                if (lane == 0) mbar_arrive(bar(&bars.settled[quad][tile & 3]));
             };
             // The reference that the tile before left (`raised` by the other warp).
             const auto follow = [&](int tile) {
-                if (!(ok = wait(&bars.settled[quad][tile & 1], tile >> 1))) return false;
-                if (*reinterpret_cast<volatile int*>(&sh.raised[quad]) != tile) return false;
-                const float to = sh.ref[mine], f = to > m_ref ? fast_exp2(m_ref - to) : 1.f;
+                if (!(ok = wait(&bars.settled[quad][tile & 3], tile >> 2))) return false;
+                if (*raised != tile) return false;
+                const float to = ref[mine], f = to > m_ref ? fast_exp2(m_ref - to) : 1.f;
                 m_ref = to;
                 l2.x *= f;
                 l2.y *= f;
@@ -279,182 +265,214 @@ prompt_kernel(const __grid_constant__ PromptParams p) {
                     const uint32_t s_addr = tm_s + uint32_t(b) * 128u + lane_base;
                     const int t0 = kt.tile(jj) * kPrKeys;
                     const bool masked = jj < kt.nsink || t0 + kPrKeys - 1 > pf || t0 < pl - p.window + 1;
-                    uint32_t w[2][32];
-                    float2 sum;
-                    // f(chunk's scores, chunk) for the tile's chunks of 16 columns, one's load in
-                    // flight while the other is worked on; hidden scores are -infinity
-                    const auto chunks = [&](auto hide, auto f) {
-                        const auto chunk = [&](uint32_t (&r)[16], auto c) {
-                            if constexpr (hide.value) {
-                                const int tc = t0 + c.value * 16;
-                                // bit e: this row sees token tc + e
-                                const auto below = [](int x) { return (1u << min(16, max(0, x))) - 1u; };
-                                const uint32_t see = below(hi - tc + 1) & (below(p.sinks - tc) | ~below(lo - tc));
-                                const bool none = __all_sync(kFull, (see & 0xFFFFu) == 0u);
-                                if (!none && !__all_sync(kFull, (see & 0xFFFFu) == 0xFFFFu)) {
+                    // Hidden ones of 16 scores from column c on become -infinity; true: all 32 rows' are hidden.
+                    const auto hide = [&](uint32_t (&r)[16], int c) {
+                        const int tc = t0 + c;
+                        // bit e: this row sees token tc + e
+                        const auto below = [](int x) { return (1u << min(16, max(0, x))) - 1u; };
+                        const uint32_t see = below(hi - tc + 1) & (below(p.sinks - tc) | ~below(lo - tc));
+                        if (__all_sync(kFull, (see & 0xFFFFu) == 0u)) return true;
+                        if (!__all_sync(kFull, (see & 0xFFFFu) == 0xFFFFu)) {
 #pragma unroll
-                                    for (int e = 0; e < 16; ++e)
-                                        if (!((see >> e) & 1u)) r[e] = 0xFF800000u;
+                            for (int e = 0; e < 16; ++e)
+                                if (!((see >> e) & 1u)) r[e] = 0xFF800000u;
+                        }
+                        return false;
+                    };
+                    // 16 scores to weights and their sum.
+                    const auto weights = [&](const uint32_t (&r)[16], uint32_t* to, float neg) {
+                        const float2 a2 = make_float2(scale, scale), b2 = make_float2(neg, neg);
+                        float2 part = make_float2(0.f, 0.f);
+#pragma unroll
+                        for (int e = 0; e < 16; e += 4) {
+                            float2 x0 = make_float2(__uint_as_float(r[e]), __uint_as_float(r[e + 1]));
+                            float2 x1 = make_float2(__uint_as_float(r[e + 2]), __uint_as_float(r[e + 3]));
+                            x0 = __ffma2_rn(x0, a2, b2);
+                            x1 = __ffma2_rn(x1, a2, b2);
+                            x0 = make_float2(fast_exp2(x0.x), fast_exp2(x0.y));
+                            x1 = make_float2(fast_exp2(x1.x), fast_exp2(x1.y));
+                            part = __fadd2_rn(part, __fadd2_rn(x0, x1));
+                            to[e / 2] = f2_to_bf16x2(x0.x, x0.y);
+                            to[e / 2 + 1] = f2_to_bf16x2(x1.x, x1.y);
+                        }
+                        return part;
+                    };
+                    float2 sum = make_float2(0.f, 0.f);
+                    // Weighed ahead of the tile before, against the reference as it is known; again where
+                    // that tile, or this one's sum, asks for another one.
+                    bool anew = jj == 0, ahead = true;
+                    if (jj > 0 && __any_sync(kFull, m_ref == -INFINITY)) {  // (not without any)
+                        (void)follow(g - 1);
+                        anew = __any_sync(kFull, m_ref == -INFINITY);
+                        ahead = false;
+                    }
+                    if (!ok) break;
+                    if (!anew) {
+                        // 16 columns at a time, one chunk's load in flight while the other is worked on
+                        uint32_t w[2][32];
+                        const auto weigh = [&](auto hidden) {
+                            const float neg = -m_ref - kPrShift;
+                            const auto chunk = [&](uint32_t (&r)[16], uint32_t* to, int c) {
+                                if constexpr (hidden.value) {
+                                    if (hide(r, c)) {
+#pragma unroll
+                                        for (int e = 0; e < 8; ++e) to[e] = 0u;
+                                        return;
+                                    }
                                 }
-                                f(r, c, none);
-                            } else {
-                                f(r, c, false);
+                                sum = __fadd2_rn(sum, weights(r, to, neg));
+                            };
+                            uint32_t ra[16], rb[16];
+                            tmem_ld_start(ra, s_addr);
+#pragma unroll
+                            for (int c = 0; c < 128; c += 32) {
+                                tmem_ld_wait(ra);
+                                tmem_ld_start(rb, s_addr + uint32_t(c + 16));
+                                chunk(ra, w[c / 64] + c % 64 / 2, c);
+                                tmem_ld_wait(rb);
+                                if (c < 96) tmem_ld_start(ra, s_addr + uint32_t(c + 32));
+                                chunk(rb, w[c / 64] + c % 64 / 2 + 8, c + 16);
                             }
                         };
-                        uint32_t ra[16], rb[16];
-                        tmem_ld_start(ra, s_addr);
-                        prompt_each<4>([&](auto h) {
-                            tmem_ld_wait(ra);
-                            tmem_ld_start(rb, s_addr + uint32_t(h.value * 32 + 16));
-                            chunk(ra, PromptIndex<2 * h.value>{});
-                            tmem_ld_wait(rb);
-                            if constexpr (h.value < 3) tmem_ld_start(ra, s_addr + uint32_t(h.value * 32 + 32));
-                            chunk(rb, PromptIndex<2 * h.value + 1>{});
-                        });
-                    };
-                    const auto weigh = [&](auto hide) {
-                        const float neg = (m_ref == -INFINITY ? 0.f : -m_ref) - kPrShift;
-                        const float2 a2 = make_float2(scale, scale), b2 = make_float2(neg, neg);
-                        sum = make_float2(0.f, 0.f);
-                        chunks(hide, [&](uint32_t (&r)[16], auto c, bool none) {
-                            uint32_t* to = w[c.value / 4] + c.value % 4 * 8;
-                            if (none) {
-#pragma unroll
-                                for (int e = 0; e < 8; ++e) to[e] = 0u;
-                                return;
-                            }
-                            float2 part = make_float2(0.f, 0.f);
-#pragma unroll
-                            for (int e = 0; e < 16; e += 4) {
-                                float2 x0 = make_float2(__uint_as_float(r[e]), __uint_as_float(r[e + 1]));
-                                float2 x1 = make_float2(__uint_as_float(r[e + 2]), __uint_as_float(r[e + 3]));
-                                x0 = __ffma2_rn(x0, a2, b2);
-                                x1 = __ffma2_rn(x1, a2, b2);
-                                x0 = make_float2(fast_exp2(x0.x), fast_exp2(x0.y));
-                                x1 = make_float2(fast_exp2(x1.x), fast_exp2(x1.y));
-                                part = __fadd2_rn(part, __fadd2_rn(x0, x1));
-                                to[e / 2] = f2_to_bf16x2(x0.x, x0.y);
-                                to[e / 2 + 1] = f2_to_bf16x2(x1.x, x1.y);
-                            }
-                            sum = __fadd2_rn(sum, part);
-                        });
-                    };
-                    // The tile's maximum becomes the reference where it is larger; O follows.
-                    const auto raise = [&](auto hide) {
+                        if (masked) weigh(PromptConst<true>{});
+                        else weigh(PromptConst<false>{});
+                        anew = (ahead && follow(g - 1)) || __any_sync(kFull, sum.x + sum.y > kPrMost);
+                        if (!ok) break;
+                        if (!anew) {
+                            settle(g);
+                            tmem_st(s_addr, w[0]);
+                            tmem_st(s_addr + 32u, w[1]);
+                        }
+                    }
+                    if (anew) {
+                        // The tile's maximum becomes the reference where it is larger; O follows.
+                        // (Rolled up: code that runs once an item is fetched anew each time.)
                         float mx = -INFINITY;
-                        chunks(hide, [&](uint32_t (&r)[16], auto, bool none) {
-                            if (none) return;
+#pragma unroll 1
+                        for (int c = 0; c < 128; c += 16) {
+                            uint32_t r[16];
+                            tmem_ld_start(r, s_addr + uint32_t(c));
+                            tmem_ld_wait(r);
+                            if (masked && hide(r, c)) continue;
 #pragma unroll
                             for (int e = 0; e < 16; ++e) mx = fmaxf(mx, __uint_as_float(r[e]));
-                        });
+                        }
                         const float to = fmaxf(m_ref, mx * scale), f = to > m_ref ? fast_exp2(m_ref - to) : 1.f;
-                        m_ref = sh.ref[mine] = to;
+                        m_ref = ref[mine] = to;
                         l2.x *= f;
                         l2.y *= f;
-                        if (lane == 0) *reinterpret_cast<volatile int*>(&sh.raised[quad]) = g;
+                        if (lane == 0) *raised = g;
                         if (jj > 0 && __any_sync(kFull, f != 1.f)) {
-                            if (!(ok = wait(&bars.pv_done[(g - 1) % kPrScores], (g - 1) / kPrScores))) return;
+                            if (!(ok = wait(&bars.pv_done[(g - 1) % kPrScores], (g - 1) / kPrScores))) break;
                             tc_fence_after();
 #pragma unroll 1
-                            for (int c = 0; c < D; c += 32) {
-                                uint32_t o[32];
-                                tmem_ld(o, o_addr + uint32_t(c));
+                            for (int c = 0; c < D; c += 16) {
+                                uint32_t o[16];
+                                tmem_ld_start(o, o_addr + uint32_t(c));
+                                tmem_ld_wait(o);
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
                                 tmem_st(o_addr + uint32_t(c), o);
                             }
                         }
-                    };
-                    const auto tile = [&](auto hide) {
-                        // a row without a reference: nothing can be weighed ahead
-                        bool early = jj == 0;
-                        if (!early && __any_sync(kFull, m_ref == -INFINITY)) {
-                            (void)follow(g - 1);
-                            if (!ok) return;
-                            early = true;
-                        }
-                        if (early && __any_sync(kFull, m_ref == -INFINITY)) {
-                            raise(hide);
-                            if (!ok) return;
-                            settle(g);
-                            weigh(hide);
-                            return;
-                        }
-                        weigh(hide);
-                        if (!early && follow(g - 1)) weigh(hide);
-                        if (!ok) return;
-                        if (__any_sync(kFull, sum.x + sum.y > kPrMost)) {
-                            raise(hide);
-                            if (!ok) return;
-                            weigh(hide);
-                        }
                         settle(g);
-                    };
-                    if (masked) tile(PromptConst<true>{});
-                    else tile(PromptConst<false>{});
-                    if (!ok) break;
+                        // weights over scores that have been read
+                        const float neg = (m_ref == -INFINITY ? 0.f : -m_ref) - kPrShift;
+                        sum = make_float2(0.f, 0.f);
+#pragma unroll 1
+                        for (int c = 0; c < 128; c += 16) {
+                            uint32_t r[16], x[8];
+                            tmem_ld_start(r, s_addr + uint32_t(c));
+                            tmem_ld_wait(r);
+                            if (masked && hide(r, c)) {
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) x[e] = 0u;
+                            } else {
+                                sum = __fadd2_rn(sum, weights(r, x, neg));
+                            }
+                            tmem_st(s_addr + uint32_t(c / 2), x);
+                        }
+                    }
                     l2 = __fadd2_rn(l2, sum);
-                    tmem_st(s_addr, w[0]);
-                    tmem_st(s_addr + 32u, w[1]);
                     tmem_wait_st();
                 } else {
                     settle(g);
+                }
+                // the first weights are for an O that begins anew
+                if (jj == 0 && unread) {
+                    if (!(ok = wait(&bars.o_read[quad], full - 1))) break;
+                    unread = false;
                 }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_peer(lead(&bars.p_full[b]));
             }
             if (!ok) break;
+            // ---- The warp that has the last tile writes the rows; the other goes on to the next
+            // item, whose first tile it has.
+            const bool last = ((g - 1) & 1) == team;
+            if (rows > 0 && !last) {
+                sh.sum[mine] = make_float2(l2.x + l2.y, m_ref);
+                if (lane == 0) bulk_wait_read();  // (of an item whose rows this warp wrote: the space is the other's now)
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(&bars.sum_there[quad]));
+                unread = true;
+                ++full;
+                ++items;
+                continue;
+            }
             if (!(ok = wait(&bars.o_full, items++))) break;
             if (rows <= 0) continue;
-            // ---- write the rows, half of the columns a warp: they pass through shared memory,
-            // chunks swizzled by row, and leave as a tensor copy, which nobody waits for. A
-            // sequence's last rows share their box with the next one's, and leave as
-            // stores of whole lines.
-            if (((g - 1) & 1) != team && !(ok = wait(&bars.settled[quad][(g - 1) & 1], (g - 1) >> 1))) break;
-            const float last = sh.ref[mine];
-            sh.sum[team][mine] = last > m_ref ? (l2.x + l2.y) * fast_exp2(m_ref - last) : l2.x + l2.y;
-            if (!(ok = meet())) break;
+            if (!(ok = wait(&bars.sum_there[quad], full++))) break;
             tc_fence_after();
-            const float l = sh.sum[0][mine] + sh.sum[1][mine], f = l > 0.f ? 1.f / l : 0.f;
-            const uint32_t st = out0 + uint32_t(warp * T::kOutBytes), o_half = o_addr + uint32_t(team * (D / 2));
-            const auto swz = [](int r) { return uint32_t(D == 128 ? r & 7 : (r >> 1) & 3); };
+            const float2 other = sh.sum[mine];
+            const float l = l2.x + l2.y + (m_ref > other.y ? other.x * fast_exp2(other.y - m_ref) : other.x), f = l > 0.f ? 1.f / l : 0.f;
+            // The rows pass through shared memory, chunks swizzled by row, and leave as tensor
+            // copies, which nobody waits for. A sequence's last rows share their box with the
+            // next one's, and leave as stores of whole lines.
+            const uint32_t st = out0 + uint32_t(quad * 2 * T::kOutBytes);
+            const uint32_t mine_at = st + uint32_t(lane * 128), sw = uint32_t(lane & 7);
             if (lane == 0) bulk_wait_read();
             __syncwarp();
-#pragma unroll
-            for (int h = 0; h < D / 64; ++h) {
+#pragma unroll 1
+            for (int h = 0; h < D / 32; ++h) {
                 uint32_t o[32];
-                tmem_ld(o, o_half + uint32_t(h * 32));
+                tmem_ld(o, o_addr + uint32_t(h * 32));
+                if (h == D / 32 - 1) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(&bars.o_read[quad]));
+                }
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     uint32_t x[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         x[k] = f2_to_bf16x2(__uint_as_float(o[8 * e + 2 * k]) * f, __uint_as_float(o[8 * e + 2 * k + 1]) * f);
-                    sts128(st + uint32_t(lane * D) + ((uint32_t(h * 4 + e) ^ swz(lane)) << 4), make_uint4(x[0], x[1], x[2], x[3]));
+                    sts128(mine_at + uint32_t(h / 2 * 4096) + ((uint32_t(h % 2 * 4 + e) ^ sw) << 4), make_uint4(x[0], x[1], x[2], x[3]));
                 }
             }
             if (rows == 32) {
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
-                    tma_store_4d(&p.tm_out, st, team * (D / 2), 0, kvh, row0 + (first >> lgG));
+#pragma unroll
+                    for (int c = 0; c < D / 64; ++c)
+                        tma_store_4d(&p.tm_out, st + uint32_t(c * 4096), c * 64, 0, kvh, row0 + (first >> lgG));
                     bulk_commit();
                 }
             } else {
                 __syncwarp();
-                constexpr int CH = D / 16;  // 16-byte chunks of half a row
+                constexpr int CH = D / 8;  // 16-byte chunks of a row
 #pragma unroll 1
                 for (int e = lane; e < rows * CH; e += 32) {
-                    const int rr = first + e / CH, ch = e % CH;
-                    const uint4 v = lds128(st + uint32_t((e / CH) * D) + ((uint32_t(ch) ^ swz(e / CH)) << 4));
+                    const int r = e / CH, ch = e % CH, rr = first + r;
+                    const uint4 v = lds128(st + uint32_t(ch / 8 * 4096 + r * 128) + ((uint32_t(ch % 8) ^ uint32_t(r & 7)) << 4));
                     *reinterpret_cast<uint4*>(p.out + int64_t(row0 + (rr >> lgG)) * p.out_stride +
-                                              (kvh * G + (rr & (G - 1))) * D + team * (D / 2) + ch * 8) = v;
+                                              (kvh * G + (rr & (G - 1))) * D + ch * 8) = v;
                 }
+                __syncwarp();
             }
-            tc_fence_before();
-            // O has been read by both warps before the next item's P is announced, by either
-            if (!(ok = meet())) break;
         }
         if (lane == 0) {
             bulk_wait();
@@ -633,13 +651,17 @@ prompt_kernel(const __grid_constant__ PromptParams p) {
             const auto publish = [&](const PromptItem& x) {
                 const int s = published & 1;
                 if (published >= 2 && !(ok = wait(&bars.item_empty[s], (published >> 1) - 1))) return false;
-                if (lane < 2) {  // to either CTA
-                    const uint32_t to = cluster_addr(smem_addr(&sh.item[s]), uint32_t(lane));
-                    const uint32_t* from = reinterpret_cast<const uint32_t*>(&x);
+                if (lane == 0) {
+                    sh.item[s] = x;
+                    mbar_arrive(bar(&bars.item_full[s]));
+                    // and to the other CTA, whose planner passes it on: a wait that
+                    // sees another CTA's stores takes long
+                    const uint32_t to = cluster_addr(smem_addr(&sh.item[s]), 1);
+                    const int words[] = {x.kind, x.kvh, x.row0, x.n, x.r_first, x.r_end, x.kt.nsink, x.kt.lo, x.kt.n};
+                    static_assert(sizeof(words) == sizeof(PromptItem), "an item's words");
 #pragma unroll
-                    for (int e = 0; e < int(sizeof(PromptItem) / 4); ++e) st_cluster_u32(to + 4u * e, from[e]);
-                    const uint32_t full = cluster_addr(bar(&bars.item_full[s]), uint32_t(lane));
-                    mbar_arrive_release_cluster(full);
+                    for (int e = 0; e < int(sizeof(words) / 4); ++e) st_cluster_u32(to + 4u * e, uint32_t(words[e]));
+                    mbar_arrive_release_cluster(cluster_addr(bar(&bars.mail[s]), 1));
                 }
                 __syncwarp();
                 ++published;
@@ -663,10 +685,19 @@ prompt_kernel(const __grid_constant__ PromptParams p) {
                 if (!more) break;
             }
             if (ok) {
+                x = PromptItem{};
                 x.kind = 2;
                 (void)publish(x);
             }
             if (!ok && lane == 0) report(p.err, kErrTimeout);
+        } else {
+            for (int q = 0;; ++q) {
+                if (!__all_sync(kFull, wait_phase_cluster(bar(&bars.mail[q & 1]), uint32_t(q >> 1) & 1u))) break;
+                const int kind = sh.item[q & 1].kind;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(&bars.item_full[q & 1]));
+                if (kind == 2) break;
+            }
         }
     }
     tc_fence_before();

@@ -31,7 +31,7 @@ extern "C" int pkv_prompt_attention(const pkv_cache_desc* c, const pkv_batch_des
     if ((st = rows_tensor_map(g, hkv, d, batch->num_tokens, q, q_stride, 128, &p.tm_q)) != PKV_OK) return st;
     if ((st = rows_tensor_map(1, hkv, d, batch->num_tokens, k, k_stride, 64, &p.tm_k)) != PKV_OK) return st;
     if ((st = rows_tensor_map(1, hkv, d, batch->num_tokens, v, v_stride, 128, &p.tm_v, d / 2)) != PKV_OK) return st;
-    if ((st = rows_tensor_map(g, hkv, d, batch->num_tokens, out, out_stride, 32, &p.tm_out, d / 2)) != PKV_OK) return st;
+    if ((st = rows_tensor_map(g, hkv, d, batch->num_tokens, out, out_stride, 32, &p.tm_out)) != PKV_OK) return st;
     p.out = static_cast<uint16_t*>(out);
     p.out_stride = out_stride;
     p.err = c->err_word;
