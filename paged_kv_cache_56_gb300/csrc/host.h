@@ -55,13 +55,13 @@ int pool_tensor_map(const void* pool, int32_t num_blocks, int32_t rows, int32_t 
                     int32_t box_rows = 16);
 
 int encode_map(CUtensorMapDataType type, int rank, const void* base, const cuuint64_t* dims, const cuuint64_t* strides,
-               const cuuint32_t* box, CUtensorMap* out, bool swizzle_64b = false);
+               const cuuint32_t* box, CUtensorMap* out);
 
 // Tensor map of token rows [tokens][kv_heads][group][head_dim], bf16, `stride`
 // elements a token, for boxes of `rows` rows (rows / group tokens x the group) x
-// `columns` elements: 64 with the 128-byte swizzle, 32 with the 64-byte one.
+// 64 elements with the 128-byte swizzle.
 int rows_tensor_map(int group, int kv_heads, int head_dim, int tokens, const void* base, int64_t stride, int rows,
-                    CUtensorMap* out, int columns = 64);
+                    CUtensorMap* out);
 
 // Raises a kernel's dynamic shared-memory limit once per kernel and device and
 // returns how many of its CTAs fit on an SM; launch_regs > 0: fails unless

@@ -29,8 +29,8 @@ extern "C" int pkv_prompt_attention(const pkv_cache_desc* c, const pkv_batch_des
     int ctas = 0;
     if ((st = prepare_kernel(reinterpret_cast<const void*>(fn), smem, kPrThreads, kPrLaunchRegs, &ctas)) != PKV_OK) return st;
     if ((st = rows_tensor_map(g, hkv, d, batch->num_tokens, q, q_stride, 128, &p.tm_q)) != PKV_OK) return st;
-    if ((st = rows_tensor_map(1, hkv, d, batch->num_tokens, k, k_stride, 64, &p.tm_k)) != PKV_OK) return st;
-    if ((st = rows_tensor_map(1, hkv, d, batch->num_tokens, v, v_stride, 128, &p.tm_v, d / 2)) != PKV_OK) return st;
+    if ((st = rows_tensor_map(1, hkv, d, batch->num_tokens, k, k_stride, 128, &p.tm_k)) != PKV_OK) return st;
+    if ((st = rows_tensor_map(1, hkv, d, batch->num_tokens, v, v_stride, 128, &p.tm_v)) != PKV_OK) return st;
     if ((st = rows_tensor_map(g, hkv, d, batch->num_tokens, out, out_stride, 32, &p.tm_out)) != PKV_OK) return st;
     p.out = static_cast<uint16_t*>(out);
     p.out_stride = out_stride;
@@ -42,13 +42,13 @@ extern "C" int pkv_prompt_attention(const pkv_cache_desc* c, const pkv_batch_des
     // never 0 or infinite: a hidden token's score is -infinity, and 0 times that is
     // not a number, nor is an infinite scale times a score of 0
     p.qscale = std::min(std::max(sm_scale * 1.4426950408889634f, 1e-37f), 3.4e38f);
-    // row tiles of all sequences, as many as the batch can have
+    // items of a kv head, as many as the batch can have
     const int64_t longest = (int64_t(batch->max_tokens) * g + 2 * kPrRows - 1) / (2 * kPrRows);
     const int64_t tiles = std::min(longest * batch->B, batch->num_tokens * int64_t(g) / (2 * kPrRows) + batch->B);
     const int64_t items = tiles * hkv;
-    // A pair drops items that the batch does not have at 0.4 us each, while its other
-    // warps wait: 2^26 items on 76 pairs are 0.35 s of the second that they do.
-    if (items > int64_t(1) << 26) return PKV_ERR_UNSUPPORTED;
+    // A CTA drops items that the batch does not have at 0.4 us each, while its other
+    // warps wait: 2^27 items on 152 SMs are 0.35 s of the second that they do.
+    if (items > int64_t(1) << 27) return PKV_ERR_UNSUPPORTED;
     p.item_tiles = int(tiles);
-    return launch(fn, dim3(unsigned(2 * items)), dim3(kPrThreads), smem, static_cast<cudaStream_t>(stream), p);
+    return launch(fn, dim3(unsigned(items)), dim3(kPrThreads), smem, static_cast<cudaStream_t>(stream), p);
 }

@@ -63,23 +63,23 @@ int sm_count(int* out) {
 }
 
 int encode_map(CUtensorMapDataType type, int rank, const void* base, const cuuint64_t* dims, const cuuint64_t* strides,
-               const cuuint32_t* box, CUtensorMap* out, bool swizzle_64b) {
+               const cuuint32_t* box, CUtensorMap* out) {
     const PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
     const cuuint32_t elem[4] = {1, 1, 1, 1};
     return enc && enc(out, type, rank, const_cast<void*>(base), dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                      swizzle_64b ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
                ? PKV_OK
                : PKV_ERR_CUDA;
 }
 
 int rows_tensor_map(int group, int kv_heads, int head_dim, int tokens, const void* base, int64_t stride, int rows,
-                    CUtensorMap* out, int columns) {
+                    CUtensorMap* out) {
     const cuuint64_t g = cuuint64_t(group), d = cuuint64_t(head_dim);
     const cuuint64_t dims[4] = {d, g, cuuint64_t(kv_heads), cuuint64_t(tokens)};
     const cuuint64_t strides[3] = {d * 2, g * d * 2, cuuint64_t(stride) * 2};
-    const cuuint32_t box[4] = {cuuint32_t(columns), cuuint32_t(g), 1, cuuint32_t(rows / g)};
-    return encode_map(CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims, strides, box, out, columns == 32);
+    const cuuint32_t box[4] = {64, cuuint32_t(g), 1, cuuint32_t(rows / g)};
+    return encode_map(CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims, strides, box, out);
 }
 
 namespace {
