@@ -728,33 +728,38 @@ def make_plan(token_starts: torch.Tensor, block_tables: torch.Tensor, ctx_lens: 
     return d
 
 
-def _pool_ids(pool: SeqPool, t, name: str, n: int, plan=None):
+def _pool_ids(pool: SeqPool, t, name: str, n: int):
     """Pointer of an int32 [n] tensor on the pool's device (None: NULL)."""
     if t is None:
         return None
-    if t.device != pool.device or (plan is not None and plan.device != pool.device):
-        raise ValueError(f"{name} and the plan must be on {pool.device}")
+    if t.device != pool.device:
+        raise ValueError(f"{name} must be on {pool.device}")
     return _dev(t, name, torch.int32, n)
+
+
+def _check_plan(pool: SeqPool, plan: PlanDesc, B: int) -> None:
+    if plan.device != pool.device:
+        raise ValueError(f"the plan must be on {pool.device}")
+    if B != plan.B or (B and plan.width != pool.max_blocks):
+        raise ValueError(f"the plan is for {plan.B} entries of {plan.width} blocks, not {B} of {pool.max_blocks}")
 
 
 def pkv_plan_batch(pool: SeqPool, slots: torch.Tensor, plan: PlanDesc, counts=None, stream=None) -> None:
     """Plans counts[b] new tokens (None: one each) of the sequences in slots[b]
     (-1: none): blocks off the pool's ring, tables, lengths and slot maps into ``plan``."""
     B = slots.numel()
-    if B != plan.B or (plan.width != pool.max_blocks and B):
-        raise ValueError(f"the plan is for {plan.B} entries of {plan.width} blocks, not {B} of {pool.max_blocks}")
+    _check_plan(pool, plan, B)
     _check("pkv_plan_batch",
-           lib().pkv_plan_batch(ctypes.byref(pool), _pool_ids(pool, slots, "slots", B, plan),
+           lib().pkv_plan_batch(ctypes.byref(pool), _pool_ids(pool, slots, "slots", B),
                                 _pool_ids(pool, counts, "counts", B), B, ctypes.byref(plan), _batch_stream(pool, stream)))
 
 
 def pkv_commit_batch(pool: SeqPool, slots: torch.Tensor, plan: PlanDesc, accepted=None, stream=None) -> None:
     """Keeps the first accepted[b] (None: all) of the tokens that the plan's entries brought."""
     B = slots.numel()
-    if B != plan.B:
-        raise ValueError(f"the plan is for {plan.B} entries, not {B}")
+    _check_plan(pool, plan, B)
     _check("pkv_commit_batch",
-           lib().pkv_commit_batch(ctypes.byref(pool), _pool_ids(pool, slots, "slots", B, plan),
+           lib().pkv_commit_batch(ctypes.byref(pool), _pool_ids(pool, slots, "slots", B),
                                   _pool_ids(pool, accepted, "accepted", B), B, ctypes.byref(plan),
                                   _batch_stream(pool, stream)))
 

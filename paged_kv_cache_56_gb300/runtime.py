@@ -138,15 +138,23 @@ class PagedKVCache:
         self.device = device
         self.layers = [LayerCache(num_blocks, num_q_heads, num_kv_heads, head_dim, block_size, f,
                                   max_slots, device) for f in flags]
-        self.alloc = pkv.pkv_allocator_create(num_blocks, block_size, initial_order)
+        self._alloc = pkv.pkv_allocator_create(num_blocks, block_size, initial_order)
+        self.pool = None  # the DevicePool that has the block lists, while they are on the GPU
         self.free_slots = list(range(max_slots))
         self.seqs: dict[int, Seq] = {}
         self.forked = False  # set by fork(): only then can a block have several holders
 
+    @property
+    def alloc(self):
+        """The host allocator's handle; RuntimeError while a DevicePool has the blocks."""
+        if self.pool is not None:
+            raise RuntimeError("the cache's block lists are on the GPU: pull() them first")
+        return self._alloc
+
     def close(self):
-        if self.alloc is not None:
-            pkv.pkv_allocator_destroy(self.alloc)
-            self.alloc = None
+        if self._alloc is not None:
+            pkv.pkv_allocator_destroy(self._alloc)
+            self._alloc = None
 
     def __del__(self):
         try:
@@ -158,6 +166,13 @@ class PagedKVCache:
     def add_sequence(self, req_id: int, n_blocks: int = 0, shared_blocks=()) -> Seq:
         if not self.free_slots:
             raise RuntimeError("no free sequence slot")
+        if self.pool is not None:  # blocks come with the first plan
+            if n_blocks or len(shared_blocks):
+                raise ValueError("a sequence begins without blocks while the block lists are on the GPU")
+            if req_id in self.seqs:
+                raise pkv.PkvError("pkv_alloc", pkv.PKV_ERR_EXISTS)
+            self.seqs[req_id] = Seq(req_id, self.free_slots.pop(0))
+            return self.seqs[req_id]
         pkv.pkv_alloc(self.alloc, req_id, n_blocks)
         if len(shared_blocks):
             pkv.pkv_attach_shared(self.alloc, req_id, list(shared_blocks))
@@ -188,6 +203,10 @@ class PagedKVCache:
         return s
 
     def remove_sequence(self, req_id: int) -> None:
+        if self.pool is not None:
+            self.pool.release([req_id])
+            self.free_slots.append(self.seqs.pop(req_id).slot)
+            return
         s = self.seqs.pop(req_id)
         pkv.pkv_free(self.alloc, req_id)
         self.free_slots.append(s.slot)
@@ -278,10 +297,14 @@ class PagedKVCache:
                 pkv.pkv_copy_blocks(lc.desc, src, dst, stream)
 
     def commit_step(self, req_ids) -> None:
+        self._lengths_are_here()
         for r in req_ids:
             self.seqs[r].length += 1
             self.seqs[r].planned = 0
 
+
+    def _lengths_are_here(self) -> None:
+        _ = self.alloc  # raises while a DevicePool keeps them
 
     # -- a chunk of new tokens a sequence ------------------------------------
     def plan_chunk(self, req_ids, counts) -> "ChunkPlan":
@@ -337,6 +360,7 @@ class PagedKVCache:
         the first token stays, p = length + 1, any of block_size - 1 - p %
         block_size tokens behind it can be rejected; of longer drafts, on a fork.
         A chunk that has run is committed, with 0 if nothing of it stays."""
+        self._lengths_are_here()
         if len(req_ids) != len(counts) or len(set(req_ids)) != len(req_ids):
             raise ValueError("counts needs one number per sequence, each sequence once")
         counts = [int(n) for n in counts]
@@ -514,13 +538,17 @@ class GraphStep:
     (R > 1 re-reads the same layer's cache with R different queries). The
     quantize kernel is always launched over a -1-padded fill list so that the
     graph does not change from step to step. The batch size is fixed at
-    capture time.
+    capture time. With a DevicePool (after ``pool.use``) the graph also holds the
+    step's plan and commit.
     """
 
     def __init__(self, cache: PagedKVCache, bufs: StepBuffers, sm_scale: float, repeat: int = 1,
-                 fused: bool = True):
+                 fused: bool = True, pool: "DevicePool | None" = None):
         self.cache, self.bufs, self.sm_scale, self.R = cache, bufs, sm_scale, repeat
         self.fused = fused  # one pkv_decode_step per layer instead of append + quantize + attention
+        self.pool = pool    # plan and commit the step on the GPU, too: a replay needs nothing of the host
+        if pool is not None and not fused:
+            raise ValueError("a step that is planned on the GPU runs the fused kernels")
         B, dev = bufs.B, cache.device
         if B == 0:
             raise ValueError("upload a plan before capturing")
@@ -535,12 +563,15 @@ class GraphStep:
     def launches_per_step(self) -> int:
         per_attn = 2 if (self.bufs.split_tokens and self.bufs.ws_count is None) else 1
         if self.fused:
-            return self.cache.L * self.R * per_attn
+            return self.cache.L * self.R * per_attn + (2 if self.pool is not None else 0)
         return sum(1 + int(f) + self.R * per_attn for f in self.cache.layer_int8)
 
     def _layers(self, attention_only: bool = False) -> None:
         c, b = self.cache, self.bufs
         B = b.B
+        planned = self.pool is not None and not attention_only
+        if planned:
+            self.pool.plan(b)
         for li, lc in enumerate(c.layers):
             fused_here = self.fused and not attention_only
             if not attention_only and not self.fused:
@@ -557,6 +588,8 @@ class GraphStep:
                     pkv.pkv_decode_attention(lc.desc, self.q[qi], b.tab[:B], b.ctx[:B], b.slot[:B],
                                              self.sm_scale, self.out[qi], b.split_tokens, b.max_splits, b.ws_o,
                                              b.ws_ml, b.ws_count)
+        if planned:
+            self.pool.commit(b)
 
     def run_eager(self) -> None:
         self._layers()
@@ -744,31 +777,108 @@ class ChunkBuffers:
         return self._ws[key]
 
 
+def axis_pairs(sections, in_turn: bool = False) -> list:
+    """Axis of each pair of a rotary turn with several axes (``pkv.make_rope_axes``):
+    sections[a] pairs turn by axis a, one section after the other, or dealt out in
+    turn (0, 1, 2, 0, 1, 2, ...) until an axis has its number."""
+    sections = [int(n) for n in sections]
+    if not 1 <= len(sections) <= 4 or any(n < 0 for n in sections):
+        raise ValueError("one to four sections of at least no pairs")
+    if not in_turn:
+        return [a for a, n in enumerate(sections) for _ in range(n)]
+    left, out = sections[:], []
+    while any(left):
+        for a in range(len(left)):
+            if left[a]:
+                left[a] -= 1
+                out.append(a)
+    return out
+
+
+class AxisPositions:
+    """Rotary positions (time, height, width) of the tokens of prompts with images
+    and video. Every sequence has a list of segments {t, h, w, step} (see
+    ``pkv_axis_positions``), kept on the GPU by its slot; ``update`` works out the
+    positions of an uploaded (or planned) batch's tokens. The tensor ``positions`` [3, max_tokens] is
+    always the same, so that a rotary descriptor made of it stays good."""
+
+    def __init__(self, cache: PagedKVCache, max_tokens: int, max_segments: int):
+        dev = cache.device
+        self.cache = cache
+        self.segments = torch.zeros((cache.max_slots, max_segments, 4), dtype=torch.int32, device=dev)
+        self.counts = torch.zeros(cache.max_slots, dtype=torch.int32, device=dev)
+        self.positions = torch.zeros((3, max_tokens), dtype=torch.int32, device=dev)
+        self.err = torch.zeros(1, dtype=torch.int32, device=dev)
+
+    def set(self, req_id: int, segments, stream=None) -> None:
+        """The sequence's segments; tokens behind them are text."""
+        a = np.asarray(list(segments), np.int64).reshape(-1, 4)
+        t, h, w, step = a.T
+        if len(a) > self.segments.shape[1]:
+            raise ValueError(f"more than {self.segments.shape[1]} segments")
+        if (a < 0).any() or ((h == 0) != (w == 0)).any() or (a > 2 ** 31 - 1).any() or any(
+                int(x) * int(y) * int(z) > 2 ** 31 - 1 or (int(x) - 1) * int(q) > 2 ** 31 - 1
+                for x, y, z, q in a if y):
+            raise ValueError("a segment is {t, 0, 0, *} or {t, h, w, step} with h, w > 0 and nothing negative or past 2^31 - 1")
+        slot = self.cache.seqs[req_id].slot
+        with _on(stream):
+            self.segments[slot, :len(a)].copy_(torch.from_numpy(a.astype(np.int32)))
+            self.counts[slot] = len(a)
+
+    def update(self, bufs: "ChunkBuffers", stream=None) -> None:
+        pkv.pkv_axis_positions(bufs.batch, self.segments, self.counts, self.positions, rows=bufs.slot, err=self.err,
+                               stream=stream)
+
+
+def _with_axes(rope):
+    """A rotary descriptor for pkv_rope_append_axes: one of one axis as it is, with all pairs on that axis."""
+    if rope is None or isinstance(rope, pkv.RopeAxesDesc):
+        return rope
+    inv_freq, positions = rope.keep
+    return pkv.make_rope_axes(inv_freq, [0] * inv_freq.numel(), positions=None if positions is None else positions[None],
+                              interleaved=bool(rope.interleaved), scale=rope.scale)
+
+
 def run_chunk(cache: PagedKVCache, bufs: ChunkBuffers, q, k, v, out, sm_scale: float, rope=None, window: int = 0,
-              sinks: int = 0, stream=None) -> None:
+              sinks: int = 0, stream=None, prompts: bool = False) -> None:
     """Kernel launches of one uploaded chunk, per layer l: turn q[l] [T, Hq, d]
     (in place) and k[l] and write k[l], v[l] [T, Hkv, d] into the cache, then attend into
     out[l]. window and sinks may be lists with one entry per layer (models that
-    alternate windowed and full layers)."""
+    alternate windowed and full layers). rope: from pkv.make_rope, or from
+    pkv.make_rope_axes for positions on several axes. prompts: every sequence is a
+    whole prompt, and attends from its rows instead of from the cache (an INT8 cache's
+    rows before they are quantized); k[l] is then turned in place, too."""
     win = list(window) if isinstance(window, (list, tuple)) else [window] * cache.L
     snk = list(sinks) if isinstance(sinks, (list, tuple)) else [sinks] * cache.L
+    axes = prompts or isinstance(rope, pkv.RopeAxesDesc)
+    if axes:
+        rope = _with_axes(rope)
     for li, lc in enumerate(cache.layers):
-        pkv.pkv_rope_append(lc.desc, bufs.batch, rope, q[li], k[li], v[li], None, stream)
+        if axes:
+            pkv.pkv_rope_append_axes(lc.desc, bufs.batch, rope, q[li], k[li], v[li], None, k[li] if prompts else None, stream)
+        else:
+            pkv.pkv_rope_append(lc.desc, bufs.batch, rope, q[li], k[li], v[li], None, stream)
+        if prompts:
+            pkv.pkv_prompt_attention(lc.desc, bufs.batch, q[li], k[li], v[li], out[li], win[li], snk[li], sm_scale, stream)
+            continue
         split, ws = bufs.workspace(lc.desc, win[li], snk[li])
         pkv.pkv_window_attention(lc.desc, bufs.batch, q[li], out[li], win[li], snk[li], sm_scale, split, ws, stream)
 
 
 def extend_step(cache: PagedKVCache, bufs: ChunkBuffers, req_ids, counts, q, k, v, out, sm_scale: float, rope=None,
-                window=0, sinks=0, stream=None) -> ChunkPlan:
+                window=0, sinks=0, stream=None, prompts: bool = False) -> ChunkPlan:
     """Host plan + upload + kernels of counts[i] new tokens of each sequence;
     advances the sequences. q, k, v, out: per layer, rows of the sequences one
     after another, bufs.max_tokens rows long (rows behind the batch's are not
-    touched). The uploads, too, are on `stream` (default: the current one)."""
+    touched). The uploads, too, are on `stream` (default: the current one).
+    prompts: as in run_chunk; the sequences must be empty before."""
+    if prompts and any(n and cache.seqs[r].length for r, n in zip(req_ids, counts)):
+        raise ValueError("a sequence that has tokens attends over the cache, not from its rows")
     plan = cache.plan_chunk(req_ids, counts)
     with _on(stream):
         cache.apply_cow(plan)
         bufs.upload(plan)
-        run_chunk(cache, bufs, q, k, v, out, sm_scale, rope, window, sinks)
+        run_chunk(cache, bufs, q, k, v, out, sm_scale, rope, window, sinks, prompts=prompts)
     cache.commit_chunk(req_ids, counts)
     return plan
 
@@ -795,3 +905,133 @@ def _read_back(cache: PagedKVCache, layer: int, req_ids, dtype):
         batch = pkv.make_batch(up(starts), up(tables), up(np.array(lens)), slots, num_tokens=T, max_tokens=max(lens))
         pkv.pkv_gather_kv(cache.layers[layer].desc, batch, k, v)
     return k, v, starts
+
+
+# ---------------------------------------------------------------------------
+# Steps planned on the GPU
+# ---------------------------------------------------------------------------
+
+class DevicePool:
+    """A cache's block lists, lengths and free blocks, moved to the GPU: steps are
+    then planned and committed there (``pkv_plan_batch``), on a stream or in a
+    captured graph, without the host's tables, uploads or lengths. Blocks are given
+    out as the host allocator would give them. While a pool is alive the cache's
+    host plans raise; ``pull`` brings everything back.
+
+    Blocks have one holder: a cache with forks that still share blocks, with a shared
+    prefix or with a planned chunk that is not committed is refused."""
+
+    def __init__(self, cache: PagedKVCache):
+        seqs = cache.seqs.values()
+        if any(s.pinned for s in seqs):
+            raise ValueError("a cache with a shared prefix is planned on the host")
+        if any(s.planned for s in seqs):
+            raise ValueError("a planned chunk is not committed")
+        if cache.max_slots > 65536:
+            raise ValueError("at most 65536 slots")
+        lists = {s.slot: cache.table(s.req_id) for s in seqs}
+        if any(pkv.pkv_block_refs(cache.alloc, b) > 1 for t in lists.values() for b in t):
+            raise ValueError("blocks that forks share are planned on the host")
+        num_blocks, free = cache.layers[0].num_blocks, pkv.pkv_free_list(cache.alloc)
+        if sum(map(len, lists.values())) + len(free) != num_blocks:
+            raise ValueError("some blocks are held by requests that are not the cache's")
+        tables = np.full((cache.max_slots, cache.max_blocks), -1, np.int32)
+        lens, held = np.zeros(cache.max_slots, np.int32), np.zeros(cache.max_slots, np.int32)
+        for s in seqs:
+            t = lists[s.slot]
+            tables[s.slot, :len(t)] = t
+            lens[s.slot], held[s.slot] = s.length, len(t)
+        ring = np.full(num_blocks, -1, np.int32)
+        ring[:len(free)] = free
+
+        def up(a):
+            return torch.from_numpy(np.ascontiguousarray(a, np.int32)).to(cache.device)
+        self.cache = cache
+        self.tables, self.lens, self.held, self.ring = up(tables), up(lens), up(held), up(ring)
+        self.state, self.err = up([0, len(free), 0, 0]), up([0])
+        self.desc = pkv.make_seq_pool(self.tables, self.lens, self.held, self.ring, self.state, block_size=cache.bs,
+                                      int8=cache.int8, err=self.err)
+        torch.cuda.synchronize()  # there, whichever stream plans first
+        cache.pool = self
+
+    def _plan_of(self, bufs):
+        B = bufs.B if isinstance(bufs, StepBuffers) else bufs.max_batch
+        if B == 0:
+            raise ValueError("use() the buffers first")
+        if getattr(bufs, "gpu_plan", None) is None or bufs.gpu_plan.B != B:
+            if torch.cuda.is_current_stream_capturing():
+                raise RuntimeError("plan the batch once before capturing it")
+            if isinstance(bufs, StepBuffers):
+                starts = torch.zeros(B + 1, dtype=torch.int32, device=self.cache.device)
+                bufs.gpu_plan = pkv.make_plan(starts, bufs.tab[:B], bufs.ctx[:B], num_tokens=B, max_tokens=1)
+            else:
+                bufs.gpu_plan = pkv.make_plan(bufs.starts, bufs.tab, bufs.ctx, num_tokens=bufs.max_tokens,
+                                              max_tokens=bufs.max_new)
+        return bufs.slot[:B], bufs.gpu_plan
+
+    def use(self, bufs, req_ids, stream=None) -> None:
+        """The sequences that the buffers' next plans are for, one for each entry;
+        None: an entry without a sequence (StepBuffers: B = len(req_ids))."""
+        if len(req_ids) > bufs.max_batch:
+            raise ValueError("batch larger than the buffers")
+        live = [r for r in req_ids if r is not None]
+        if len(set(live)) != len(live):
+            raise ValueError("a sequence may be in a batch once")
+        with _on(stream):
+            bufs.copied.synchronize()  # do not overwrite pinned data a pending copy still reads
+            a = bufs.h_slot.numpy()
+            a[:] = -1
+            a[:len(req_ids)] = [-1 if r is None else self.cache.seqs[r].slot for r in req_ids]
+            bufs.slot.copy_(bufs.h_slot, non_blocking=True)
+            bufs.copied.record()
+        if isinstance(bufs, StepBuffers):
+            bufs.B = len(req_ids)
+
+    def plan(self, bufs, counts=None, stream=None) -> None:
+        """Plans counts[b] new tokens (a device int32 tensor; None: one each) of the
+        entries of ``use`` into the buffers: what ``plan_step`` or ``plan_chunk`` and
+        ``upload`` do from the host. What cannot be planned is an empty batch (see error_bits)."""
+        slots, plan = self._plan_of(bufs)
+        pkv.pkv_plan_batch(self.desc, slots, plan, counts, stream)
+
+    def commit(self, bufs, accepted=None, stream=None) -> None:
+        """Advances the sequences of the buffers' last plan by all, or accepted[b], of their new tokens."""
+        slots, plan = self._plan_of(bufs)
+        pkv.pkv_commit_batch(self.desc, slots, plan, accepted, stream)
+
+    def release(self, req_ids, stream=None) -> None:
+        """Gives the sequences' blocks back; they are empty afterwards. (``remove_sequence`` does this, too.)"""
+        if len(set(req_ids)) != len(req_ids):
+            raise ValueError("a sequence may be given back once")
+        with _on(stream):
+            slots = torch.tensor([self.cache.seqs[r].slot for r in req_ids], dtype=torch.int32, device=self.cache.device)
+            if slots.numel():
+                pkv.pkv_release_batch(self.desc, slots)
+
+    def error_bits(self) -> int:
+        """PKV_DEVERR_* bits of the plans, commits and releases since the last call (waits for the GPU)."""
+        bits = int(self.err.item())
+        if bits:
+            self.err.zero_()
+        return bits
+
+    def pull(self) -> None:
+        """Brings lists, lengths and the free list back to the host (waits for the GPU); the pool is done with."""
+        c = self.cache
+        if c.pool is not self:
+            raise RuntimeError("the cache's block lists are not in this pool")
+        torch.cuda.synchronize()
+        tables, lens, held, ring = (t.cpu().numpy() for t in (self.tables, self.lens, self.held, self.ring))
+        head, free = self.state[:2].tolist()
+        N = ring.size
+        order = [b for s in c.seqs.values() for b in tables[s.slot, :held[s.slot]].tolist()]
+        order += ring[(head + np.arange(free)) % N].tolist()
+        if sorted(order) != list(range(N)):
+            raise RuntimeError("the block lists on the GPU do not hold every block once")
+        # an allocator whose free list begins with the lists, in order, gives each back as it was
+        alloc = pkv.pkv_allocator_create(N, c.bs, order)
+        for s in c.seqs.values():
+            pkv.pkv_alloc(alloc, s.req_id, int(held[s.slot]))
+            s.length, s.planned = int(lens[s.slot]), 0
+        pkv.pkv_allocator_destroy(c._alloc)
+        c._alloc, c.pool, c.forked = alloc, None, False
