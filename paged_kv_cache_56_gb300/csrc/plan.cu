@@ -29,7 +29,7 @@ struct PoolView {
     int32_t* ring;
     int32_t* state;
     int32_t* err;
-    int32_t max_slots, max_blocks, num_blocks, bs, int8;
+    int32_t max_slots, max_blocks, num_blocks, bs, lg, int8;  // lg: bs = 1 << lg
 };
 
 struct PlanParams {
@@ -75,7 +75,7 @@ __device__ __forceinline__ Entry load_entry(const PlanParams& p, int e, int& bad
         x.n = 0;
         return x;
     }
-    const int64_t blocks = (int64_t(x.len) + x.n + p.pool.bs - 1) / p.pool.bs;
+    const int64_t blocks = (int64_t(x.len) + x.n + p.pool.bs - 1) >> p.pool.lg;
     if (blocks > p.pool.max_blocks) {
         bad |= kErrCtxLen;
         x.n = 0;
@@ -122,11 +122,18 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
             sh.warp[1][warp] = b;
         }
         __syncthreads();
-        long long a0 = row0, b0 = off0;
-        for (int w = 0; w < warp; ++w) {
-            a0 += sh.warp[0][w];
-            b0 += sh.warp[1][w];
+        constexpr int W = kPlanThreads / 32;
+        long long a0 = lane < W ? sh.warp[0][lane] : 0, b0 = lane < W ? sh.warp[1][lane] : 0;
+#pragma unroll
+        for (int o = 1; o < W; o <<= 1) {
+            const long long u = __shfl_up_sync(kFull, a0, o), v = __shfl_up_sync(kFull, b0, o);
+            if (lane >= o) {
+                a0 += u;
+                b0 += v;
+            }
         }
+        a0 = row0 + (warp > 0 ? __shfl_sync(kFull, a0, warp - 1) : 0);  // (of the warps before)
+        b0 = off0 + (warp > 0 ? __shfl_sync(kFull, b0, warp - 1) : 0);
         sh.entry[tid] = x;
         sh.start[tid] = a0 + a - x.n;
         sh.off[tid] = b0 + b - x.move;
@@ -136,6 +143,27 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
         }
         __syncthreads();
     };
+
+    // ---- this CTA's share of the tables (in words of one or four entries), entries and rows
+    const int G = gridDim.x, cta = blockIdx.x, mb = pool.max_blocks, vec = p.wide ? 4 : 1, wpr = mb / vec;  // words a row
+    const long long words = (long long)p.B * wpr;
+    const long long w0 = words * cta / G, w1 = words * (cta + 1) / G;
+    const int e0 = int((long long)p.B * cta / G), e1 = int((long long)p.B * (cta + 1) / G);
+    const int r0 = int((long long)p.rows * cta / G), r1 = int((long long)p.rows * (cta + 1) / G);
+    // A thread's first word of a list is on its way before the batch has been looked at: whatever
+    // the verdict, it lies inside the lists.
+    const auto entry_of = [&](long long w) {
+        return words <= 0x7FFFFFFF ? int(uint32_t(w) / uint32_t(wpr)) : int(w / wpr);
+    };
+    int4 ahead = make_int4(-1, -1, -1, -1);
+    if (!RELEASE && w0 + tid < w1) {
+        const int e = entry_of(w0 + tid), slot = p.slots[e];
+        const int32_t* list = pool.tables + size_t(slot) * mb + size_t(w0 + tid - (long long)e * wpr) * vec;
+        if (slot >= 0 && slot < pool.max_slots) {
+            if (p.wide) ahead = *reinterpret_cast<const int4*>(list);
+            else ahead.x = *list;
+        }
+    }
 
     // ---- what the batch needs, and whether it can be had
     const int tiles = (p.B + kPlanThreads - 1) / kPlanThreads;
@@ -186,12 +214,6 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     if (bad && blockIdx.x == 0 && tid == 0) report(pool.err, bad);
     if (RELEASE && bad) return;
 
-    // ---- this CTA's share of the tables (in words of one or four entries), entries and rows
-    const int G = gridDim.x, cta = blockIdx.x, mb = pool.max_blocks, vec = p.wide ? 4 : 1, wpr = mb / vec;  // words a row
-    const long long words = (long long)p.B * wpr;
-    const long long w0 = words * cta / G, w1 = words * (cta + 1) / G;
-    const int e0 = int((long long)p.B * cta / G), e1 = int((long long)p.B * (cta + 1) / G);
-    const int r0 = int((long long)p.rows * cta / G), r1 = int((long long)p.rows * (cta + 1) / G);
     // the i-th id from the ring's front (plan: taken) or end (release: given back)
     const auto place = [&](long long i) {
         i += (long long)head + (RELEASE ? free : 0);  // < 2 N
@@ -215,7 +237,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
             // tables
             const long long wa = max(w0, (long long)first * wpr), wb = min(w1, (long long)end * wpr);
             for (long long w = wa + tid; w < wb; w += kPlanThreads) {
-                const int e = int(w / wpr), c0 = int(w - (long long)e * wpr) * vec;
+                const int e = entry_of(w), c0 = int(w - (long long)e * wpr) * vec;
                 const Entry x = sh.entry[e - first];
                 const long long off = sh.off[e - first];
                 int32_t* list = pool.tables + size_t(max(0, x.slot)) * mb + c0;
@@ -229,8 +251,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
                 }
                 const int have = x.held + x.move;
                 int4 id = make_int4(-1, -1, -1, -1);
-                if (p.wide && c0 + 4 <= x.held) {
-                    id = *reinterpret_cast<const int4*>(list);
+                if (c0 + vec <= x.held) {
+                    if (w == w0 + tid) id = ahead;
+                    else if (p.wide) id = *reinterpret_cast<const int4*>(list);
+                    else id.x = *list;
                 } else if (c0 < have) {
                     int y[4] = {-1, -1, -1, -1};
                     for (int v = 0; v < vec; ++v) {
@@ -255,7 +279,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
                     p.out.token_starts[e + 1] = int(sh.start[e - first + 1]);
                     p.out.ctx_lens[e] = ctx;
                     if (p.out.fill_blocks)
-                        p.out.fill_blocks[e] = x.n > 0 && ctx % pool.bs == 0 ? block(e - first, ctx / pool.bs - 1) : -1;
+                        p.out.fill_blocks[e] = x.n > 0 && (ctx & (pool.bs - 1)) == 0 ? block(e - first, (ctx >> pool.lg) - 1) : -1;
                 }
                 if (cta == 0 && tid == 0 && t == 0) p.out.token_starts[0] = 0;
                 const int ra = max(r0, int(sh.start[0])), rb = min(r1, int(sh.start[kPlanThreads]));
@@ -268,8 +292,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
                     }
                     const Entry& x = sh.entry[lo];
                     const int pos = x.len + r - int(sh.start[lo]);
-                    if (p.out.block_ids) p.out.block_ids[r] = block(lo, pos / pool.bs);
-                    if (p.out.offsets) p.out.offsets[r] = pos % pool.bs;
+                    if (p.out.block_ids) p.out.block_ids[r] = block(lo, pos >> pool.lg);
+                    if (p.out.offsets) p.out.offsets[r] = pos & (pool.bs - 1);
                     if (p.out.token_slots) p.out.token_slots[r] = x.slot;
                     if (p.out.positions) p.out.positions[r] = pos;
                 }
@@ -352,7 +376,7 @@ int check_pool(const pkv_seq_pool* pool, PoolView* v) {
     if ((pool->block_size != 16 && pool->block_size != 64) || pool->max_slots > kMaxPoolSlots) return PKV_ERR_UNSUPPORTED;
     if (int64_t(pool->max_blocks) * pool->block_size >= (int64_t(1) << 31) - 65536) return PKV_ERR_INVALID;
     *v = PoolView{pool->tables, pool->lens, pool->held, pool->ring, pool->state, pool->err_word,
-                  pool->max_slots, pool->max_blocks, pool->num_blocks, pool->block_size, pool->int8};
+                  pool->max_slots, pool->max_blocks, pool->num_blocks, pool->block_size, pool->block_size == 16 ? 4 : 6, pool->int8};
     return PKV_OK;
 }
 

@@ -35,19 +35,22 @@
 // 595 to 600 us, 1670 TF/s, 640 us once the GPU has come to its power limit (cuBLAS:
 // 1930 and 1744); one of 16384 tokens, 32 and 8 heads, 2.2 TF in 1250 us, 1760 TF/s;
 // of 5000 to 8192 tokens, window 1024, 211 GF in 181 us; 32 of 16 to 4096 tokens,
-// 422 GF in 303 us; d = 64, two of 8000, 16 and 8 heads, 254 us, 1030 TF/s. A key tile
-// of both row tiles takes 2650 cycles, its multiplies 2048 by themselves and 2440 beside
-// the softmax (they read 192 KB of shared memory, at 128 bytes a cycle at most).
-// A tile's chain is 930 cycles of softmax (its 512 exponentials a warp take 512 of
-// them), 190 until the weights are announced, 200 until they are seen, 1220 of
-// multiplies. An item's beginning and end cost some 4000 cycles beside that, so windows
-// (ten tiles an item) and short prompts are further from the floor. Without the softmax
-// the first case takes 549 us.
+// 422 GF in 303 us (with inputs that are not in L2 652, 190 and 329 us); d = 64, two of
+// 8000, 16 and 8 heads, 254 us, 1030 TF/s. A key tile of both row tiles takes 2650
+// cycles, its multiplies 2048 by themselves and 2440 beside the softmax (they read 192
+// KB of shared memory, at 128 bytes a cycle at most). A tile's chain is 930 cycles of
+// softmax (a warp's 128 exponentials a thread take 512 of them), 190 until the weights
+// are announced, 200 until they are seen, 1220 of multiplies. An item's beginning and
+// end cost some 4000 cycles beside that, so windows (ten tiles an item) and short
+// prompts are further from the floor. Without the softmax the first case takes 549 us.
 // Other forms, the first case and the windowed one: a pair of CTAs with one row tile
 // each (cta_group::2, three tiles of scores ahead) 600 and 213 us; the multiplies of
 // each row tile by a warp of its own 824 and 222 (they interleave, and both end late);
 // outputs by four more warps 669 and 193 (registers); K waited for before O += P V
-// instead of behind it 644 and 183; three stages of K and V or four, the same.
+// instead of behind it 644 and 183; three stages of K and V or four, the same; hidden
+// scores selected in the plain tile's pass, without branches 609 and 184 (short
+// prompts 6% faster, d = 64 4% slower), with branches 673 and 199: a branch between two
+// chunks keeps one's end from overlapping the next one's beginning.
 #pragma once
 
 #include "ptx_tc.cuh"
@@ -579,6 +582,13 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
                 }
                 ++published;
                 if (x.kind == 0) {
+                    // its place is free only behind the last scores of the item before: to L2 meanwhile
+                    if (leader && loaded > 0) {
+                        for (int i = 0; i < 2; ++i)
+                            for (int h = 0; h < D / 64; ++h)
+                                if (x.r_first + i * kPrRows < x.r_end)
+                                    tma_prefetch_4d(&p.tm_q, h * 64, 0, x.kvh, x.row0 + ((x.r_first + i * kPrRows) >> lgG));
+                    }
                     if (loaded > 0 && !(ok = wait(&bars.q_empty, loaded - 1))) break;
                     if (leader) {
                         const int nq = x.r_end - x.r_first > kPrRows ? 2 : 1;

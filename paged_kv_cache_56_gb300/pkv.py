@@ -213,7 +213,7 @@ def _stream(stream) -> int:
 
 
 def _dev(t: torch.Tensor, name: str, dtype, min_numel: int = 0) -> int:
-    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
@@ -606,10 +606,11 @@ def _rows(t: torch.Tensor, name: str, batch: BatchDesc, heads: int, dim: int, dt
 # the current stream's handle without a Stream object around it, which costs
 # more than the launch of a small kernel
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _batch_stream(batch: BatchDesc, stream) -> int:
-    if batch.device.index != torch.cuda.current_device():
+    if batch.device.index != _current_device():
         raise ValueError(f"the batch is on {batch.device}, which is not the current device")
     if stream is None and _raw_stream is not None:
         return _raw_stream(batch.device.index)
