@@ -662,7 +662,8 @@ int pkv_set_programmatic_launch(int enable);
  * pkv_window_attention with up to 8 rows a kv head (max_tokens x group) does
  * the same, its first CTA being the first split of the first row tile; with 9 to
  * 16 rows it returns PKV_ERR_UNSUPPORTED; with more, whatever the shape, its
- * first CTA leaves out the copy of the queries of its work item of that index.
+ * first CTA leaves out the copy of the queries of its work item of that index, and
+ * so does pkv_prompt_attention's.
  * PKV_ERR_INVALID for tile < -1. Process-wide. */
 int pkv_debug_skip_copy(int32_t tile);
 

@@ -35,6 +35,7 @@ extern "C" int pkv_prompt_attention(const pkv_cache_desc* c, const pkv_batch_des
     p.out = static_cast<uint16_t*>(out);
     p.out_stride = out_stride;
     p.err = c->err_word;
+    p.skip_copy = g_skip_copy.load(std::memory_order_relaxed);
     p.Hq = hq;
     p.Hkv = hkv;
     p.window = window > 0 ? window : 0x7FFFFFFF;

@@ -234,6 +234,34 @@ def test_programmatic_launches():
     assert all(torch.equal(x, want) for x in outs)
 
 
+@pytest.mark.parametrize("heads", [(16, 8, 64), (16, 8, 128)])
+@pytest.mark.parametrize("item", [0, 1])
+def test_the_call_after_a_wait_that_ran_out_is_right(heads, item):
+    """The library's test hook leaves the queries of one item uncopied: the call reports it and returns."""
+    p = Prompts(59, [6000, 700], heads)  # 424 items: every CTA has two or three
+    want = p.run()
+    assert pkv.pkv_sync_status([p.lc.desc]) == 0
+    pkv.pkv_debug_skip_copy(item)
+    try:
+        p.run()
+        with pytest.raises(pkv.PkvError) as e:
+            pkv.pkv_sync_status([p.lc.desc])
+        assert e.value.code == pkv.PKV_ERR_DEVICE_TIMEOUT
+    finally:
+        pkv.pkv_debug_skip_copy(-1)
+    for _ in range(2):
+        assert torch.equal(p.run()[:p.T], want[:p.T])
+        assert pkv.pkv_sync_status([p.lc.desc]) == 0
+
+
+def test_contexts_need_no_block_table():
+    """Only that there are no earlier tokens matters: a table too short for the rows is not looked at."""
+    p = Prompts(61, [2000, 30], (8, 1, 64))
+    want = p.check()
+    p.batch = pkv.make_batch(p.starts, dev(np.zeros((2, 1))), p.ctx, num_tokens=p.T + p.behind, max_tokens=2000)
+    assert torch.equal(p.check(), want)
+
+
 def test_empty_calls():
     for new in ([], [0, 0]):
         p = Prompts(1, new, (4, 2, 64), behind=0)
