@@ -958,16 +958,18 @@ class DevicePool:
         B = bufs.B if isinstance(bufs, StepBuffers) else bufs.max_batch
         if B == 0:
             raise ValueError("use() the buffers first")
-        if getattr(bufs, "gpu_plan", None) is None or bufs.gpu_plan.B != B:
+        if getattr(bufs, "gpu_plans", None) is None:
             if torch.cuda.is_current_stream_capturing():
                 raise RuntimeError("plan the batch once before capturing it")
-            if isinstance(bufs, StepBuffers):
-                starts = torch.zeros(B + 1, dtype=torch.int32, device=self.cache.device)
-                bufs.gpu_plan = pkv.make_plan(starts, bufs.tab[:B], bufs.ctx[:B], num_tokens=B, max_tokens=1)
-            else:
-                bufs.gpu_plan = pkv.make_plan(bufs.starts, bufs.tab, bufs.ctx, num_tokens=bufs.max_tokens,
-                                              max_tokens=bufs.max_new)
-        return bufs.slot[:B], bufs.gpu_plan
+            # one array for every B: captured steps of several batch sizes keep writing to it
+            bufs.gpu_plans = {}
+            bufs.gpu_starts = (torch.zeros(bufs.max_batch + 1, dtype=torch.int32, device=self.cache.device)
+                               if isinstance(bufs, StepBuffers) else bufs.starts)
+        if B not in bufs.gpu_plans:
+            rows, new = (B, 1) if isinstance(bufs, StepBuffers) else (bufs.max_tokens, bufs.max_new)
+            bufs.gpu_plans[B] = pkv.make_plan(bufs.gpu_starts[:B + 1], bufs.tab[:B], bufs.ctx[:B], num_tokens=rows,
+                                              max_tokens=new)
+        return bufs.slot[:B], bufs.gpu_plans[B]
 
     def use(self, bufs, req_ids, stream=None) -> None:
         """The sequences that the buffers' next plans are for, one for each entry;
