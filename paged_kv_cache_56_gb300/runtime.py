@@ -607,6 +607,8 @@ class GraphStep:
         torch.cuda.synchronize()
 
     def replay(self) -> None:
+        if self.pool is not None:
+            self.pool._alive()  # the graph would plan from lists that are not the cache's any more
         self.graph.replay()
 
 
@@ -954,7 +956,12 @@ class DevicePool:
         torch.cuda.synchronize()  # there, whichever stream plans first
         cache.pool = self
 
+    def _alive(self) -> None:
+        if self.cache.pool is not self:
+            raise RuntimeError("the cache's block lists are not in this pool")
+
     def _plan_of(self, bufs):
+        self._alive()
         B = bufs.B if isinstance(bufs, StepBuffers) else bufs.max_batch
         if B == 0:
             raise ValueError("use() the buffers first")
@@ -973,7 +980,10 @@ class DevicePool:
 
     def use(self, bufs, req_ids, stream=None) -> None:
         """The sequences that the buffers' next plans are for, one for each entry;
-        None: an entry without a sequence (StepBuffers: B = len(req_ids))."""
+        None: an entry without a sequence (StepBuffers: B = len(req_ids)). Once one of them
+        has been removed, use() comes before the next plan or replay: its slot is
+        another's."""
+        self._alive()
         if len(req_ids) > bufs.max_batch:
             raise ValueError("batch larger than the buffers")
         live = [r for r in req_ids if r is not None]
@@ -1002,7 +1012,8 @@ class DevicePool:
         pkv.pkv_commit_batch(self.desc, slots, plan, accepted, stream)
 
     def release(self, req_ids, stream=None) -> None:
-        """Gives the sequences' blocks back; they are empty afterwards. (``remove_sequence`` does this, too.)"""
+        """Gives the sequences' blocks back; they are empty afterwards. (``remove_sequence`` does this, too, on the current stream.)"""
+        self._alive()
         if len(set(req_ids)) != len(req_ids):
             raise ValueError("a sequence may be given back once")
         with _on(stream):
@@ -1019,9 +1030,8 @@ class DevicePool:
 
     def pull(self) -> None:
         """Brings lists, lengths and the free list back to the host (waits for the GPU); the pool is done with."""
+        self._alive()
         c = self.cache
-        if c.pool is not self:
-            raise RuntimeError("the cache's block lists are not in this pool")
         torch.cuda.synchronize()
         tables, lens, held, ring = (t.cpu().numpy() for t in (self.tables, self.lens, self.held, self.ring))
         head, free = self.state[:2].tolist()

@@ -56,3 +56,23 @@ def test_captured_steps_of_two_batch_sizes_share_their_buffers(int8):
     assert pool.error_bits() == 0 and all(lc.error_bits() == 0 for lc in gpu.layers)
     pool.pull()
     caches_are_the_same(gpu, host)
+
+
+def test_a_pulled_pool_plans_nothing():
+    c = make_cache(False)
+    begin(c, [20, 33], 71)
+    bufs, pool = StepBuffers(c, 2), DevicePool(c)
+    pool.use(bufs, [0, 1])
+    step = GraphStep(c, bufs, SCALE, pool=pool)
+    step.run_eager()
+    step.capture()
+    step.replay()
+    pool.pull()
+    for again in (False, True):  # a pool of its own later on does not bring the old one back
+        newer = DevicePool(c) if again else None
+        for call in (lambda: pool.use(bufs, [0, 1]), lambda: pool.plan(bufs), lambda: pool.commit(bufs),
+                     lambda: pool.release([0]), pool.pull, step.replay, step.run_eager):
+            with pytest.raises(RuntimeError, match="not in this pool"):
+                call()
+    newer.pull()
+    assert [c.seqs[r].length for r in (0, 1)] == [22, 35]
