@@ -801,7 +801,8 @@ class AxisPositions:
     """Rotary positions (time, height, width) of the tokens of prompts with images
     and video. Every sequence has a list of segments {t, h, w, step} (see
     ``pkv_axis_positions``), kept on the GPU by its slot; ``update`` works out the
-    positions of an uploaded (or planned) batch's tokens. The tensor ``positions`` [3, max_tokens] is
+    positions of an uploaded (or planned) batch's tokens. Slots are used again: set() every
+    new sequence, with [] where it is all text. The tensor ``positions`` [3, max_tokens] is
     always the same, so that a rotary descriptor made of it stays good."""
 
     def __init__(self, cache: PagedKVCache, max_tokens: int, max_segments: int):
@@ -895,6 +896,7 @@ def read_back(cache: PagedKVCache, layer: int, req_ids, dtype=torch.bfloat16, st
 
 
 def _read_back(cache: PagedKVCache, layer: int, req_ids, dtype):
+    cache._lengths_are_here()
     lens = [cache.seqs[r].length for r in req_ids]
     starts = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
     T, dev = int(starts[-1]), cache.layers[layer].k_pool.device

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from libpkv import ensure_built
-from paged_kv_cache_56_gb300.runtime import DevicePool, GraphStep, StepBuffers, decode_step
+from paged_kv_cache_56_gb300.runtime import DevicePool, GraphStep, StepBuffers, decode_step, read_back
 from test_gpu_planned import HEADS, assert_same_rows, begin, caches_are_the_same, make_cache, rows
 
 pytestmark = pytest.mark.gpu
@@ -76,3 +76,16 @@ def test_a_pulled_pool_plans_nothing():
                 call()
     newer.pull()
     assert [c.seqs[r].length for r in (0, 1)] == [22, 35]
+
+
+def test_a_sequence_that_began_on_the_gpu_is_not_read_back_as_empty():
+    c = make_cache(False)
+    c.add_sequence(0)
+    bufs, pool = StepBuffers(c, 1), DevicePool(c)
+    pool.use(bufs, [0])
+    step = GraphStep(c, bufs, SCALE, pool=pool)
+    step.run_eager()
+    with pytest.raises(RuntimeError, match="GPU"):
+        read_back(c, 0, [0])
+    pool.pull()
+    assert read_back(c, 0, [0])[0].shape[0] == 1
