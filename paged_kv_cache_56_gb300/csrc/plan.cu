@@ -10,7 +10,14 @@
 // front of the list on. All CTAs come to the same verdict about the batch, so that all
 // of them make the plan or none does. New ids go into the pool's lists by the CTA
 // that copies that part of the table; numbers that others still read (held,
-// the ring's front) are changed by the CTA that is last to arrive.
+// the ring's front) are changed by the CTA that is last to arrive. A thread's first
+// word of a list is read before the sums are there (its place depends on the slot alone).
+//
+// Bound by latency: launch, slots -> lengths -> sums (two barriers) -> lists. In a
+// graph 5.3 us for 4 entries, 5.4 us for 144 entries with tables of 1024 blocks (0.7
+// MB), 6.4 to 7.0 us for 512 entries that bring 1 to 200 tokens each (2.9 MB; 0.4 us at the
+// memory's rate). Called one by one from Python 9 to 12 us: the call. Entries are
+// taken 512 at a time, twice when there are more: 1024 take 7.7 us, 4096 18 us, 8192 38 us.
 #include <algorithm>
 
 #include "batch.cuh"

@@ -6,6 +6,11 @@
 // each segment's first token and base, and the CTA's tokens that fall into the
 // tile find their segment by bisection in shared memory. It ends with the tile that
 // holds its last token, or with the list; tokens behind that are text.
+//
+// Bound by latency: 3.0 us in a graph for 128 single tokens behind 24 segments, 4.9 us
+// for 53600 tokens of 8 prompts with 48 segments (0.65 MB; 0.1 us at the memory's rate):
+// launch, lengths -> number of segments -> segments -> two sums, then eight
+// steps of the bisection a token.
 #include "batch.cuh"
 #include "host.h"
 

@@ -33,7 +33,7 @@
 //
 // Measured, d = 128: prompts of 7400 to 8000 tokens, 16 query and 8 kv heads, 1.0 TF in
 // 595 to 600 us, 1670 TF/s, 640 us once the GPU has come to its power limit (cuBLAS:
-// 1930 and 1744); one of 16384 tokens, 32 and 8 heads, 2.2 TF in 1250 us, 1760 TF/s;
+// 1897 and 1699); one of 16384 tokens, 32 and 8 heads, 2.2 TF in 1250 us, 1760 TF/s;
 // of 5000 to 8192 tokens, window 1024, 211 GF in 181 us; 32 of 16 to 4096 tokens,
 // 422 GF in 303 us (with inputs that are not in L2 652, 190 and 329 us); d = 64, two of
 // 8000, 16 and 8 heads, 254 us, 1030 TF/s. A key tile of both row tiles takes 2650
@@ -47,7 +47,7 @@
 // each (cta_group::2, three tiles of scores ahead) 600 and 213 us; the multiplies of
 // each row tile by a warp of its own 824 and 222 (they interleave, and both end late);
 // outputs by four more warps 669 and 193 (registers); K waited for before O += P V
-// instead of behind it 644 and 183; three stages of K and V or four, the same; hidden
+// instead of behind it 644 to 660 and 190; three stages of K and V or four, the same; hidden
 // scores selected in the plain tile's pass, without branches 609 and 184 (short
 // prompts 6% faster, d = 64 4% slower), with branches 673 and 199: a branch between two
 // chunks keeps one's end from overlapping the next one's beginning.
@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
     const int G = p.Hq / p.Hkv, lgG = 31 - __clz(G);
     uint8_t* q_smem = smem + ((1024u - (smem_addr(smem) & 1023u)) & 1023u);
     const uint32_t q_addr = smem_addr(q_smem), kv_addr = q_addr + 2 * T::kTileBytes;
-    const uint32_t stage0 = kv_addr + STAGES * T::kTileBytes;  // 4 KB a softmax warp, for its output rows
+    const uint32_t stage0 = kv_addr + STAGES * T::kTileBytes;  // kOutBytes a softmax warp, for its output rows
     const uint32_t bar0 = smem_addr(&bars);
     const auto bar = [&](const uint64_t* x) {
         return bar0 + uint32_t(reinterpret_cast<const uint8_t*>(x) - reinterpret_cast<const uint8_t*>(&bars));
