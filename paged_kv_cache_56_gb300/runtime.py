@@ -974,6 +974,7 @@ class DevicePool:
             bufs.gpu_plans = {}
             bufs.gpu_starts = (torch.zeros(bufs.max_batch + 1, dtype=torch.int32, device=self.cache.device)
                                if isinstance(bufs, StepBuffers) else bufs.starts)
+            torch.cuda.synchronize()  # zeroed, whichever stream plans into it
         if B not in bufs.gpu_plans:
             rows, new = (B, 1) if isinstance(bufs, StepBuffers) else (bufs.max_tokens, bufs.max_new)
             bufs.gpu_plans[B] = pkv.make_plan(bufs.gpu_starts[:B + 1], bufs.tab[:B], bufs.ctx[:B], num_tokens=rows,
