@@ -16,6 +16,7 @@ binding. A decode step for B running sequences is:
 from __future__ import annotations
 
 import math
+import weakref
 from collections import Counter
 from dataclasses import dataclass
 
@@ -205,7 +206,9 @@ class PagedKVCache:
     def remove_sequence(self, req_id: int) -> None:
         if self.pool is not None:
             self.pool.release([req_id])
-            self.free_slots.append(self.seqs.pop(req_id).slot)
+            slot = self.seqs.pop(req_id).slot
+            self.pool._forget(slot)
+            self.free_slots.append(slot)
             return
         s = self.seqs.pop(req_id)
         pkv.pkv_free(self.alloc, req_id)
@@ -952,6 +955,7 @@ class DevicePool:
         def up(a):
             return torch.from_numpy(np.ascontiguousarray(a, np.int32)).to(cache.device)
         self.cache = cache
+        self._used = weakref.WeakSet()  # buffers that use() has been called with
         self.tables, self.lens, self.held, self.ring = up(tables), up(lens), up(held), up(ring)
         self.state, self.err = up([0, len(free), 0, 0]), up([0])
         self.desc = pkv.make_seq_pool(self.tables, self.lens, self.held, self.ring, self.state, block_size=cache.bs,
@@ -984,9 +988,9 @@ class DevicePool:
 
     def use(self, bufs, req_ids, stream=None) -> None:
         """The sequences that the buffers' next plans are for, one for each entry;
-        None: an entry without a sequence (StepBuffers: B = len(req_ids)). Once one of them
-        has been removed, use() comes before the next plan or replay: its slot is
-        another's."""
+        None: an entry without a sequence (StepBuffers: B = len(req_ids)). The entry of a
+        sequence that is removed from the cache becomes one without a sequence (on the
+        stream that is then the current one), in captured steps, too."""
         self._alive()
         if len(req_ids) > bufs.max_batch:
             raise ValueError("batch larger than the buffers")
@@ -1000,8 +1004,21 @@ class DevicePool:
             a[:len(req_ids)] = [-1 if r is None else self.cache.seqs[r].slot for r in req_ids]
             bufs.slot.copy_(bufs.h_slot, non_blocking=True)
             bufs.copied.record()
+        self._used.add(bufs)
         if isinstance(bufs, StepBuffers):
             bufs.B = len(req_ids)
+
+    def _forget(self, slot: int) -> None:
+        """Takes a slot that nobody has any more out of the buffers that are used with it:
+        a plan, captured or not, would give it blocks and tokens, and the next sequence that gets
+        the slot would begin with them."""
+        for bufs in self._used:
+            bufs.copied.synchronize()  # do not overwrite pinned data a pending copy still reads
+            a = bufs.h_slot.numpy()
+            if (a == slot).any():
+                a[a == slot] = -1
+                bufs.slot.copy_(bufs.h_slot, non_blocking=True)
+                bufs.copied.record()
 
     def plan(self, bufs, counts=None, stream=None) -> None:
         """Plans counts[b] new tokens (a device int32 tensor; None: one each) of the

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from libpkv import ensure_built
-from paged_kv_cache_56_gb300.runtime import AxisPositions, ChunkBuffers, DevicePool, StepBuffers
+from paged_kv_cache_56_gb300.runtime import AxisPositions, ChunkBuffers, DevicePool, GraphStep, StepBuffers, read_back
 from test_gpu_axes import positions_of
 from test_gpu_planned import begin, make_cache
 
@@ -55,3 +55,53 @@ def test_axis_positions_set_on_another_stream():
     where.update(bufs, stream=side)
     torch.cuda.synchronize()
     assert np.array_equal(where.positions.cpu().numpy(), positions_of(segs, 40)) and where.err.item() == 0
+
+
+@pytest.mark.parametrize("int8", [False, True])
+def test_a_removed_sequence_is_not_stepped(int8):
+    """A captured step replayed after one of its sequences was removed, without use() in between: the
+    others go on, the slot stays empty, and the next sequence that gets it begins empty."""
+    c = make_cache(int8)
+    begin(c, [20, 33, 47], 71)
+    steps, chunks, pool = StepBuffers(c, 3), ChunkBuffers(c, 4, 8, 2), DevicePool(c)
+    pool.use(steps, [2, 0, 1])
+    pool.use(chunks, [1, 0])
+    step = GraphStep(c, steps, 0.1, pool=pool)
+    step.run_eager()
+    step.capture()
+    step.replay()
+    slot, free = c.seqs[1].slot, pool.state[1].item()
+    c.remove_sequence(1)
+    assert pool.state[1].item() == free + 3  # 35 tokens
+    step.out.fill_(7.0)
+    step.replay()
+    assert (step.out[:, 2] == 0).all() and (step.out[:, :2] != 7).any()
+    pool.plan(chunks, torch.tensor([2, 2, 2, 2], dtype=torch.int32, device="cuda"))
+    assert chunks.starts.tolist() == [0, 0, 2, 2, 2]  # the entry of 0 alone: the one of 1 has no sequence now
+    assert pool.lens[slot].item() == pool.held[slot].item() == 0
+    while slot in c.free_slots:  # the last of them gets the slot
+        c.add_sequence(10 + len(c.seqs))
+    step.replay()
+    assert pool.error_bits() == 0 and all(lc.error_bits() == 0 for lc in c.layers)
+    pool.pull()
+    assert lengths(c) == [24, 51, 0, 0, 0, 0]
+    assert all(read_back(c, 0, [r])[0].shape[0] == c.seqs[r].length for r in c.seqs)
+
+
+def test_buffers_that_are_gone_are_forgotten():
+    c = make_cache(False)
+    begin(c, [20, 33], 71)
+    a, b, pool = StepBuffers(c, 2), StepBuffers(c, 2), DevicePool(c)
+    pool.use(a, [0, 1])
+    pool.use(b, [1])
+    del b
+    c.remove_sequence(1)
+    assert a.slot.tolist() == [c.seqs[0].slot, -1]
+    pool.use(a, [None, 0])  # a sequence that was not there is not looked for
+    c.remove_sequence(0)
+    assert a.slot.tolist() == [-1, -1]
+    pool.plan(a)
+    pool.commit(a)
+    assert a.ctx.tolist() == [0, 0] and pool.error_bits() == 0
+    pool.pull()
+    assert not c.seqs and len(c.free_slots) == 6
