@@ -541,8 +541,9 @@ class GraphStep:
     (R > 1 re-reads the same layer's cache with R different queries). The
     quantize kernel is always launched over a -1-padded fill list so that the
     graph does not change from step to step. The batch size is fixed at
-    capture time. With a DevicePool (after ``pool.use``) the graph also holds the
-    step's plan and commit.
+    capture time: a replay while the buffers hold more entries is refused. With a
+    DevicePool (after ``pool.use``) the graph also holds the step's plan and commit, and
+    entries behind those of a smaller ``use`` bring nothing.
     """
 
     def __init__(self, cache: PagedKVCache, bufs: StepBuffers, sm_scale: float, repeat: int = 1,
@@ -562,6 +563,7 @@ class GraphStep:
         self.out = torch.zeros((L * repeat, B, cache.hq, cache.d), dtype=torch.bfloat16, device=dev)
         self.graph = None
         self.attn_graph = None
+        self.captured = 0  # entries of the captured step
 
     def launches_per_step(self) -> int:
         per_attn = 2 if (self.bufs.split_tokens and self.bufs.ws_count is None) else 1
@@ -572,6 +574,8 @@ class GraphStep:
     def _layers(self, attention_only: bool = False) -> None:
         c, b = self.cache, self.bufs
         B = b.B
+        if B > self.q.shape[1]:
+            raise ValueError(f"the step is for {self.q.shape[1]} entries, the buffers hold {B}")
         planned = self.pool is not None and not attention_only
         if planned:
             self.pool.plan(b)
@@ -601,6 +605,7 @@ class GraphStep:
         """Captures the step (and an attention-only variant used for timing).
         Call after one eager step so every kernel attribute is already set."""
         torch.cuda.synchronize()
+        self.captured = self.bufs.B
         self.graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(self.graph):
             self._layers()
@@ -612,6 +617,8 @@ class GraphStep:
     def replay(self) -> None:
         if self.pool is not None:
             self.pool._alive()  # the graph would plan from lists that are not the cache's any more
+        if self.bufs.B > self.captured:
+            raise ValueError(f"the step was captured for {self.captured} entries, the buffers hold {self.bufs.B}")
         self.graph.replay()
 
 

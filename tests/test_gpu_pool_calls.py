@@ -105,3 +105,26 @@ def test_buffers_that_are_gone_are_forgotten():
     assert a.ctx.tolist() == [0, 0] and pool.error_bits() == 0
     pool.pull()
     assert not c.seqs and len(c.free_slots) == 6
+
+
+def test_a_step_captured_for_fewer_entries_is_refused():
+    """A replay after use() of more sequences than the step was captured for would leave the last ones where they are."""
+    c = make_cache(False)
+    begin(c, [20, 33, 47], 71)
+    bufs, pool = StepBuffers(c, 3), DevicePool(c)
+    pool.use(bufs, [0, 1])
+    step = GraphStep(c, bufs, 0.1, pool=pool)
+    step.run_eager()
+    step.capture()
+    pool.use(bufs, [2, 0, 1])
+    for call in (step.replay, step.run_eager):
+        with pytest.raises(ValueError, match="entries"):
+            call()
+    pool.use(bufs, [2])
+    step.replay()
+    step.replay()
+    pool.use(bufs, [1, 2])
+    step.replay()
+    assert pool.error_bits() == 0
+    pool.pull()
+    assert lengths(c) == [21, 35, 50]
