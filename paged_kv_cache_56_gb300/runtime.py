@@ -1030,7 +1030,11 @@ class DevicePool:
     def plan(self, bufs, counts=None, stream=None) -> None:
         """Plans counts[b] new tokens (a device int32 tensor; None: one each) of the
         entries of ``use`` into the buffers: what ``plan_step`` or ``plan_chunk`` and
-        ``upload`` do from the host. What cannot be planned is an empty batch (see error_bits)."""
+        ``upload`` do from the host. What cannot be planned is an empty batch (see error_bits).
+        StepBuffers take no counts: a step's kernels write a token of every entry that has
+        one, so an entry without a new one would have its last token written over."""
+        if counts is not None and isinstance(bufs, StepBuffers):
+            raise ValueError("a step brings one token an entry: use() without the sequences that bring none")
         slots, plan = self._plan_of(bufs)
         pkv.pkv_plan_batch(self.desc, slots, plan, counts, stream)
 

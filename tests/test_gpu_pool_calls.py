@@ -128,3 +128,19 @@ def test_a_step_captured_for_fewer_entries_is_refused():
     assert pool.error_bits() == 0
     pool.pull()
     assert lengths(c) == [21, 35, 50]
+
+
+def test_a_step_takes_no_counts():
+    """An entry of a step that brought no token would have its last one written over."""
+    c = make_cache(False)
+    begin(c, [20, 33], 71)
+    bufs, chunks, pool = StepBuffers(c, 2), ChunkBuffers(c, 2, 2, 1), DevicePool(c)
+    counts = torch.tensor([1, 0], dtype=torch.int32, device="cuda")
+    for b in (bufs, chunks):
+        pool.use(b, [0, 1])
+    with pytest.raises(ValueError, match="one token"):
+        pool.plan(bufs, counts)
+    pool.plan(chunks, counts)  # the chunk operators write new tokens alone
+    pool.commit(chunks)
+    pool.pull()
+    assert lengths(c) == [21, 33]
