@@ -509,7 +509,10 @@ def run_layers(cache: PagedKVCache, bufs: StepBuffers, q, k_new, v_new, out, sm_
 
     quantize="auto" launches the quantize kernel only when the plan has a
     filled block; "always" launches it every step over a -1-padded list (the
-    form a captured CUDA graph needs)."""
+    form a captured CUDA graph needs). Rows go where an uploaded plan says: a DevicePool's
+    plans leave those arrays as they were, and RuntimeError is raised while the cache has one
+    (``GraphStep`` runs its steps)."""
+    cache._lengths_are_here()
     B = bufs.B
     for li, lc in enumerate(cache.layers):
         pkv.pkv_append_kv(lc.desc, k_new[li], v_new[li], bufs.blk[:B], bufs.off[:B], bufs.slot[:B], stream)
@@ -571,9 +574,15 @@ class GraphStep:
             return self.cache.L * self.R * per_attn + (2 if self.pool is not None else 0)
         return sum(1 + int(f) + self.R * per_attn for f in self.cache.layer_int8)
 
+    def _kernels_are_for_the_plan(self) -> None:
+        if not self.fused:  # they write where an uploaded plan says
+            self.cache._lengths_are_here()
+
     def _layers(self, attention_only: bool = False) -> None:
         c, b = self.cache, self.bufs
         B = b.B
+        if not attention_only:
+            self._kernels_are_for_the_plan()
         if B > self.q.shape[1]:
             raise ValueError(f"the step is for {self.q.shape[1]} entries, the buffers hold {B}")
         planned = self.pool is not None and not attention_only
@@ -604,19 +613,20 @@ class GraphStep:
     def capture(self) -> None:
         """Captures the step (and an attention-only variant used for timing).
         Call after one eager step so every kernel attribute is already set."""
+        self._kernels_are_for_the_plan()
         torch.cuda.synchronize()
-        self.captured = self.bufs.B
-        self.graph = torch.cuda.CUDAGraph()
-        with torch.cuda.graph(self.graph):
+        graph, attn_graph = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
             self._layers()
-        self.attn_graph = torch.cuda.CUDAGraph()
-        with torch.cuda.graph(self.attn_graph):
+        with torch.cuda.graph(attn_graph):
             self._layers(attention_only=True)
         torch.cuda.synchronize()
+        self.graph, self.attn_graph, self.captured = graph, attn_graph, self.bufs.B
 
     def replay(self) -> None:
         if self.pool is not None:
             self.pool._alive()  # the graph would plan from lists that are not the cache's any more
+        self._kernels_are_for_the_plan()
         if self.bufs.B > self.captured:
             raise ValueError(f"the step was captured for {self.captured} entries, the buffers hold {self.bufs.B}")
         self.graph.replay()

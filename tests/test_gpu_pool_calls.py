@@ -6,9 +6,9 @@ import pytest
 import torch
 
 from libpkv import ensure_built
-from paged_kv_cache_56_gb300.runtime import AxisPositions, ChunkBuffers, DevicePool, GraphStep, StepBuffers, read_back
+from paged_kv_cache_56_gb300.runtime import AxisPositions, ChunkBuffers, DevicePool, GraphStep, StepBuffers, decode_step, read_back, run_layers
 from test_gpu_axes import positions_of
-from test_gpu_planned import begin, make_cache
+from test_gpu_planned import HEADS, begin, make_cache, rows
 
 pytestmark = pytest.mark.gpu
 
@@ -144,3 +144,31 @@ def test_a_step_takes_no_counts():
     pool.commit(chunks)
     pool.pull()
     assert lengths(c) == [21, 33]
+
+
+@pytest.mark.parametrize("int8", [False, True])
+def test_unfused_steps_need_a_plan_of_the_host(int8):
+    """The kernels that append and attend apart take block, offset and fill block of each row from an upload; what
+    a pool plans does not say them, and the last upload's would be written over."""
+    c = make_cache(int8)
+    begin(c, [20, 33], 71)
+    bufs = StepBuffers(c, 2)
+    q, k, v = (rows(80 + i, 2, 2, h) for i, h in enumerate((HEADS[0], HEADS[1], HEADS[1])))
+    decode_step(c, bufs, [0, 1], q, k, v, torch.empty_like(q), 0.1)
+    unfused = GraphStep(c, bufs, 0.1, fused=False)
+    unfused.capture()
+    before = [read_back(c, 1, [r]) for r in (0, 1)]
+    pool = DevicePool(c)
+    pool.use(bufs, [1, 0])
+    pool.plan(bufs)
+    for call in (lambda: run_layers(c, bufs, q, k, v, torch.empty_like(q), 0.1, "always"), unfused.run_eager, unfused.replay,
+                 unfused.capture):
+        with pytest.raises(RuntimeError, match="GPU"):
+            call()
+    torch.cuda.synchronize()
+    pool.pull()
+    assert lengths(c) == [21, 34]
+    for r in (0, 1):
+        assert all(torch.equal(x, y) for x, y in zip(read_back(c, 1, [r])[:2], before[r][:2]))
+    decode_step(c, bufs, [0, 1], q, k, v, torch.empty_like(q), 0.1)
+    assert lengths(c) == [22, 35]
