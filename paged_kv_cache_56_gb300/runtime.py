@@ -987,7 +987,7 @@ class DevicePool:
     def _plan_of(self, bufs):
         self._alive()
         B = bufs.B if isinstance(bufs, StepBuffers) else bufs.max_batch
-        if B == 0:
+        if B == 0 or bufs not in self._used:  # (their slots may be those of sequences long gone, or zeros)
             raise ValueError("use() the buffers first")
         if getattr(bufs, "gpu_plans", None) is None:
             if torch.cuda.is_current_stream_capturing():

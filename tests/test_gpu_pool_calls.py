@@ -172,3 +172,29 @@ def test_unfused_steps_need_a_plan_of_the_host(int8):
         assert all(torch.equal(x, y) for x, y in zip(read_back(c, 1, [r])[:2], before[r][:2]))
     decode_step(c, bufs, [0, 1], q, k, v, torch.empty_like(q), 0.1)
     assert lengths(c) == [22, 35]
+
+
+def test_only_buffers_that_were_used_with_the_pool_are_planned():
+    """Slots that are not from this pool's use() -- zeros, an upload's, an earlier pool's -- name sequences
+    that nobody asked for."""
+    c = make_cache(False)
+    begin(c, [20, 33], 71)
+    fresh, steps = ChunkBuffers(c, 1, 4, 4), StepBuffers(c, 2)
+    q, k, v = (rows(80 + i, 2, 2, h) for i, h in enumerate((HEADS[0], HEADS[1], HEADS[1])))
+    decode_step(c, steps, [0, 1], q, k, v, torch.empty_like(q), 0.1)
+    pool = DevicePool(c)
+    for again in (False, True):
+        for bufs in (fresh, steps):
+            for call in (pool.plan, pool.commit):
+                with pytest.raises(ValueError, match="use"):
+                    call(bufs)
+        if not again:
+            pool.use(fresh, [1])
+            pool.use(steps, [0])
+            pool.plan(fresh)
+            pool.commit(fresh)
+            pool.pull()
+            pool = DevicePool(c)
+    assert pool.error_bits() == 0
+    pool.pull()
+    assert lengths(c) == [21, 35]
