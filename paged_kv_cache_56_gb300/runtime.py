@@ -1009,6 +1009,8 @@ class DevicePool:
         sequence that is removed from the cache becomes one without a sequence (on the
         stream that is then the current one), in captured steps, too."""
         self._alive()
+        if bufs.cache is not self.cache:
+            raise ValueError("the buffers are another cache's")
         if len(req_ids) > bufs.max_batch:
             raise ValueError("batch larger than the buffers")
         live = [r for r in req_ids if r is not None]

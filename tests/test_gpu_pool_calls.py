@@ -198,3 +198,16 @@ def test_only_buffers_that_were_used_with_the_pool_are_planned():
     assert pool.error_bits() == 0
     pool.pull()
     assert lengths(c) == [21, 35]
+
+
+def test_buffers_of_another_cache_are_refused():
+    """They would get this cache's blocks, and steps over them read and write the other's."""
+    c, other = make_cache(False), make_cache(False)
+    begin(c, [20, 33], 71)
+    begin(other, [5], 72)
+    pool = DevicePool(c)
+    for bufs in (StepBuffers(other, 2), ChunkBuffers(other, 2, 4, 2)):
+        with pytest.raises(ValueError, match="another cache"):
+            pool.use(bufs, [0])
+    pool.pull()
+    assert lengths(c) == [20, 33] and lengths(other) == [5]
