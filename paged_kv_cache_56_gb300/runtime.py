@@ -1067,6 +1067,7 @@ class DevicePool:
 
     def error_bits(self) -> int:
         """PKV_DEVERR_* bits of the plans, commits and releases since the last call (waits for the GPU)."""
+        torch.cuda.synchronize(self.err.device)  # whichever streams they are on
         bits = int(self.err.item())
         if bits:
             self.err.zero_()

@@ -6,6 +6,7 @@ import pytest
 import torch
 
 from libpkv import ensure_built
+from paged_kv_cache_56_gb300 import pkv
 from paged_kv_cache_56_gb300.runtime import AxisPositions, ChunkBuffers, DevicePool, GraphStep, StepBuffers, decode_step, read_back, run_layers
 from test_gpu_axes import positions_of
 from test_gpu_planned import HEADS, begin, make_cache, rows
@@ -211,3 +212,20 @@ def test_buffers_of_another_cache_are_refused():
             pool.use(bufs, [0])
     pool.pull()
     assert lengths(c) == [20, 33] and lengths(other) == [5]
+
+
+def test_error_bits_of_plans_on_another_stream():
+    """They wait for every stream: a plan that is still to come on another one has its say."""
+    c = make_cache(False, blocks=5)
+    begin(c, [33, 30], 71)
+    bufs, pool, side = ChunkBuffers(c, 2, 8, 4), DevicePool(c), torch.cuda.Stream()
+    pool.use(bufs, [0, 1])
+    counts = torch.tensor([4, 4], dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)  # cycles: some 10 ms
+        pool.plan(bufs, counts)  # the second sequence's third block is not there
+    assert pool.error_bits() == pkv.PKV_DEVERR_OOM
+    assert pool.error_bits() == 0
+    pool.pull()
+    assert lengths(c) == [33, 30]
