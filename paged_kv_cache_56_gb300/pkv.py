@@ -391,8 +391,13 @@ def pkv_debug_skip_copy(tile: int) -> None:
     _check("pkv_debug_skip_copy", lib().pkv_debug_skip_copy(tile))
 
 
+programmatic_launch = False  # as last set here
+
+
 def pkv_set_programmatic_launch(enable: bool) -> None:
+    global programmatic_launch
     _check("pkv_set_programmatic_launch", lib().pkv_set_programmatic_launch(1 if enable else 0))
+    programmatic_launch = bool(enable)
 
 
 def pkv_splitk_ws_o_bytes(B: int, Hq: int, head_dim: int, max_splits: int) -> int:

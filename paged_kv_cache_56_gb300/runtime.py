@@ -571,7 +571,9 @@ class GraphStep:
     def launches_per_step(self) -> int:
         per_attn = 2 if (self.bufs.split_tokens and self.bufs.ws_count is None) else 1
         if self.fused:
-            return self.cache.L * self.R * per_attn + (2 if self.pool is not None else 0)
+            # plan and commit, and the empty kernel behind a plan with programmatic launch on
+            planned = 2 + int(pkv.programmatic_launch) if self.pool is not None else 0
+            return self.cache.L * self.R * per_attn + planned
         return sum(1 + int(f) + self.R * per_attn for f in self.cache.layer_int8)
 
     def _kernels_are_for_the_plan(self) -> None:

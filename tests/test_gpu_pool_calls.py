@@ -1,6 +1,8 @@
 """Calls of a DevicePool in other orders and on other streams: what they do is what
 the host would have done, or they are refused."""
 
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -229,3 +231,24 @@ def test_error_bits_of_plans_on_another_stream():
     assert pool.error_bits() == 0
     pool.pull()
     assert lengths(c) == [33, 30]
+
+
+@pytest.mark.parametrize("pdl", [False, True])
+def test_launches_of_a_planned_step(pdl):
+    c = make_cache(False)
+    begin(c, [20, 33], 71)
+    bufs, pool = StepBuffers(c, 2), DevicePool(c)
+    pool.use(bufs, [0, 1])
+    pkv.pkv_set_programmatic_launch(pdl)
+    try:
+        step = GraphStep(c, bufs, 0.1, pool=pool)
+        step.run_eager()
+        graph, n = torch.cuda.CUDAGraph(keep_graph=True), ctypes.c_size_t(0)
+        with torch.cuda.graph(graph):
+            step.run_eager()
+        assert ctypes.CDLL("libcuda.so.1").cuGraphGetNodes(ctypes.c_void_p(graph.raw_cuda_graph()), None, ctypes.byref(n)) == 0
+        assert step.launches_per_step() == n.value == c.L + 2 + pdl
+    finally:
+        pkv.pkv_set_programmatic_launch(False)
+    assert GraphStep(c, bufs, 0.1).launches_per_step() == c.L
+    pool.pull()
