@@ -572,7 +572,8 @@ int pkv_release_batch(const pkv_seq_pool* pool, const int32_t* slots, int32_t B,
  * negative numbers, with only one of h and w 0, of more than 2^31 - 1 tokens or
  * positions counts as empty (PKV_DEVERR_SEGMENT); a number of segments outside
  * [0, max_segments], too, leaves the sequence's rows as they were, and so does a
- * row outside [0, num_rows) (PKV_DEVERR_SLOT). err_word may be NULL. */
+ * row outside [0, num_rows) (PKV_DEVERR_SLOT). Segments behind the one that holds the
+ * sequence's last token of the batch may not be looked at. err_word may be NULL. */
 int pkv_axis_positions(const pkv_batch_desc* batch, const int32_t* segments, const int32_t* num_segments,
                        int32_t num_rows, int32_t max_segments, const int32_t* rows, int32_t* positions,
                        int64_t axis_stride, int32_t* err_word, void* stream);

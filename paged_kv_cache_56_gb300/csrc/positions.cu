@@ -78,12 +78,12 @@ __global__ void __launch_bounds__(kPosThreads) positions_kernel(const __grid_con
         long long tokens = 0, moves = 0;
         if (g.y == 0 && g.z == 0) {
             tokens = moves = max(g.x, 0);
-            if (g.x < 0 && blockIdx.x == 0) report(p.err, kErrSegment);
+            if (g.x < 0) report(p.err, kErrSegment);  // (any CTA: the first one ends with its own last token)
         } else {
             const long long area = (long long)g.y * g.z, frames = ((long long)g.x - 1) * g.w;
             const bool fine = g.x >= 0 && g.y > 0 && g.z > 0 && g.w >= 0 && area <= 0x7FFFFFFF &&
                               area * g.x <= 0x7FFFFFFF && frames <= 0x7FFFFFFF;
-            if (!fine && blockIdx.x == 0) report(p.err, kErrSegment);
+            if (!fine) report(p.err, kErrSegment);
             if (fine && g.x > 0) {
                 tokens = area * g.x;
                 moves = max(frames, (long long)max(g.y, g.z) - 1) + 1;
