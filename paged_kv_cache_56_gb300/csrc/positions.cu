@@ -77,8 +77,9 @@ __global__ void __launch_bounds__(kPosThreads) positions_kernel(const __grid_con
         if (s0 + tid < count) g = p.segments[size_t(r) * p.max_segments + s0 + tid];
         long long tokens = 0, moves = 0;
         if (g.y == 0 && g.z == 0) {
-            tokens = moves = max(g.x, 0);
-            if (g.x < 0) report(p.err, kErrSegment);  // (any CTA: the first one ends with its own last token)
+            const bool fine = g.x >= 0 && g.w >= 0;
+            tokens = moves = fine ? g.x : 0;
+            if (!fine) report(p.err, kErrSegment);  // (any CTA: the first one ends with its own last token)
         } else {
             const long long area = (long long)g.y * g.z, frames = ((long long)g.x - 1) * g.w;
             const bool fine = g.x >= 0 && g.y > 0 && g.z > 0 && g.w >= 0 && area <= 0x7FFFFFFF &&

@@ -32,3 +32,18 @@ def test_bad_segments_far_behind_the_first_tokens_are_reported(at, bad):
         want = positions_of(good, ctx)[:, ctx - new:]  # it counts as empty
         assert np.array_equal(out[:, :2 * new].cpu().numpy(), np.tile(want, 2))
         assert err.item() == pkv.PKV_DEVERR_SEGMENT
+
+
+@pytest.mark.parametrize("bad", [(4, 0, 0, -1), (1, 0, 0, -2 ** 31), (-3, 0, 0, -3)])
+def test_text_with_a_negative_step_counts_as_empty(bad):
+    """A segment with negative numbers is bad, whether the number would matter or not."""
+    segs, good = [(3, 0, 0, 1), bad, (1, 2, 2, 0), (2, 0, 0, 0)], [(3, 0, 0, 1), (1, 2, 2, 0), (2, 0, 0, 0)]
+    batch, table, count, out = make([segs, good], [11, 11], [11, 11])
+    err = dev([0])
+    pkv.pkv_axis_positions(batch, table, count, out, err=err)
+    assert np.array_equal(out[:, :22].cpu().numpy(), np.tile(positions_of(good, 11), 2))
+    assert err.item() == pkv.PKV_DEVERR_SEGMENT
+    batch, table, count, out = make([good], [11], [11])
+    err.zero_()
+    pkv.pkv_axis_positions(batch, table, count, out, err=err)
+    assert np.array_equal(out[:, :11].cpu().numpy(), positions_of(good, 11)) and err.item() == 0
