@@ -63,6 +63,7 @@ constexpr int kPrKeys = 128;  // tokens of a key tile
 constexpr float kPrShift = 40.f;
 constexpr float kPrAhead = 12.f;
 constexpr float kPrMost = 0x1p-20f;  // 2^20 in units of 2^-40
+constexpr float kPrLarge = 0x1p28f;  // references whose rounding an exponent must not see
 constexpr int kPrThreads = 384;
 constexpr int kPrLaunchRegs = 168;
 
@@ -210,6 +211,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
             const KeyTiles kt = im.kt;
             const int n = kt.n;
             float m_ref = have ? -INFINITY : INFINITY;  // reference of the exponent (base 2); no row: weights of 0
+            bool odd = true;  // some row of the warp has no reference yet, or one of 2^28 and more
             float2 l2 = make_float2(0.f, 0.f);
             const int hi = have ? row >> lgG : -1, lo = max(0, hi - p.window + 1);
             // the warp's first and last position, and where their windows begin
@@ -223,8 +225,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
                     const bool masked = jj < kt.nsink || t0 + kPrKeys - 1 > pf || t0 < wl;
                     float2 sum = make_float2(0.f, 0.f);
                     // `count` scores to weights, into `to`, and their sum.
-                    const auto weights = [&](const uint32_t* r, auto count, uint32_t* to, float neg) {
-                        const float2 a2 = make_float2(scale, scale), b2 = make_float2(neg, neg);
+                    const auto weights = [&](const uint32_t* r, auto count, uint32_t* to, float mul, float neg) {
+                        const float2 a2 = make_float2(mul, mul), b2 = make_float2(neg, neg);
                         float2 part = make_float2(0.f, 0.f);
 #pragma unroll
                         for (int e = 0; e < count.value; e += 4) {
@@ -270,6 +272,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
                         const bool up = mx > m_ref && (all || mx - m_ref > kPrAhead);
                         const float f = up ? fast_exp2(m_ref - mx) : 1.f;
                         if (up) m_ref = mx;
+                        odd = __any_sync(kFull, fabsf(m_ref) >= kPrLarge && m_ref < INFINITY);
                         l2.x *= f;
                         l2.y *= f;
                         if (jj > 0 && __any_sync(kFull, up)) {
@@ -284,14 +287,25 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
                         }
                     };
                     // Weights over scores that have been read, rolled up: for what is not the plain tile.
+                    // A score's exponent is score * scale - reference, in one rounding: up to half a step of
+                    // the reference above 0. From 2^28 on that is 16 and more, from 2^31 on the weight overflows.
+                    // There products are rounded as the reference was, and lie 32 or more apart or are the same.
+                    const auto large = [&]() { return __any_sync(kFull, fabsf(m_ref) >= kPrLarge && fabsf(m_ref) < INFINITY); };
                     const auto weigh_in_place = [&]() {
-                        const float neg = (m_ref == -INFINITY ? 0.f : -m_ref) - kPrShift;
+                        const float ref = m_ref == -INFINITY ? 0.f : m_ref;
+                        const bool rounded = large();
+                        const float mul = rounded ? 1.f : scale, neg = (rounded ? 0.f : -ref) - kPrShift;
                         sum = make_float2(0.f, 0.f);
 #pragma unroll 1
                         for (int c = 0; c < 128; c += 32) {
                             uint32_t r[32], x[16];
                             if (scores(r, c)) {
-                                weights(r, PromptCount<32>{}, x, neg);
+                                if (rounded) {
+#pragma unroll
+                                    for (int e = 0; e < 32; ++e)
+                                        r[e] = __float_as_uint(__fadd_rn(__fmul_rn(__uint_as_float(r[e]), scale), -ref));
+                                }
+                                weights(r, PromptCount<32>{}, x, mul, neg);
                             } else {
 #pragma unroll
                                 for (int e = 0; e < 16; ++e) x[e] = 0u;
@@ -299,9 +313,12 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
                             tmem_st(s_addr + uint32_t(c / 2), x);
                         }
                     };
-                    const bool unset = __any_sync(kFull, m_ref == -INFINITY);
-                    if (masked || unset) raise(false);
-                    if (masked) {
+                    bool slow = masked;
+                    if (masked || odd) {
+                        raise(false);
+                        slow |= large();
+                    }
+                    if (slow) {
                         weigh_in_place();
                     } else {
                         // 16 columns at a time, one chunk's load in flight while the other is worked on
@@ -312,10 +329,10 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
                         for (int c = 0; c < 128; c += 32) {
                             tmem_ld_wait(ra);
                             tmem_ld_start(rb, s_addr + uint32_t(c + 16));
-                            weights(ra, PromptCount<16>{}, w[c / 64] + c % 64 / 2, neg);
+                            weights(ra, PromptCount<16>{}, w[c / 64] + c % 64 / 2, scale, neg);
                             tmem_ld_wait(rb);
                             if (c < 96) tmem_ld_start(ra, s_addr + uint32_t(c + 32));
-                            weights(rb, PromptCount<16>{}, w[c / 64] + c % 64 / 2 + 8, neg);
+                            weights(rb, PromptCount<16>{}, w[c / 64] + c % 64 / 2 + 8, scale, neg);
                         }
                         if (__any_sync(kFull, sum.x + sum.y > kPrMost)) {
                             raise(true);
