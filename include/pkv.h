@@ -409,8 +409,9 @@ int pkv_rope_append(const pkv_cache_desc* c, const pkv_batch_desc* batch, const 
  * partly filled last block from the slot's tail). q, out: [num_tokens][Hq][d]
  * bf16 with token strides of q_stride, out_stride elements (multiples of 8; both
  * 16-byte aligned); out may be q itself with the same stride, otherwise they
- * must not overlap. sm_scale is finite and not negative, and scores are within
- * +-1e30.
+ * must not overlap. sm_scale is finite and not negative. Scores (times sm_scale)
+ * are within +-5e29 in a call of up to 16 rows a kv head (max_tokens x group), within
+ * +-3e8 in one of more: past that its weights overflow.
  *
  * Scores, exponentials and all sums are fp32. A weight meets V in 16 bits (two
  * bf16 parts; INT8: 11, one f16) in a call of up to 16 rows a kv head (max_tokens
