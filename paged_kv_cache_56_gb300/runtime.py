@@ -834,7 +834,8 @@ class AxisPositions:
         self.counts = torch.zeros(cache.max_slots, dtype=torch.int32, device=dev)
         self.positions = torch.zeros((3, max_tokens), dtype=torch.int32, device=dev)
         self.err = torch.zeros(1, dtype=torch.int32, device=dev)
-        torch.cuda.synchronize()  # zeroed, whichever stream sets the first sequence
+        if self.err.is_cuda:
+            torch.cuda.synchronize(self.err.device)  # zeroed, whichever stream sets the first sequence
 
     def set(self, req_id: int, segments, stream=None) -> None:
         """The sequence's segments; tokens behind them are text."""
