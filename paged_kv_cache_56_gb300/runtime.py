@@ -196,11 +196,12 @@ class PagedKVCache:
         self.seqs[child] = s
         if self.int8 and p.length % self.bs:
             dev = self.layers[0].k_pool.device
-            src = torch.tensor([p.slot], dtype=torch.int32, device=dev)
-            dst = torch.tensor([s.slot], dtype=torch.int32, device=dev)
-            for lc in self.layers:
-                if lc.int8:
-                    pkv.pkv_copy_slots(lc.desc, src, dst, stream)
+            with _on(stream):  # (the ids, too: their memory may be another's as soon as this returns)
+                src = torch.tensor([p.slot], dtype=torch.int32, device=dev)
+                dst = torch.tensor([s.slot], dtype=torch.int32, device=dev)
+                for lc in self.layers:
+                    if lc.int8:
+                        pkv.pkv_copy_slots(lc.desc, src, dst)
         return s
 
     def remove_sequence(self, req_id: int) -> None:
@@ -293,11 +294,12 @@ class PagedKVCache:
         if not plan.cow or all(self.layer_int8):
             return
         dev = self.layers[0].k_pool.device
-        src = torch.tensor([a for a, _ in plan.cow], dtype=torch.int32, device=dev)
-        dst = torch.tensor([b for _, b in plan.cow], dtype=torch.int32, device=dev)
-        for lc in self.layers:
-            if not lc.int8:
-                pkv.pkv_copy_blocks(lc.desc, src, dst, stream)
+        with _on(stream):  # (the ids, too: their memory may be another's as soon as this returns)
+            src = torch.tensor([a for a, _ in plan.cow], dtype=torch.int32, device=dev)
+            dst = torch.tensor([b for _, b in plan.cow], dtype=torch.int32, device=dev)
+            for lc in self.layers:
+                if not lc.int8:
+                    pkv.pkv_copy_blocks(lc.desc, src, dst)
 
     def commit_step(self, req_ids) -> None:
         self._lengths_are_here()
@@ -404,7 +406,13 @@ def prefill(cache: PagedKVCache, layer: int, req_ids, k_rows, v_rows, starts=Non
     sequence req_ids[i] at positions starts[i] .. starts[i]+n_i-1 (starts must
     be multiples of block_size; the sequence must already hold the blocks).
     BF16 cache: one append of all rows. INT8 cache: whole blocks are quantized
-    straight from the rows; the trailing partial block goes to the tail."""
+    straight from the rows; the trailing partial block goes to the tail. What is
+    made of the rows on the way is made on `stream`, too."""
+    with _on(stream):
+        _prefill(cache, layer, req_ids, k_rows, v_rows, starts)
+
+
+def _prefill(cache: PagedKVCache, layer: int, req_ids, k_rows, v_rows, starts) -> None:
     lc = cache.layers[layer]
     bs = cache.bs
     dev = lc.k_pool.device
@@ -420,7 +428,7 @@ def prefill(cache: PagedKVCache, layer: int, req_ids, k_rows, v_rows, starts=Non
             return
         pkv.pkv_append_kv(lc.desc, torch.cat(list(k_rows)).contiguous(), torch.cat(list(v_rows)).contiguous(),
                           torch.from_numpy(np.concatenate(blk)).to(dev), torch.from_numpy(np.concatenate(off)).to(dev),
-                          None, stream)
+                          None)
         return
     fk, fv, fb, tk, tv, ts, to = [], [], [], [], [], [], []
     for r, t, s0, k, v in zip(req_ids, tabs, starts, k_rows, v_rows):
@@ -439,11 +447,11 @@ def prefill(cache: PagedKVCache, layer: int, req_ids, k_rows, v_rows, starts=Non
             to.extend(range(n % bs))
     if fb:
         pkv.pkv_quantize_blocks_from(lc.desc, torch.cat(fk).contiguous(), torch.cat(fv).contiguous(),
-                                     torch.tensor(fb, dtype=torch.int32, device=dev), stream)
+                                     torch.tensor(fb, dtype=torch.int32, device=dev))
     if ts:
         pkv.pkv_append_kv(lc.desc, torch.cat(tk).contiguous(), torch.cat(tv).contiguous(), None,
                           torch.tensor(to, dtype=torch.int32, device=dev),
-                          torch.tensor(ts, dtype=torch.int32, device=dev), stream)
+                          torch.tensor(ts, dtype=torch.int32, device=dev))
 
 
 # ---------------------------------------------------------------------------
