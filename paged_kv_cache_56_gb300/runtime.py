@@ -1043,12 +1043,7 @@ class DevicePool:
         a plan, captured or not, would give it blocks and tokens, and the next sequence that gets
         the slot would begin with them."""
         for bufs in self._used:
-            bufs.copied.synchronize()  # do not overwrite pinned data a pending copy still reads
-            a = bufs.h_slot.numpy()
-            if (a == slot).any():
-                a[a == slot] = -1
-                bufs.slot.copy_(bufs.h_slot, non_blocking=True)
-                bufs.copied.record()
+            bufs.slot.masked_fill_(bufs.slot == slot, -1)
 
     def plan(self, bufs, counts=None, stream=None) -> None:
         """Plans counts[b] new tokens (a device int32 tensor; None: one each) of the

@@ -100,7 +100,7 @@ def test_buffers_that_are_gone_are_forgotten():
     del b
     c.remove_sequence(1)
     assert a.slot.tolist() == [c.seqs[0].slot, -1]
-    pool.use(a, [None, 0])  # a sequence that was not there is not looked for
+    pool.use(a, [None, 0])
     c.remove_sequence(0)
     assert a.slot.tolist() == [-1, -1]
     pool.plan(a)
@@ -252,3 +252,19 @@ def test_launches_of_a_planned_step(pdl):
         pkv.pkv_set_programmatic_launch(False)
     assert GraphStep(c, bufs, 0.1).launches_per_step() == c.L
     pool.pull()
+
+
+def test_what_the_gpu_has_put_into_the_slots_stays():
+    """A program that stops sequences on the GPU, by an entry of -1, removes another one: its own entries stay."""
+    c = make_cache(False)
+    begin(c, [20, 33, 47], 71)
+    bufs, pool = StepBuffers(c, 3), DevicePool(c)
+    pool.use(bufs, [0, 1, 2])
+    bufs.slot[1] = -1
+    c.remove_sequence(0)
+    assert bufs.slot.tolist() == [-1, -1, c.seqs[2].slot]
+    pool.plan(bufs)
+    pool.commit(bufs)
+    assert pool.error_bits() == 0
+    pool.pull()
+    assert lengths(c) == [33, 48]
