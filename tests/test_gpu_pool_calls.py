@@ -9,9 +9,10 @@ import torch
 
 from libpkv import ensure_built
 from paged_kv_cache_56_gb300 import pkv
-from paged_kv_cache_56_gb300.runtime import AxisPositions, ChunkBuffers, DevicePool, GraphStep, StepBuffers, decode_step, read_back, run_layers
+from paged_kv_cache_56_gb300.runtime import (AxisPositions, ChunkBuffers, DevicePool, GraphStep, StepBuffers, axis_pairs,
+                                             decode_step, read_back, rope_frequencies, run_chunk, run_layers)
 from test_gpu_axes import positions_of
-from test_gpu_planned import HEADS, begin, make_cache, rows
+from test_gpu_planned import HEADS, begin, caches_are_the_same, make_cache, rows
 
 pytestmark = pytest.mark.gpu
 
@@ -268,3 +269,56 @@ def test_what_the_gpu_has_put_into_the_slots_stays():
     assert pool.error_bits() == 0
     pool.pull()
     assert lengths(c) == [33, 48]
+
+
+@pytest.mark.parametrize("int8", [False, True])
+def test_steps_over_several_axes_captured_with_their_plan(int8):
+    """Plan, positions, turn, append, attention and commit of one token a sequence in one graph: what the same calls do one
+    by one, sequences that end and begin among the replays."""
+    a, b = make_cache(int8), make_cache(int8)
+    f, factor = rope_frequencies(HEADS[2])
+    runs = []
+    for c in (a, b):
+        begin(c, [20, 33, 47], 71)
+        chunks, where = ChunkBuffers(c, 4, 4, 1), AxisPositions(c, 4, 4)
+        where.set(0, [(5, 0, 0, 1), (1, 4, 4, 1)])
+        for r in (1, 2):
+            where.set(r, [(2, 2, 3, 2)])
+        rope = pkv.make_rope_axes(torch.as_tensor(f).cuda(), axis_pairs((16, 24, 24)), positions=where.positions, scale=factor)
+        q, k, v = (torch.zeros((2, 4, h, HEADS[2]), dtype=torch.bfloat16, device="cuda") for h in (HEADS[0], HEADS[1], HEADS[1]))
+        out, pool = torch.zeros_like(q), DevicePool(c)
+
+        def step(c=c, chunks=chunks, where=where, rope=rope, q=q, k=k, v=v, out=out, pool=pool):
+            pool.plan(chunks)
+            where.update(chunks)
+            run_chunk(c, chunks, q, k, v, out, HEADS[2] ** -0.5, rope)
+            pool.commit(chunks)
+        runs.append((c, chunks, where, q, k, v, out, pool, step))
+    graph = None
+    for n in range(24):
+        for which, (c, chunks, where, q, k, v, out, pool, step) in enumerate(runs):
+            if n == 0:
+                pool.use(chunks, [2, 0, None, 1])
+            if n == 9:
+                c.remove_sequence(0)  # (its entry is one without a sequence until the next use)
+            if n == 13:
+                c.add_sequence(8)
+                where.set(8, [(3, 0, 0, 1), (1, 2, 2, 1)])
+                pool.use(chunks, [8, None, 2, 1])
+            for i, x in enumerate((q, k, v)):
+                x.copy_(rows(500 + 3 * n + i, 2, 4, x.shape[2]))
+            if which == 0 or n == 0:
+                step()
+            else:
+                if graph is None:
+                    graph = torch.cuda.CUDAGraph()
+                    with torch.cuda.graph(graph):
+                        step()
+                graph.replay()
+        live = int(runs[0][1].starts[-1].item())
+        assert live == (2 if 9 <= n < 13 else 3) and torch.equal(runs[0][6][:, :live], runs[1][6][:, :live])
+    for c, _, where, *_, pool, _ in runs:
+        assert pool.error_bits() == 0 and where.err.item() == 0 and all(lc.error_bits() == 0 for lc in c.layers)
+        pool.pull()
+    caches_are_the_same(a, b)
+    assert lengths(b) == [57, 71, 11]
