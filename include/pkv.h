@@ -541,7 +541,8 @@ int pkv_plan_batch(const pkv_seq_pool* pool, const int32_t* slots, const int32_t
  * an INT8 context that would end in another block than the chunk without ending at
  * a block's end (its rows are gone: see pkv_rope_append), leaves the length as it
  * was (PKV_DEVERR_CTX_LEN); so does a length that is not ctx_lens[b] - n_b: a
- * plan is committed once. A slot twice among entries with tokens is not found. */
+ * plan is committed once. An entry with new tokens whose slot is out of range, or has become
+ * -1 since the plan, keeps nothing (PKV_DEVERR_SLOT). A slot twice among entries with tokens is not found. */
 int pkv_commit_batch(const pkv_seq_pool* pool, const int32_t* slots, const int32_t* accepted, int32_t B,
                      const pkv_plan* plan, void* stream);
 
@@ -562,7 +563,9 @@ int pkv_release_batch(const pkv_seq_pool* pool, const int32_t* slots, int32_t B,
  *   else     : a grid of t frames of h rows of w tokens, token (i, j, k) at
  *              (base + i * step, base + j, base + k), `step` positions a frame;
  * the first base is 0, the next one 1 + the largest position of the segment on
- * any axis. Tokens behind the last segment are text. segments
+ * any axis. Tokens behind the last segment are text. Steps are whole numbers: frames that lie
+ * otherwise (at a rate that is no multiple of the trained one) have positions that a
+ * caller works out, for pkv_rope_axes takes any. segments
  * [num_rows][max_segments][4] and num_segments [num_rows] (device int32, 16- and
  * 4-byte aligned) are looked up at row rows[b] (device [B]; NULL: row b -- pass the
  * batch's slots to keep a list for each slot). positions: device int32, axis a at
@@ -570,8 +573,8 @@ int pkv_release_batch(const pkv_seq_pool* pool, const int32_t* slots, int32_t B,
  * written, others left. Positions stop at 2^31 - 1.
  *
  * Of the batch, token_starts, ctx_lens (below 2^31 - 2^16) and the bounds are used. A segment with
- * negative numbers, with only one of h and w 0, of more than 2^31 - 1 tokens or
- * positions counts as empty (PKV_DEVERR_SEGMENT); a number of segments outside
+ * negative numbers, with only one of h and w 0, of more than 2^31 - 1 tokens, or whose last
+ * frame lies more than 2^31 - 1 behind its first counts as empty (PKV_DEVERR_SEGMENT); a number of segments outside
  * [0, max_segments], too, leaves the sequence's rows as they were, and so does a
  * row outside [0, num_rows) (PKV_DEVERR_SLOT). Segments behind the one that holds the
  * sequence's last token of the batch may not be looked at. err_word may be NULL. */
@@ -617,7 +620,8 @@ int pkv_rope_append_axes(const pkv_cache_desc* c, const pkv_batch_desc* batch, c
  *
  * Of the descriptors, the heads, head_dim and err_word, token_starts, ctx_lens
  * and the bounds are used. ctx_lens[b] == n_b says that the sequence has no
- * earlier tokens: the rows of one that has are zero (PKV_DEVERR_CTX_LEN).
+ * earlier tokens: the rows of one that has are zero (PKV_DEVERR_CTX_LEN). The last
+ * sequence is begun first: prompts packed by ascending length end soonest.
  * Precision is that of pkv_window_attention with more than 16 rows. The K and V
  * of a sequence's rows must be finite; those of other sequences, and rows behind the
  * batch, may hold anything. */

@@ -13,11 +13,18 @@
 // the ring's front) are changed by the CTA that is last to arrive. A thread's first
 // word of a list is read before the sums are there (its place depends on the slot alone).
 //
-// Bound by latency: launch, slots -> lengths -> sums (two barriers) -> lists. In a
-// graph 5.3 us for 4 entries, 5.4 us for 144 entries with tables of 1024 blocks (0.7
-// MB), 6.4 to 7.0 us for 512 entries that bring 1 to 200 tokens each (2.9 MB; 0.4 us at the
-// memory's rate). Called one by one from Python 9 to 12 us: the call. Entries are
-// taken 512 at a time, twice when there are more: 1024 take 7.7 us, 4096 18 us, 8192 38 us.
+// Bound by latency: launch, slots -> lengths -> sums (two barriers) -> lists, and where
+// blocks are taken ring -> lists, a fence, the arrivals and the last CTA's pass. In a graph, us:
+//                                                        all held   blocks taken
+//   4 entries                                               5.1          -
+//   144 entries, 128 single tokens, tables of 1024          5.4      7.5 (9 blocks)
+//   512 entries of 1 to 200 tokens, the same (2.9 MB)       6.6      9.1 (1271)
+//   1024 single tokens, the same                           10.8     13.6 (68)
+//   4096 single tokens, tables of 64                       18.7     24.7 (262)
+// (0.4 us of the third are bytes at the memory's rate.) Commit 1.9 to 2.3; release of 144
+// entries with 17975 blocks 6.4, of 512 with 119586 8.0. Steps that go on, plan and commit of 128
+// sequences, 8 of which need a block: 10.4 for both. Called one by one from Python 10 to 16 us: the
+// call. Entries are taken 512 at a time, by every CTA, and twice when there are more than 512.
 #include <algorithm>
 
 #include "batch.cuh"

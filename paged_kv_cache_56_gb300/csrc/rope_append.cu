@@ -31,7 +31,10 @@
 // that the host has made: no table, no branch. The turned k leaves as rows from the
 // registers that the cache's rows are written from. 30718 tokens of 16 query heads, bf16,
 // k rows too: 567 MB in 88 us, 6.4 TB/s; 12535 tokens of 32 query heads, INT8: 308 MB in
-// 58 us, 5.3 TB/s; 128 single tokens, INT8, 8.7 us.
+// 58 us, 5.3 TB/s; 128 single tokens, INT8, 8.7 us. INT8 blocks of 64 take longer: 12.7 us for the
+// single tokens, 68 us for the 12535 tokens, 153 us for 30718 of 32 query heads (134 with blocks
+// of 16, bf16 126). By reading, four CTAs meet for every head's maximum, and registers are
+// spilled; what each of the two costs has not been measured.
 //
 // Layout: with a token a thread the angles are worked out once and stay in
 // registers (shared-memory tables: 131 us for the bf16 case), consecutive lanes
