@@ -805,7 +805,7 @@ class ChunkBuffers:
             split = pkv.pkv_window_split_tokens(desc, self.batch, window, sinks)
             n = pkv.pkv_window_ws_bytes(desc, self.batch, window, sinks, split)
             self._ws[key] = (split, torch.zeros(n, dtype=torch.uint8, device=self.cache.device) if n else None)
-            torch.cuda.synchronize()  # zeroed, whichever stream uses it
+            torch.cuda.synchronize(self.starts.device)  # zeroed, whichever stream uses it
         return self._ws[key]
 
 
@@ -988,7 +988,7 @@ class DevicePool:
         self.state, self.err = up([0, len(free), 0, 0]), up([0])
         self.desc = pkv.make_seq_pool(self.tables, self.lens, self.held, self.ring, self.state, block_size=cache.bs,
                                       int8=cache.int8, err=self.err)
-        torch.cuda.synchronize()  # there, whichever stream plans first
+        torch.cuda.synchronize(self.tables.device)  # there, whichever stream plans first
         cache.pool = self
 
     def _alive(self) -> None:
@@ -1007,7 +1007,7 @@ class DevicePool:
             bufs.gpu_plans = {}
             bufs.gpu_starts = (torch.zeros(bufs.max_batch + 1, dtype=torch.int32, device=self.cache.device)
                                if isinstance(bufs, StepBuffers) else bufs.starts)
-            torch.cuda.synchronize()  # zeroed, whichever stream plans into it
+            torch.cuda.synchronize(bufs.gpu_starts.device)  # zeroed, whichever stream plans into it
         if B not in bufs.gpu_plans:
             rows, new = (B, 1) if isinstance(bufs, StepBuffers) else (bufs.max_tokens, bufs.max_new)
             bufs.gpu_plans[B] = pkv.make_plan(bufs.gpu_starts[:B + 1], bufs.tab[:B], bufs.ctx[:B], num_tokens=rows,
@@ -1083,7 +1083,7 @@ class DevicePool:
         """Brings lists, lengths and the free list back to the host (waits for the GPU); the pool is done with."""
         self._alive()
         c = self.cache
-        torch.cuda.synchronize()
+        torch.cuda.synchronize(self.tables.device)
         tables, lens, held, ring = (t.cpu().numpy() for t in (self.tables, self.lens, self.held, self.ring))
         head, free = self.state[:2].tolist()
         N = ring.size

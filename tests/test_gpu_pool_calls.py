@@ -322,3 +322,23 @@ def test_steps_over_several_axes_captured_with_their_plan(int8):
         pool.pull()
     caches_are_the_same(a, b)
     assert lengths(b) == [57, 71, 11]
+
+
+def test_waits_are_for_the_device_that_holds_the_pool(monkeypatch):
+    """Not for the one that is current: with several GPUs that may be another."""
+    waited, wait = [], torch.cuda.synchronize
+    monkeypatch.setattr(torch.cuda, "synchronize", lambda device=None: (waited.append(device), wait(device)))
+    c = make_cache(False)
+    begin(c, [20], 71)
+    here = c.layers[0].k_pool.device
+    chunks, bufs = ChunkBuffers(c, 1, 20, 20), StepBuffers(c, 1)
+    waited.clear()
+    chunks.workspace(c.layers[0].desc, 0, 0)
+    AxisPositions(c, 4, 4)
+    pool = DevicePool(c)
+    pool.use(bufs, [0])
+    pool.plan(bufs)
+    pool.commit(bufs)
+    assert pool.error_bits() == 0
+    pool.pull()
+    assert waited == [here] * 6 and lengths(c) == [21]
