@@ -39,13 +39,15 @@
 // 1897 and 1699); one of 16384 tokens, 32 and 8 heads, 2.2 TF in 1250 us, 1760 TF/s;
 // of 5000 to 8192 tokens, window 1024, 211 GF in 181 us; 32 of 16 to 4096 tokens,
 // 422 GF in 303 us (with inputs that are not in L2 644, 189 and 325 us); d = 64, two of
-// 8000, 16 and 8 heads, 250 to 253 us, 1040 TF/s, of 5000 to 8192 with 32 and 8, window 1024,
-// 146 us, 720. One prompt by itself, d = 128, 16 / 32 query heads over 8, us in a graph: 128 tokens
-// 10.8 / 10.9, 512 14.9 / 15.4, 1024 20.4 / 20.6, 2048 30.7 / 40.1, 4096 68 / 92 (floors 0.2 / 0.4, 0.9 /
-// 1.5, 2.3 / 4.5, 9.1 / 18, 36 / 73): no item is spread over several CTAs, so the longest item's chain
-// is the time while there are fewer items than SMs (2048 tokens: 128, of up to 16 key tiles, where
-// an even share is 7). 16 prompts of 1 to 512 tokens, 32 heads, 28.8 us (floor 6.8). A key tile of both row tiles takes 2650
-// cycles, its multiplies 2048 by themselves and 2440 beside the softmax (they read 192
+// 8000, 16 and 8 heads, 250 to 253 us, 1040 TF/s, of 5000 to 8192 with 32 and 8, window
+// 1024, 146 us, 720. One prompt by itself, d = 128, 16 / 32 query heads over 8, us in a graph:
+//   tokens        128          512        1024        2048      4096
+//   us        10.8/10.9    14.9/15.4   20.4/20.6   30.7/40.1   68/92
+//   floor      0.2/0.4      0.9/1.5     2.3/4.5     9.1/18     36/73
+// No item is spread over several CTAs, so the longest item's chain is the time while there are
+// fewer items than SMs (2048 tokens: 128, of up to 16 key tiles, where an even share is 7). 16
+// prompts of 1 to 512 tokens, 32 heads, 28.8 us (floor 6.8). A key tile of both row tiles takes
+// 2650 cycles, its multiplies 2048 by themselves and 2440 beside the softmax (they read 192
 // KB of shared memory, at 128 bytes a cycle at most). A tile's chain is 930 cycles of
 // softmax (a warp's 128 exponentials a thread take 512 of them), 190 until the weights
 // are announced, 200 until they are seen, 1220 of multiplies. An item's beginning and

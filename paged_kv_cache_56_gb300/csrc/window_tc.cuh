@@ -7,7 +7,7 @@
 // tokens, gathered block by block through the block table. There is one CTA a
 // SM; it walks from item to item, taking the grid's next one from the hardware
 // (launch cancellation) while it works, so that an item's first loads and
-// scores overlap the end of the item before. Long items are first in the grid.
+// scores overlap the end of the item before. The last sequence is first in the grid, its longest items first.
 //
 //   warps 0-3, 4-7: softmax of row tile 0 and 1, one row a thread -- no shuffle
 //                   anywhere; scores from tensor memory, weights back to it
